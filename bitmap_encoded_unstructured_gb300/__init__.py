@@ -8,7 +8,8 @@ memory and streams.
 Two layers:
 
 * ``bsp_*`` functions with the C names, taking raw pointers / ints;
-* ``BitmapMatrix``, a handle owner with tensor-level methods.
+* ``BitmapMatrix``, ``UnionMatrix`` (weights) and ``KvCache`` (the paged
+  8-bit KV cache and its attention), handle owners with tensor-level methods.
 
 The library is loaded on first use; if it is missing or fails to load, the
 call raises ``RuntimeError`` (there is no fallback of any kind).
@@ -30,7 +31,9 @@ TEST_LIB_PATH = os.path.join(_HERE, "libbsp_test.so")
 
 BSP_FP16 = 0
 BSP_INT8 = 1
+BSP_BF16 = 2
 BSP_DECODE_MAX_N = 16
+BSP_KV_MAX_BATCH = 16384
 
 STATUS = {
     0: "BSP_OK", 1: "BSP_ERR_INVALID_ARG", 2: "BSP_ERR_SHAPE", 3: "BSP_ERR_DTYPE",
@@ -76,6 +79,15 @@ SIGNATURES = {
     "bsp_union_encode_reordered": (C.c_int, [_P, C.c_int, _I64, _I64, _P, C.POINTER(_P)]),
     "bsp_union_export_perms": (C.c_int, [_P, _P, _P]),
     "bsp_reorder_rows": (C.c_int, [_P, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, _P, C.POINTER(_I64)]),
+    "bsp_kv_create": (C.c_int, [_P, _P, C.POINTER(_P)]),
+    "bsp_kv_destroy": (C.c_int, [_P]),
+    "bsp_kv_check": (C.c_int, [_P, _P]),
+    "bsp_kv_plan": (C.c_int, [_P, _P, _P, C.c_int32, _P, C.c_int32, _I64, _P, C.c_int32, _P, _I64, _P, _P, _P, _P,
+                              _P, _P, _P]),
+    "bsp_kv_append": (C.c_int, [_P, _P, _P, _P, C.c_int, _I64, _I64, _I64, _I64, _I64, _P]),
+    "bsp_kv_read": (C.c_int, [_P, _P, _I64, _P, _P, C.c_int, _P]),
+    "bsp_kv_attention": (C.c_int, [_P, _P, _P, C.c_int, _I64, C.c_int32, _I64, _I64, C.c_float, C.c_int32, _P, _I64,
+                                   _I64, _P, _P]),
 }
 
 # Entry points of the test build only (include/bsp_testing.h).
@@ -102,6 +114,19 @@ class bsp_union_info_t(C.Structure):
                 ("NLT", C.c_int64), ("nnz", C.c_uint64), ("total_values", C.c_uint64),
                 ("value_bytes", C.c_uint64), ("masks", C.c_void_p), ("offsets", C.c_void_p),
                 ("values", C.c_void_p), ("reordered", C.c_int32)]
+
+
+class bsp_kv_desc_t(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("pages", C.c_int64), ("heads", C.c_int32), ("page", C.c_int32), ("dim", C.c_int32),
+                ("page_stride", C.c_int64), ("head_stride", C.c_int64), ("row_stride", C.c_int64),
+                ("scale_stride", C.c_int64)]
+
+
+class bsp_kv_step_t(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("width", C.c_int32), ("table_stride", C.c_int64),
+                ("block_table", C.c_void_p), ("seq_len", C.c_void_p), ("q_start", C.c_void_p),
+                ("max_new", C.c_int64)]
 
 
 class BspError(RuntimeError):
@@ -604,3 +629,210 @@ class UnionMatrix:
         Y = out if out is not None else torch.empty((N, self.M), dtype=torch.int32, device=self.device)
         bsp_union_spmm(self.h, X.data_ptr(), N, Y.data_ptr(), _stream(stream))
         return Y
+
+
+def _row_dtype(dtype):
+    import torch
+    if dtype is torch.float16:
+        return BSP_FP16
+    if dtype is torch.bfloat16:
+        return BSP_BF16
+    raise TypeError("rows must be float16 or bfloat16")
+
+
+def _int32(name, t, shape, device):
+    import torch
+    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+class KvStep:
+    """One step's ragged rows over a block table: request b has new rows
+    ``q_start[b]`` to ``q_start[b + 1]`` and ``seq_len[b]`` rows with them.
+    ``KvCache.plan`` makes one from request lengths; ``KvStep(block_table,
+    seq_len, q_start, max_new)`` takes existing int32 CUDA tensors.
+    ``max_new`` bounds a request's new rows (0: not known)."""
+
+    def __init__(self, block_table, seq_len, q_start, max_new: int = 0):
+        self.granted = self.slots = self.positions = self.free_count = None
+        self.seq_len, self.q_start = seq_len, q_start
+        self._bind(block_table, max_new)
+
+    @classmethod
+    def empty(cls, batch: int, tokens: int, device=None, free_count=None):
+        """Buffers for ``KvCache.plan(..., out=step)``: a server keeps one step
+        and plans into it again and again.  ``free_count``: the tensor that
+        receives the new count; the one that the plan reads updates it in
+        place."""
+        import torch
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        s = cls.__new__(cls)
+        i32 = dict(dtype=torch.int32, device=dev)
+        s.block_table = None
+        s.seq_len, s.granted = torch.empty(batch, **i32), torch.empty(batch, **i32)
+        s.q_start = torch.empty(batch + 1, **i32)
+        s.slots = torch.empty(tokens, dtype=torch.int64, device=dev)
+        s.positions = torch.empty(tokens, **i32)
+        s.free_count = torch.empty(1, **i32) if free_count is None else free_count
+        _int32("free_count", s.free_count, (1,), dev)
+        s._out = tuple(t.data_ptr() for t in (s.seq_len, s.q_start, s.granted, s.slots, s.positions, s.free_count))
+        return s
+
+    def _bind(self, block_table, max_new):
+        import torch
+        t = block_table
+        if t.dtype is not torch.int32 or not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+            raise ValueError("block_table must be an int32 CUDA tensor [batch][width], rows contiguous")
+        batch, width = t.shape
+        self.device = t.device
+        self.block_table = t
+        stride = t.stride(0) if batch > 1 else width
+        self._c = bsp_kv_step_t(batch, width, stride, t.data_ptr(),
+                                _int32("seq_len", self.seq_len, (batch,), t.device),
+                                _int32("q_start", self.q_start, (batch + 1,), t.device), int(max_new))
+        self._ref = C.addressof(self._c)
+
+
+class KvCache:
+    """The paged 8-bit KV cache over tensors the caller owns: ``k``, ``v``
+    int8 [pages][heads][page][dim] (any strides with dim contiguous, the same
+    for both), ``k_scale``, ``v_scale`` float32 [pages][heads].  A cached value
+    is code * scale of its page and head.
+
+    ``plan`` grants pages and lays out a step from request lengths, ``append``
+    stores its new rows, ``attention`` attends over them and what was cached
+    before, ``read`` returns rows by slot.  All are asynchronous on the
+    stream and can be captured in a CUDA graph."""
+
+    def __init__(self, k, v, k_scale, v_scale, stream=None):
+        import torch
+        for name, t in (("k", k), ("v", v)):
+            if t.dtype is not torch.int8 or not t.is_cuda or t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+                raise TypeError(f"{name} must be an int8 CUDA tensor [pages][heads][page][dim], dim contiguous")
+        if k.shape != v.shape or k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v must have the same shape, strides and device")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if (t.dtype is not torch.float32 or t.device != k.device or t.shape != k.shape[:2]
+                    or (t.shape[1] > 1 and t.stride(1) != 1)):
+                raise ValueError(f"{name} must be a float32 tensor [pages][heads] beside k, heads contiguous")
+        if k_scale.stride() != v_scale.stride():
+            raise ValueError("k_scale and v_scale must have the same strides")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page, self.dim = k.shape
+        self.device = k.device
+        d = bsp_kv_desc_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages, self.heads,
+                          self.page, self.dim, k.stride(0), k.stride(1), k.stride(2), k_scale.stride(0))
+        h = C.c_void_p()
+        with torch.cuda.device(self.device):
+            _check("bsp_kv_create", lib().bsp_kv_create(C.addressof(d), _stream(stream), C.byref(h)))
+        self.h = h.value
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, page: int = 64, device=None):
+        """A cache on new tensors, zeroed."""
+        import torch
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        kv = [torch.zeros((pages, heads, page, dim), dtype=torch.int8, device=dev) for _ in range(2)]
+        sc = [torch.zeros((pages, heads), dtype=torch.float32, device=dev) for _ in range(2)]
+        return cls(*kv, *sc)
+
+    def close(self):
+        if getattr(self, "h", None):
+            _check("bsp_kv_destroy", lib().bsp_kv_destroy(self.h))
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def check(self, stream=None):
+        """Synchronise and raise if a kernel on this handle gave up a wait."""
+        _check("bsp_kv_check", lib().bsp_kv_check(self.h, _stream(stream)))
+
+    def plan(self, ctx_len, new_len, block_table, free_list, free_count, tokens: int, out=None, max_new: int = 0,
+             stream=None):
+        """A ``KvStep`` from request lengths (int32 CUDA tensors): ``ctx_len``
+        rows cached, ``new_len`` rows asked for (negative: the request has
+        ended and gives its pages back).  Granted pages come off ``free_list``
+        (``free_count`` entries live) into ``block_table``, first come, first
+        served; ``tokens`` is the row capacity of the step.  The step also
+        carries ``granted``, ``slots``, ``positions`` and the new
+        ``free_count``."""
+        batch, width = block_table.shape
+        dev = block_table.device
+        step = KvStep.empty(batch, tokens, dev) if out is None else out
+        if step.block_table is not block_table:
+            step._bind(block_table, max_new)
+        step._c.max_new = int(max_new)
+        if step.slots is None or step.slots.shape[0] != tokens or step._c.batch != batch:
+            raise ValueError("out does not have this batch and these tokens (KvStep.empty)")
+        seq_len, q_start, granted, slots, positions, count = step._out
+        _check("bsp_kv_plan", lib().bsp_kv_plan(
+            self.h, _int32("ctx_len", ctx_len, (batch,), dev), _int32("new_len", new_len, (batch,), dev), batch,
+            step._c.block_table, width, step._c.table_stride,
+            _int32("free_list", free_list, free_list.shape[:1], dev), free_list.shape[0],
+            _int32("free_count", free_count, (1,), dev), tokens, seq_len, q_start, granted, slots, positions, count,
+            _stream(stream)))
+        return step
+
+    def _rows(self, name, x, heads=None):
+        """(pointer, row stride, head stride) of rows [n][heads][dim]."""
+        shape = x.shape
+        if (x.device != self.device or len(shape) != 3 or shape[2] != self.dim or (heads and shape[1] != heads)
+                or (shape[2] > 1 and x.stride(2) != 1)):
+            raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, dim contiguous")
+        return x.data_ptr(), x.stride(0), x.stride(1)
+
+    def append(self, step, k, v, stream=None):
+        """Quantise new rows ``k``, ``v`` [rows][heads][dim] (float16 or
+        bfloat16, views of a QKV output allowed) into the step's pages."""
+        dt = _row_dtype(k.dtype)
+        if v.dtype is not k.dtype or v.shape != k.shape:
+            raise ValueError("k and v must have the same shape and type")
+        pk, kr, kh = self._rows("k", k, self.heads)
+        pv, vr, vh = self._rows("v", v, self.heads)
+        _check("bsp_kv_append", lib().bsp_kv_append(self.h, step._ref, pk, pv, dt, k.shape[0], kr, kh, vr, vh,
+                                                    _stream(stream)))
+
+    def read(self, slots, dtype=None, out=None, stream=None):
+        """Cached rows of int64 ``slots``: (k, v) [n][heads][dim]; zeros for a
+        slot outside the cache."""
+        import torch
+        if slots.dtype is not torch.int64 or slots.device != self.device or slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError(f"slots must be a contiguous int64 vector on {self.device}")
+        n = slots.shape[0]
+        dtype = torch.float16 if dtype is None else dtype
+        dt = _row_dtype(dtype)
+        if out is None:
+            out = torch.empty((2, n, self.heads, self.dim), dtype=dtype, device=self.device).unbind(0)
+        k, v = out
+        for t in (k, v):
+            if t.dtype is not dtype or t.shape != (n, self.heads, self.dim) or not t.is_contiguous():
+                raise ValueError("out must be two contiguous tensors [n][heads][dim] of the type")
+        _check("bsp_kv_read", lib().bsp_kv_read(self.h, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt,
+                                                _stream(stream)))
+        return k, v
+
+    def attention(self, step, q, scale=None, window: int = 0, out=None, with_lse: bool = False, stream=None):
+        """Attention of the step's new rows ``q`` [rows][heads][dim] over what
+        their requests have cached (their own rows included, causal; the last
+        ``window`` rows only if it is positive).  ``scale`` defaults to
+        dim ** -0.5.  Returns out, or (out, lse) with float32 lse
+        [rows][heads]."""
+        import torch
+        dt = _row_dtype(q.dtype)
+        pq, qr, qh = self._rows("q", q)
+        rows, heads = q.shape[0], q.shape[1]
+        if out is None:
+            out = torch.empty((rows, heads, self.dim), dtype=q.dtype, device=self.device)
+        elif out.dtype is not q.dtype or out.shape != q.shape:
+            raise ValueError("out must have q's shape and type")
+        po, orow, oh = self._rows("out", out)
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=self.device) if with_lse else None
+        _check("bsp_kv_attention", lib().bsp_kv_attention(
+            self.h, step._ref, pq, dt, rows, heads, qr, qh, self.dim ** -0.5 if scale is None else scale, window, po,
+            orow, oh, lse.data_ptr() if with_lse else None, _stream(stream)))
+        return (out, lse) if with_lse else out

@@ -71,7 +71,8 @@ typedef enum {
 
 typedef enum {
     BSP_FP16 = 0, /* IEEE binary16 values, fp32 accumulation, fp16 output */
-    BSP_INT8 = 1  /* int8 values, int32 accumulation (exact)             */
+    BSP_INT8 = 1, /* int8 values, int32 accumulation (exact)             */
+    BSP_BF16 = 2  /* bfloat16: rows and queries of the KV cache only     */
 } bsp_dtype_t;
 
 /* Largest N of the decode path (the skinny product, N <= 16): split-K
@@ -545,6 +546,144 @@ bsp_status_t bsp_union_decode(bsp_union_t h, int8_t *W_out, bsp_stream_t stream)
 
 /* Synchronise stream and report (then clear) a device-side wait that gave up. */
 bsp_status_t bsp_union_check(bsp_union_t h, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 8-bit KV cache, and the attention that reads it: what a decoder
+ * layer computes between its QKV and output projections.
+ *
+ * The caller owns the cache (from its own allocator) and describes it once:
+ *   k, v               int8 codes [pages][heads][page][dim], dim contiguous
+ *   k_scale, v_scale   fp32 [pages][heads], one for each page and KV head
+ * and a cached value is code * scale.  A request's rows fill the pages its
+ * block table row names, `page` rows to a page, in order.
+ *
+ * A step brings new rows of several requests ("ragged"): request b has
+ * new rows q_start[b] .. q_start[b + 1] - 1 and, with them, seq_len[b] rows
+ * in all; the i-th of its n new rows has position seq_len[b] - n + i.  All
+ * of it is device memory, so that a step can be captured in a graph and
+ * replayed on other lengths.  Page numbers outside 0 .. pages - 1 (-1 by
+ * convention) mean "no page": append drops rows that fall there, attention
+ * does not see them.
+ *
+ * Calls are asynchronous on `stream`, allocate nothing and synchronise
+ * nothing.  Calls on one handle must be serialised on one stream.
+ * ------------------------------------------------------------------------ */
+typedef struct bsp_kv *bsp_kv_t;
+
+/* Largest batch of a step. */
+#define BSP_KV_MAX_BATCH 16384
+
+typedef struct {
+    int8_t *k, *v;            /* device, 16-B aligned                          */
+    float *k_scale, *v_scale; /* device                                        */
+    int64_t pages;            /* 1 .. 2^31 - 1                                 */
+    int32_t heads;            /* KV heads, 1 .. 32767                          */
+    int32_t page;             /* rows of a page: 16, 32, 64, 128 or 256        */
+    int32_t dim;              /* values of a row: a multiple of 16, 16 .. 256  */
+    int64_t page_stride;      /* codes between pages, heads and rows of k (and */
+    int64_t head_stride;      /*   of v), multiples of 16; row_stride >= dim   */
+    int64_t row_stride;
+    int64_t scale_stride;     /* scales between pages (heads are contiguous)   */
+} bsp_kv_desc_t;
+
+typedef struct {
+    int32_t batch;            /* requests, 0 .. BSP_KV_MAX_BATCH               */
+    int32_t width;            /* entries of a block table row, >= 1            */
+    int64_t table_stride;     /* entries between rows, >= width                */
+    const int32_t *block_table; /* device [batch][width] page numbers          */
+    const int32_t *seq_len;   /* device [batch]                                */
+    const int32_t *q_start;   /* device [batch + 1], q_start[0] = 0, rising    */
+    int64_t max_new;          /* bound on a request's new rows; 0: not known   */
+} bsp_kv_step_t;
+
+/*
+ * A handle over a caller-owned cache.  Copies the description (the arrays
+ * must outlive the handle) and allocates the scratch of its calls on the
+ * current device; synchronises `stream`.  BSP_ERR_SHAPE for sizes or strides
+ * outside the ranges above, BSP_ERR_ALIGN for codes not 16-B aligned.
+ */
+bsp_status_t bsp_kv_create(const bsp_kv_desc_t *desc, bsp_stream_t stream, bsp_kv_t *out);
+
+/* Free a handle (synchronises the device first); the arrays stay. */
+bsp_status_t bsp_kv_destroy(bsp_kv_t h);
+
+/* Synchronise stream and report (then clear) a device-side wait that gave up. */
+bsp_status_t bsp_kv_check(bsp_kv_t h, bsp_stream_t stream);
+
+/*
+ * Plan a step from request lengths, on the device.
+ *   ctx_len   [batch] rows cached so far; new_len [batch] rows asked for, or
+ *             negative: the request has ended and gives its pages back.
+ *   block_table [batch][width] the first ceil(ctx_len / page) entries name
+ *             the request's pages; entries of granted pages are written,
+ *             others are left as they are.
+ *   free_list [free_capacity] a stack of page numbers, of which *free_count
+ *             (device) are live.  Pages given back go on top of it in order
+ *             of request and page, first; then granted pages come off the
+ *             top, in order of request and page.  *free_count_out (device;
+ *             may be free_count) receives the new count; entries from there
+ *             on keep what they held.
+ *   tokens    rows that the step's buffers hold.
+ * First come, first served: a request's rows are granted if, counting every
+ * request up to it, the pages asked for are there and the rows asked for
+ * fit `tokens`; from the first that does not fit on, nothing is granted
+ * (granted = 0).  A request that would outgrow its block table row asks for
+ * nothing.
+ * Outputs: seq_len [batch] (0 for an ended request), q_start [batch + 1],
+ * granted [batch], slots [tokens] (page * page_size + row, int64) and
+ * positions [tokens] of the granted rows, -1 beyond them.
+ */
+bsp_status_t bsp_kv_plan(bsp_kv_t h, const int32_t *ctx_len, const int32_t *new_len, int32_t batch,
+                         int32_t *block_table, int32_t width, int64_t table_stride, int32_t *free_list,
+                         int32_t free_capacity, const int32_t *free_count, int64_t tokens, int32_t *seq_len,
+                         int32_t *q_start, int32_t *granted, int64_t *slots, int32_t *positions,
+                         int32_t *free_count_out, bsp_stream_t stream);
+
+/*
+ * Store the step's new K and V rows, quantised, in their pages.
+ *   k, v   device [rows][heads][dim], dtype BSP_FP16 or BSP_BF16, dim
+ *          contiguous; strides in elements, multiples of 8; 16-B aligned.
+ *          Rows from q_start[batch] on are ignored.
+ * For each page and head that receives rows (K and V apart), with top the
+ * largest finite |x| among them:
+ *   scale' = max(top / 127, scale if the page holds earlier rows of the request)
+ *   earlier codes become round(code * (scale / scale'))
+ *   new codes are round(x / scale') within -127 .. 127; NaN is stored as 0,
+ *   and everything as 0 while scale' is 0.
+ * All in fp32, rounded to nearest even.  A page that receives rows must
+ * belong to one request of the step.
+ */
+bsp_status_t bsp_kv_append(bsp_kv_t h, const bsp_kv_step_t *step, const void *k, const void *v,
+                           bsp_dtype_t dtype, int64_t rows, int64_t k_row_stride, int64_t k_head_stride,
+                           int64_t v_row_stride, int64_t v_head_stride, bsp_stream_t stream);
+
+/*
+ * Cached rows back by slot: k, v device [n][heads][dim] contiguous, 16-B
+ * aligned, BSP_FP16 or BSP_BF16: code * scale in fp32, rounded once.  Slots
+ * outside the cache give zeros.
+ */
+bsp_status_t bsp_kv_read(bsp_kv_t h, const int64_t *slots, int64_t n, void *k, void *v, bsp_dtype_t dtype,
+                         bsp_stream_t stream);
+
+/*
+ * Attention of the step's new rows (stored already) over their requests'
+ * cached rows: for query row i of request b and head a,
+ *   out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale * q . k_j),
+ * over positions j <= pos(i), and j > pos(i) - window if window > 0, whose
+ * page is there; head a reads KV head a / (heads / KV heads).
+ *   q      device [rows][heads][dim], BSP_FP16 or BSP_BF16, dim contiguous,
+ *          strides in elements, multiples of 8; 16-B aligned.
+ *   heads  a multiple of the cache's heads.
+ *   out    device [rows][heads][dim], q's dtype and rules.
+ *   lse    device fp32 [rows][heads] contiguous, log sum_j p_j, or NULL.
+ * A row that sees nothing, and rows from q_start[batch] on, get out = 0 and
+ * lse = -inf.  Logits, maxima and sums are fp32; a probability (relative to
+ * the largest seen) times its V scale is rounded to fp16 for the product.
+ */
+bsp_status_t bsp_kv_attention(bsp_kv_t h, const bsp_kv_step_t *step, const void *q, bsp_dtype_t dtype,
+                              int64_t rows, int32_t heads, int64_t q_row_stride, int64_t q_head_stride,
+                              float scale, int32_t window, void *out, int64_t out_row_stride,
+                              int64_t out_head_stride, float *lse, bsp_stream_t stream);
 
 #ifdef __cplusplus
 }
