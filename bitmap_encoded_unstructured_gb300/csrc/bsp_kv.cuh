@@ -5,6 +5,7 @@
 
 #include "bsp_internal.cuh"
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #define BSP_KV_MAGIC 0xB5B1CAC8u
@@ -29,8 +30,16 @@ struct bsp_kv {
     uint32_t magic;
     int device, num_sms;
     KvView view;
+    // the codes as 4-D tensors {dim, row, head, page}: boxes of up to 32
+    // rows of a page by 64 or 128 dims, swizzled by their width (kv_decode)
+    CUtensorMap map_k, map_v;
     int* ticket;  // arrivals of a plan whose count is updated in place; zero between calls
     int* err;     // as bsp_handle::err
+    // decode: partial results of segments split between CTAs, two slots a
+    // CTA, and the arrivals of each split segment (zero between calls)
+    float* parts;
+    int* arrivals;
+    int decode_ctas;
 };
 
 namespace bspkv {
@@ -60,7 +69,7 @@ KvStepView view_of(const bsp_kv_step_t* st, int64_t rows);
 
 // The request's lengths, held inside its block table row and the call's
 // rows whatever the arrays say: n new rows from row r0 on, the last of them
-// at position len - 1.
+// at position len - 1 (rows at negative positions see and store nothing).
 struct Request {
     int32_t r0, n, len;
 };
@@ -72,9 +81,8 @@ __device__ __forceinline__ Request request_of(const KvStepView& s, int page_shif
     const int64_t len = s.seq_len[b], room = (int64_t)s.width << page_shift;
     r.r0 = (int32_t)(lo < 0 ? 0 : lo);
     r.len = (int32_t)(len < 0 ? 0 : (len > room ? room : len));
-    int64_t n = (hi < s.rows ? hi : s.rows) - r.r0;
-    n = n < 0 ? 0 : n;
-    r.n = (int32_t)(n > r.len ? r.len : n);
+    const int64_t n = (hi < s.rows ? hi : s.rows) - r.r0;
+    r.n = (int32_t)(n < 0 ? 0 : n);
     return r;
 }
 
@@ -91,6 +99,10 @@ template <>
 __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+
+// Encode the tensor maps and allocate the decode scratch of a new handle.
+bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s);
+void attention_free(bsp_kv* h);
 
 }  // namespace bspkv
 

@@ -206,11 +206,11 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs a)
     const bool is_v = unit & 1;
     const int b = item_request(a.s, sh, blockIdx.x);
     const Request r = request_of(a.s, sh, b);
-    const int start = r.len - r.n;                       // position of the first new row
-    const int64_t jj = (start >> sh) + (int64_t)blockIdx.x - ((a.s.q_start[b] >> sh) + 2 * (int64_t)b);
-    if (jj < (start >> sh) || jj << sh >= r.len) return;
+    const int start = r.len - r.n, from = max(start, 0);  // position of the first new row; of the first stored
+    const int64_t jj = (from >> sh) + (int64_t)blockIdx.x - ((a.s.q_start[b] >> sh) + 2 * (int64_t)b);
+    if (jj < (from >> sh) || jj << sh >= r.len) return;
     const int j = (int)jj;
-    const int lo = max(start, j << sh), hi = (int)min((int64_t)r.len, (jj + 1) << sh);  // new rows of this page
+    const int lo = max(from, j << sh), hi = (int)min((int64_t)r.len, (jj + 1) << sh);  // new rows of this page
     if (lo >= hi) return;
     const int p = a.s.table[(int64_t)b * a.s.table_stride + j];
     if (p < 0 || p >= a.c.pages) return;
@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const ReadArgs a)
 void free_kv(bsp_kv* h)
 {
     if (!h) return;
+    attention_free(h);
     cudaFree(h->ticket);
     cudaFree(h->err);
     h->magic = 0;
@@ -372,8 +373,11 @@ bsp_status_t bsp_kv_create(const bsp_kv_desc_t* d, bsp_stream_t stream, bsp_kv_t
     else if (cudaMalloc(&h->ticket, sizeof(int)) != cudaSuccess || cudaMalloc(&h->err, sizeof(int)) != cudaSuccess)
         st = BSP_ERR_OOM;
     else if (cudaMemsetAsync(h->ticket, 0, sizeof(int), s) != cudaSuccess ||
-             cudaMemsetAsync(h->err, 0, sizeof(int), s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
+             cudaMemsetAsync(h->err, 0, sizeof(int), s) != cudaSuccess)
         st = BSP_ERR_CUDA;
+    else
+        st = attention_setup(h, s);
+    if (st == BSP_OK && cudaStreamSynchronize(s) != cudaSuccess) st = BSP_ERR_CUDA;
     if (st != BSP_OK) {
         free_kv(h);
         return st;

@@ -61,7 +61,8 @@ def append(codes, scale, x, table, seq, q_start, page):
     f = np.float32
     for b in range(len(seq)):
         lo, n = int(q_start[b]), int(q_start[b + 1] - q_start[b])
-        start, done = int(seq[b]) - n, 0
+        start = int(seq[b]) - n
+        done = max(0, -start)  # rows at negative positions are not stored
         while done < n:
             j, off = (start + done) // page, (start + done) % page
             m = min(n - done, page - off)

@@ -138,6 +138,18 @@ def test_missing_pages_leave_rows_empty(new):
 
 
 @pytest.mark.parametrize("new", [1, 4, 70])
+def test_more_rows_than_length(new):
+    """Idle requests of a padded batch: rows whose position is negative see nothing."""
+    import torch
+    c = case([(60, new), (0, new), (0, new), (9, new)], 4, 2, 64, 16, torch.float16, 6 + new)
+    c["seq"][1] = 0
+    c["seq"][2] = new // 2
+    out, lse = run(c)
+    check(c, out, lse)
+    assert torch.isneginf(lse[new:2 * new]).all()
+
+
+@pytest.mark.parametrize("new", [1, 4, 70])
 def test_unseen_rows_do_not_matter(new):
     """Garbage in rows and scales that no query sees changes nothing, bit for bit."""
     import torch

@@ -160,6 +160,21 @@ def test_append_drops_rows_without_a_page():
     check_append([(3, 90), (0, 40), (31, 1), (5, 5)], 2, 64, 16, torch.float16, np.random.default_rng(9), drop=True)
 
 
+def test_append_more_rows_than_length():
+    import torch
+    g = np.random.default_rng(13)
+    k, v, ks, vs = make_cache(6, 2, 16, 32, g)
+    table = np.array([[0, 4], [5, 2], [1, 3]], np.int32)
+    seq, start = np.array([0, 3, 20], np.int32), np.array([0, 2, 9, 20], np.int32)
+    x = dev(g.standard_normal((20, 2, 32)).astype(np.float16))
+    t = [dev(a) for a in (k, v, ks, vs)]
+    cache = bsp.KvCache(*t)
+    cache.append(bsp.KvStep(dev(table), dev(seq), dev(start)), x, x)
+    c, s = kv.append(k, ks, x.float().cpu().numpy(), table, seq, start, 16)
+    assert np.array_equal(t[0].cpu().numpy(), c) and np.array_equal(t[2].cpu().numpy(), s)
+    cache.close()
+
+
 def test_append_scales_that_differ_widely():
     import torch
     g = np.random.default_rng(10)
