@@ -4,6 +4,7 @@
 #pragma once
 
 #include "bsp_internal.cuh"
+#include "bsp_ptx.cuh"
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -63,8 +64,11 @@ struct DeviceGuard {
     }
 };
 
-// Checks of a step and of the row tensors' strides, before any CUDA call.
-bsp_status_t check_step(const bsp_kv_step_t* st, int64_t rows);
+// Rows of a call and rows a block table row can name: positions, and their
+// differences to a window, stay in 32 bits.
+constexpr int64_t MOST_ROWS = (int64_t)1 << 30;
+// Checks of a step, before any CUDA call.
+bsp_status_t check_step(const bsp_kv_step_t* st, int64_t rows, int page_shift);
 KvStepView view_of(const bsp_kv_step_t* st, int64_t rows);
 
 // The request's lengths, held inside its block table row and the call's
@@ -100,11 +104,62 @@ __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
 
+struct AttnArgs {
+    KvView c;
+    KvStepView s;
+    const void* q;
+    void* out;
+    float* lse;
+    int64_t q_row, q_head, o_row, o_head;
+    float scale;
+    int32_t heads, group, window;
+};
+
+// Softmax statistics, in powers of two.  A row keeps the largest logit seen
+// (m), the largest logit + log2(V scale) seen (mw), l = sum of 2^(x - m) and
+// O = sum of 2^(x - mw) * V scale * codes; both maxima may lag, so that the
+// sums are rescaled a few times a row, not at every tile.  Two maxima,
+// because the weights 2^(x - mw) * V scale go through fp16: they stay in its
+// range whatever the V scales are.
+constexpr float NONE = -1e30f;           // running maximum before any row is seen
+constexpr float LAZY = 8.f;              // a maximum may lag by 2^8 before sums are rescaled
+constexpr float LIFT = 64.f;             // weights are held 2^6 up, away from fp16's subnormals
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Two fp16 from bytes of w (already offset by 128) picked by sel.
+__device__ __forceinline__ uint32_t widen(uint32_t w, uint32_t sel)
+{
+    const uint32_t h = __byte_perm(w, 0x64646464u, sel);
+    return h2bits(__hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480))));
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(bspx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bspx::smem_u32(bar))
+        : "memory");
+}
+
 // Encode the tensor maps and allocate the decode scratch of a new handle.
 bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s);
 void attention_free(bsp_kv* h);
 
 }  // namespace bspkv
+
+// Attention of the requests with more than `few` query rows per KV head
+// (kv_prompt.cu); dim <= 128.
+bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dtype_t dtype, int32_t few,
+                               cudaStream_t s);
 
 bsp_status_t bsp_run_kv_attention(const bsp_kv* h, const KvStepView& st, int64_t max_new, const void* q,
                                   bsp_dtype_t dtype, int32_t heads, int64_t q_row, int64_t q_head, float scale,

@@ -16,17 +16,6 @@ namespace {
 
 using namespace bspkv;
 
-struct AttnArgs {
-    KvView c;
-    KvStepView s;
-    const void* q;
-    void* out;
-    float* lse;
-    int64_t q_row, q_head, o_row, o_head;
-    float scale;
-    int32_t heads, group, window;
-};
-
 // ------------------------------------------------------------ few queries
 //
 // One kernel for requests with few query rows per KV head (decoding,
@@ -48,9 +37,6 @@ struct AttnArgs {
 constexpr int DEC_WARPS = 4;
 constexpr int SUB = 32;                  // rows of a unit that one warp takes
 constexpr int UNIT = DEC_WARPS * SUB;
-constexpr float NONE = -1e30f;           // running maximum before any row is seen
-constexpr float LAZY = 8.f;              // a maximum may lag by 2^8 before sums are rescaled
-constexpr float LIFT = 64.f;             // weights are held 2^6 up, away from fp16's subnormals
 constexpr int PART_FLOATS = 4352;        // of one partial result: queries x (dims + 3), at most
 
 template <int DP, int NT>
@@ -79,22 +65,6 @@ struct DecodeArgs {
     int32_t most_rows;  // requests with more query rows than this (per KV head) are not this kernel's
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-
-// Two fp16 from bytes of w (already offset by 128) picked by sel.
-__device__ __forceinline__ uint32_t widen(uint32_t w, uint32_t sel)
-{
-    const uint32_t h = __byte_perm(w, 0x64646464u, sel);
-    return h2bits(__hsub2(*reinterpret_cast<const __half2*>(&h), __half2half2(__ushort_as_half(0x6480))));
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
@@ -110,15 +80,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(bspx::smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bspx::smem_u32(bar))
-        : "memory");
 }
 
 // A request's share of the work: cached rows [lo, len) that some query sees
@@ -673,84 +634,6 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
 }
 
-// One warp per (row, head): lane i takes token i of a run of 32, softmax
-// statistics are the warp's, then lane i owns dims i, i + 32, ...
-template <class T>
-__global__ void __launch_bounds__(128) kv_attention_rows_kernel(const AttnArgs a, int few)
-{
-    __shared__ __align__(16) float qs[4][256];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, dim = a.c.dim, sh = a.c.page_shift;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + w;
-    if (unit >= a.s.rows * a.heads) return;
-    const int row = (int)(unit / a.heads), head = (int)(unit % a.heads), kvh = head / a.group;
-    int lo = 0, hi = a.s.batch;
-    while (hi - lo > 1) {  // the request of the row
-        const int mid = (lo + hi) >> 1;
-        if (a.s.q_start[mid] <= row) lo = mid;
-        else hi = mid;
-    }
-    int pos = -1;
-    if (a.s.batch) {
-        const Request r = request_of(a.s, sh, lo);
-        if (row >= r.r0 && row < r.r0 + r.n) pos = r.len - r.n + row - r.r0;
-        if ((int64_t)r.n * a.group <= few) return;  // the other kernel's
-    }
-    const T* q = (const T*)a.q + row * a.q_row + head * a.q_head;
-    for (int d = lane; d < dim; d += 32) qs[w][d] = to_float(q[d]) * a.scale;
-    __syncwarp();
-    const int first = a.window ? max(0, pos - a.window + 1) : 0;
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    for (int j0 = first; j0 <= pos; j0 += 32) {
-        const int j = j0 + lane;
-        int p = -1;
-        float x = -INFINITY, vs = 0.f;
-        if (j <= pos) {
-            p = a.s.table[(int64_t)lo * a.s.table_stride + (j >> sh)];
-            if (p >= a.c.pages) p = -1;
-        }
-        const int64_t at = (int64_t)(p < 0 ? 0 : p) * a.c.page_stride + (int64_t)kvh * a.c.head_stride +
-                           (int64_t)(j & ((1 << sh) - 1)) * a.c.row_stride;
-        if (p >= 0) {
-            float sum = 0.f;
-            for (int d = 0; d < dim; d += 16) {
-                const int4 raw = *reinterpret_cast<const int4*>(a.c.k + at + d);
-                const int8_t* e = reinterpret_cast<const int8_t*>(&raw);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) sum += qs[w][d + c] * (float)e[c];
-            }
-            x = sum * a.c.k_scale[(int64_t)p * a.c.scale_stride + kvh];
-            vs = a.c.v_scale[(int64_t)p * a.c.scale_stride + kvh];
-        }
-        float top = x;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        top = fmaxf(top, m);
-        if (top == -INFINITY) continue;  // nothing seen yet
-        const float back = __expf(m - top), e = p >= 0 ? __expf(x - top) : 0.f;
-        m = top;
-        float sum = e;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        l = l * back + sum;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) o[c] *= back;
-        const float pv = e * vs;
-        for (int t = 0; t < 32; ++t) {
-            const float f = __shfl_sync(0xFFFFFFFFu, pv, t);
-            const int64_t vat = __shfl_sync(0xFFFFFFFFu, at, t);
-            if (__shfl_sync(0xFFFFFFFFu, p, t) < 0) continue;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                if (lane + 32 * c < dim) o[c] += f * (float)a.c.v[vat + lane + 32 * c];
-        }
-    }
-    T* out = (T*)a.out + row * a.o_row + head * a.o_head;
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-        if (lane + 32 * c < dim) out[lane + 32 * c] = from_float<T>(l > 0.f ? o[c] / l : 0.f);
-    if (a.lse && lane == 0) a.lse[(int64_t)row * a.heads + head] = l > 0.f ? m + logf(l) : -INFINITY;
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
     static std::once_flag once;
@@ -806,16 +689,14 @@ bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream
 {
     const int64_t most = max_new * a.group;
     // Query blocks of 8, 16 or 32 rows: the smallest that holds the largest
-    // request, as far as the kernel is for it
-    const int few = 32;
+    // request.  Requests with more rows are the prompt kernel's, whose row
+    // tiles have 128 rows and whose dims end at 128.
+    const int few = a.c.dim > 128 ? INT32_MAX : 32;
     const int nt = most <= 8 ? 1 : most <= 16 ? 2 : 4;
-    const DecodeArgs d = {a, h->parts, h->arrivals, h->err, bsp_spin_cap(), most <= few ? INT32_MAX : few};
+    const DecodeArgs d = {a, h->parts, h->arrivals, h->err, bsp_spin_cap(), few};
     if (const bsp_status_t st = run_decode<T>(h, d, nt, s)) return st;
-    if (most <= few) return BSP_OK;
-    const int64_t grid = (a.s.rows * a.heads + 3) / 4;
-    if (grid > 0x7FFFFFFF) return BSP_ERR_INVALID_ARG;
-    kv_attention_rows_kernel<T><<<(unsigned)grid, 128, 0, s>>>(a, few);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    if (most <= few || !a.s.batch) return BSP_OK;
+    return bsp_run_kv_prompt(h, a, std::is_same<T, __half>::value ? BSP_FP16 : BSP_BF16, few, s);
 }
 
 }  // namespace
@@ -862,6 +743,8 @@ bsp_status_t bsp_run_kv_attention(const bsp_kv* h, const KvStepView& st, int64_t
                                   int32_t window, void* out, int64_t o_row, int64_t o_head, float* lse,
                                   cudaStream_t s)
 {
+    // a window no row can look beyond is none (and positions minus a window stay in 32 bits)
+    if (window >= (int64_t)st.width << h->view.page_shift) window = 0;
     const AttnArgs a = {h->view, st, q, out, lse, q_row, q_head, o_row, o_head, scale, heads, heads / h->view.heads,
                         window};
     return dtype == BSP_FP16 ? run<__half>(h, a, max_new, s) : run<__nv_bfloat16>(h, a, max_new, s);

@@ -326,12 +326,14 @@ bool good_strides(int64_t row, int64_t head, int32_t dim, int64_t rows, int32_t 
 
 namespace bspkv {
 
-bsp_status_t check_step(const bsp_kv_step_t* st, int64_t rows)
+bsp_status_t check_step(const bsp_kv_step_t* st, int64_t rows, int page_shift)
 {
-    if (!st || rows < 0 || rows > INT32_MAX) return BSP_ERR_INVALID_ARG;
+    if (!st || rows < 0 || rows > MOST_ROWS) return BSP_ERR_INVALID_ARG;
     if (st->batch < 0 || st->batch > BSP_KV_MAX_BATCH || st->max_new < 0) return BSP_ERR_INVALID_ARG;
     if (st->batch && (!st->block_table || !st->seq_len || !st->q_start)) return BSP_ERR_INVALID_ARG;
-    if (st->batch && (st->width < 1 || st->table_stride < st->width)) return BSP_ERR_SHAPE;
+    if (st->batch && (st->width < 1 || st->table_stride < st->width ||
+                      (int64_t)st->width << page_shift > MOST_ROWS))
+        return BSP_ERR_SHAPE;
     return BSP_OK;
 }
 
@@ -442,7 +444,7 @@ bsp_status_t bsp_kv_append(bsp_kv_t h, const bsp_kv_step_t* step, const void* k,
                            bsp_stream_t stream)
 {
     if (!valid(h)) return BSP_ERR_INVALID_ARG;
-    if (const bsp_status_t st = check_step(step, rows)) return st;
+    if (const bsp_status_t st = check_step(step, rows, h->view.page_shift)) return st;
     if (dtype != BSP_FP16 && dtype != BSP_BF16) return BSP_ERR_DTYPE;
     if (!rows || !step->batch) return BSP_OK;
     if (!k || !v) return BSP_ERR_INVALID_ARG;
@@ -485,7 +487,7 @@ bsp_status_t bsp_kv_attention(bsp_kv_t h, const bsp_kv_step_t* step, const void*
                               int64_t o_row, int64_t o_head, float* lse, bsp_stream_t stream)
 {
     if (!valid(h)) return BSP_ERR_INVALID_ARG;
-    if (const bsp_status_t st = check_step(step, rows)) return st;
+    if (const bsp_status_t st = check_step(step, rows, h->view.page_shift)) return st;
     if (dtype != BSP_FP16 && dtype != BSP_BF16) return BSP_ERR_DTYPE;
     // scale: finite and not negative (a comparison that NaN fails)
     if (window < 0 || !(scale >= 0.f && scale < INFINITY)) return BSP_ERR_INVALID_ARG;

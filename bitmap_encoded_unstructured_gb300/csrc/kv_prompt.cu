@@ -1,0 +1,606 @@
+// Attention of many queries (prompts, chunks of prompts) over the paged
+// 8-bit cache, on the 5th-generation tensor cores.
+//
+// A CTA takes 256 query rows of one request and KV head (a row = a query
+// token and one of the heads that share the KV head) as two row tiles of
+// 128, and walks the cached rows they see in tiles of 128:
+//   S = Q . codes_K^T     tcgen05.mma 128 x 128 x dim, Q and K in shared memory
+//   P = 2^(S * k scale - m), W = fp16(P * V scale)      one thread per row
+//   O += W . codes_V      tcgen05.mma 128 x dim x 128, W in tensor memory
+// The codes are exact in fp16, so the products see them unrounded; the
+// scales (one for each page) are factors of 16 or more columns and are
+// applied to S and P.  While one row tile's softmax runs, the tensor cores
+// work on the other's.
+//
+// Warps: 0 loads codes (TMA boxes of the paged cache) and scales; 1 issues
+// the MMAs; 4-7 turn codes into fp16 tiles; 8-11 and 12-15 are the softmax
+// of row tiles 0 and 1 (a warp reaches the 32 tensor-memory lanes 32 (w % 4)
+// .. + 31).  Rings: codes (K and V tiles in turn, four deep), fp16 tiles
+// (three deep: V of a tile and K of the next are live while the next V is
+// made).  Both fp16 tiles have one layout, rows of 64 dims swizzled by 128
+// bytes: K-major for the first product, MN-major for the second.
+// Tensor memory: S0, S1 (128 fp32 columns each; W takes the lower half of
+// its own S), O0, O1.
+#include "bsp_kv.cuh"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace {
+
+using namespace bspkv;
+
+constexpr uint32_t FULL = 0xFFFFFFFFu;
+constexpr int ROWS = 256;      // query rows of a CTA
+constexpr int TOK = 128;       // cached rows of a tile
+constexpr int GROUPS = TOK / 16;
+constexpr int NC = 4, NF = 3, NM = 4;  // rings: codes, fp16 tiles, scales
+constexpr int THREADS = 512;
+constexpr uint32_t kSleepNs = 200;     // suspend hint of a waiting poll
+
+template <int DP>
+struct Cfg {
+    static constexpr int BLK = TOK * 128;               // 128 rows x 64 dims fp16 (or a Q block)
+    static constexpr int QT = BLK * (DP / 64);          // Q of a row tile
+    static constexpr int FT = BLK * (DP / 64);          // fp16 K or V tile
+    static constexpr int CT = TOK * DP;                 // codes of a tile
+    static constexpr int OFF_F = 2 * QT;
+    static constexpr int OFF_C = OFF_F + NF * FT;
+    static constexpr int OFF_META = OFF_C + NC * CT;    // per scale slot: ks, vs, log2 vs [8] each, mask
+    static constexpr int META = 3 * GROUPS + 4;         // floats
+    static constexpr int OFF_BAR = OFF_META + NM * META * 4;
+    static constexpr int NBAR = 2 * NC + 2 * NF + NM + 1 + 3 * 2 + 1;
+    static constexpr int END = OFF_BAR + NBAR * 8 + 16;
+    // one CTA per SM: it may take all of the tensor memory
+    static constexpr int SMEM = (END > 120 * 1024 ? END : 120 * 1024) + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+struct PromptArgs {
+    AttnArgs a;
+    int* err;
+    uint32_t spin_cap;
+    int32_t few;
+    int64_t items;  // CTAs of one KV head
+};
+
+// kind::f16 instruction descriptor: D fp32, A and B fp16, M = 128.
+__host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major)
+{
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+// Shared-memory matrix descriptor, rows of 128 B swizzled by 128 B, 8-row
+// atoms of 1 KB.  K-major: the rows are M or N, the stride between atoms is
+// 1 KB, the leading offset is not used.  MN-major: the rows are K, the
+// stride between 8-row atoms is 1 KB and the leading offset is the distance
+// of the next 64 columns.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t leading)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((leading >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1u << 46;  // descriptor version of sm_100
+    d |= (uint64_t)2u << 61;  // SWIZZLE_128B
+    return d;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accum)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accum)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     bspx::smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// 32 consecutive tensor-memory columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+// The whole warp waits; false if the wait ran out.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t cap)
+{
+    return __all_sync(FULL, bspx::mbar_wait_sleep(bar, parity, cap, kSleepNs));
+}
+
+template <class T, int DP>
+__global__ void __launch_bounds__(THREADS, 1)
+kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PromptArgs d)
+{
+    using C = Cfg<DP>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (bspx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    const AttnArgs& a = d.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sh = a.c.page_shift, dim = a.c.dim;
+    const int H = a.c.heads;
+
+    // the item: long rows first (later rows of a causal prompt see more),
+    // the heads of one row tile side by side
+    const int h = (int)(blockIdx.x % H);
+    const int64_t item = d.items - 1 - (int64_t)(blockIdx.x / H);
+    int b = 0;
+    {  // request b's items start at F(b) = q_start[b] * group / ROWS + b
+        int hi = a.s.batch;
+        while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if ((int64_t)a.s.q_start[mid] * a.group / ROWS + mid <= item) b = mid;
+            else hi = mid;
+        }
+    }
+    const Request rq = request_of(a.s, sh, b);
+    const int64_t rows = (int64_t)rq.n * a.group;
+    const int64_t row0 = (item - ((int64_t)a.s.q_start[b] * a.group / ROWS + b)) * ROWS;
+    if (row0 < 0 || row0 >= rows || rows <= d.few) return;
+    const int n_rows = (int)min((int64_t)ROWS, rows - row0);
+    const bool two = n_rows > 128;
+    const int first = rq.len - rq.n;                                 // position of the request's first query
+    const int pos0 = first + (int)(row0 / a.group), pos1 = first + (int)((row0 + n_rows - 1) / a.group);
+    const int seen = a.window ? max(0, pos0 - a.window + 1) : 0;    // first cached row that a query sees
+    const int t0 = seen & ~(TOK - 1);
+    const int tiles = pos1 >= t0 ? (pos1 + 1 - t0 + TOK - 1) / TOK : 0;
+    const uint32_t cap = d.spin_cap;
+
+    uint64_t* c_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* c_empty = c_full + NC;
+    uint64_t* f_full = c_empty + NC;
+    uint64_t* f_empty = f_full + NF;
+    uint64_t* m_full = f_empty + NF;
+    uint64_t* q_full = m_full + NM;
+    uint64_t* s_full = q_full + 1;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_done = p_full + 2;
+    uint64_t* drain = o_done + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    float* meta = reinterpret_cast<float*>(smem + C::OFF_META);
+
+    if (warp == 1) {
+        __syncwarp();
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         bspx::smem_u32(tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NC; ++i) {
+            bspx::mbar_init(c_full + i, 1);
+            bspx::mbar_init(c_empty + i, 4);
+        }
+        for (int i = 0; i < NF; ++i) {
+            bspx::mbar_init(f_full + i, 4);
+            bspx::mbar_init(f_empty + i, 1);
+        }
+        for (int i = 0; i < NM; ++i) bspx::mbar_init(m_full + i, 1);
+        bspx::mbar_init(q_full, 8);
+        for (int i = 0; i < 2; ++i) {
+            bspx::mbar_init(s_full + i, 1);
+            bspx::mbar_init(p_full + i, 4);
+            bspx::mbar_init(o_done + i, 1);
+        }
+        bspx::mbar_init(drain, 1);
+        bspx::fence_mbar_init();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tmem_slot;
+    bool failed = false;
+
+    if (warp == 0) {
+        // ---------------- codes and scales: lane l < 8 looks after rows 16 l ..
+        const int32_t* table = a.s.table + (int64_t)b * a.s.table_stride;
+        const int box = min(32, 1 << sh);
+        auto page_of = [&](int j) {
+            const int tok = t0 + j * TOK + 16 * lane;
+            int p = -1;
+            if (lane < GROUPS && j < tiles && tok < rq.len && ((tok >> sh) + 1) << sh > seen) {
+                p = table[tok >> sh];
+                if (p >= a.c.pages) p = -1;
+            }
+            return p;
+        };
+        int p = page_of(0);
+        int n = 0;  // tiles issued, K and V counted apart
+        for (int j = 0; j < tiles && !failed; ++j) {
+            const int next = page_of(j + 1);
+            const int tok = t0 + j * TOK + 16 * lane;
+            const bool mine = p >= 0 && (box == 16 || (lane & 1) == 0);
+            const uint32_t bytes = __popc(__ballot_sync(FULL, mine)) * box * DP;
+            for (int v = 0; v < 2; ++v, ++n) {
+                const int slot = n % NC;
+                if (n >= NC && !wait(c_empty + slot, (n / NC - 1) & 1, cap)) {
+                    failed = true;
+                    break;
+                }
+                if (lane == 0) {
+                    if (bytes) bspx::mbar_arrive_expect_tx(c_full + slot, bytes);
+                    else bspx::mbar_arrive(c_full + slot);
+                }
+                __syncwarp();
+                if (mine)
+                    tma_load_4d(smem + C::OFF_C + slot * C::CT + 16 * lane * DP, v ? &map_v : &map_k, 0,
+                                tok & ((1 << sh) - 1), h, p, c_full + slot);
+            }
+            if (failed) break;
+            // slot j % NM was last read for tile j - NM, whose products are done:
+            // the codes of tile j could not have been asked for otherwise
+            float* mt = meta + (j % NM) * C::META;
+            const float ks = p >= 0 ? a.c.k_scale[(int64_t)p * a.c.scale_stride + h] : 0.f;
+            const float vs = p >= 0 ? a.c.v_scale[(int64_t)p * a.c.scale_stride + h] : 0.f;
+            const uint32_t there = __ballot_sync(FULL, p >= 0);
+            if (lane < GROUPS) {
+                mt[lane] = ks;
+                mt[GROUPS + lane] = vs;
+                mt[2 * GROUPS + lane] = vs != 0.f ? __log2f(fabsf(vs)) : NONE;
+            }
+            if (lane == 0) reinterpret_cast<uint32_t*>(mt)[3 * GROUPS] = there;
+            __syncwarp();
+            if (lane == 0) bspx::mbar_arrive(m_full + j % NM);
+            p = next;
+        }
+        for (int i = std::max(0, n - NC); i < n; ++i)  // no copy may land after the CTA is gone
+            bspx::mbar_wait_bounded(c_full + i % NC, (i / NC) & 1, cap);
+    } else if (warp == 1) {
+        // ---------------- MMA issuer
+        const int ks_steps = dim / 16;
+        const uint32_t q_at = bspx::smem_u32(smem), f_at = bspx::smem_u32(smem + C::OFF_F);
+        const uint32_t id_s = idesc(TOK, false), id_o = idesc(dim, true);
+        auto product_s = [&](int t, int n) {  // S of row tile t from K tile n of the fp16 ring
+            if (lane == 0) {
+                for (int k = 0; k < ks_steps; ++k) {
+                    const uint32_t at = (k >> 2) * C::BLK + (k & 3) * 32;
+                    mma_ss(tmem + t * TOK, smem_desc(q_at + t * C::QT + at, 16),
+                           smem_desc(f_at + (n % NF) * C::FT + at, 16), id_s, k ? 1u : 0u);
+                }
+                commit(s_full + t);
+            }
+            __syncwarp();
+        };
+        auto product_o = [&](int t, int n, bool more) {
+            if (lane == 0) {
+#pragma unroll
+                for (int k = 0; k < TOK / 16; ++k)
+                    mma_ts(tmem + 2 * TOK + t * DP, tmem + t * TOK + 8 * k,
+                           smem_desc(f_at + (n % NF) * C::FT + k * 2048, C::BLK), id_o, (more || k) ? 1u : 0u);
+                commit(o_done + t);
+            }
+            __syncwarp();
+        };
+        auto release = [&](int n) {
+            if (lane == 0) commit(f_empty + n % NF);
+            __syncwarp();
+        };
+        auto ready = [&](uint64_t* bar, uint32_t parity) {
+            if (!failed && !wait(bar, parity, cap)) failed = true;
+            tc_after();
+            return !failed;
+        };
+        if (tiles && ready(q_full, 0) && ready(f_full, 0)) {
+            product_s(0, 0);
+            if (two) product_s(1, 0);
+            release(0);
+            for (int j = 0; j < tiles; ++j) {
+                const int v = 2 * j + 1, k = 2 * j + 2;
+                const bool more = j + 1 < tiles;
+                if (!ready(f_full + v % NF, (v / NF) & 1) || !ready(p_full, j & 1)) break;
+                product_o(0, v, j > 0);
+                if (more) {
+                    if (!ready(f_full + k % NF, (k / NF) & 1)) break;
+                    product_s(0, k);
+                }
+                if (two) {
+                    if (!ready(p_full + 1, j & 1)) break;
+                    product_o(1, v, j > 0);
+                }
+                release(v);
+                if (more) {
+                    if (two) product_s(1, k);
+                    release(k);
+                }
+            }
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------- codes -> fp16.  A thread's chunk of 16 codes and the
+        // rows of its eight-lane phase (r and r ^ 5) are such that both the
+        // loads and the two stores of a phase fall into distinct banks.
+        const int w = warp - 4, c = lane & 3, r8 = ((lane >> 3) & 3) ^ ((lane & 4) ? 5 : 0);
+        for (int n = 0; n < 2 * tiles; ++n) {
+            const int from = n % NC, to = n % NF;
+            if (!wait(c_full + from, (n / NC) & 1, cap) || (n >= NF && !wait(f_empty + to, (n / NF - 1) & 1, cap))) {
+                failed = true;
+                break;
+            }
+            const uint8_t* src = smem + C::OFF_C + from * C::CT;
+            uint8_t* dst = smem + C::OFF_F + to * C::FT;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 8 * (w + 4 * i) + r8;
+#pragma unroll
+                for (int half = 0; half < DP / 64; ++half) {
+                    const int ch = c + 4 * half;
+                    const int sw = DP == 64 ? (row >> 1) & 3 : row & 7;
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + row * DP + ((ch ^ sw) << 4));
+                    const uint32_t x[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+                    uint8_t* at = dst + half * C::BLK + row * 128;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint4*>(at + (((2 * c + e) ^ (row & 7)) << 4)) =
+                            make_uint4(widen(x[2 * e], 0x4140), widen(x[2 * e], 0x4342), widen(x[2 * e + 1], 0x4140),
+                                       widen(x[2 * e + 1], 0x4342));
+                }
+            }
+            bspx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                bspx::mbar_arrive(f_full + to);
+                bspx::mbar_arrive(c_empty + from);
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------- softmax of one row per thread
+        const int t = (warp - 8) >> 2, quad = warp & 3;
+        const int tr = 32 * quad + lane;                     // row of the tile
+        const int64_t r = row0 + 128 * t + tr;               // row of the request
+        const bool mine = 128 * t + tr < n_rows;
+        const int64_t q_tok = rq.r0 + r / a.group;
+        const int head = h * a.group + (int)(r % a.group);
+        // the query row to shared memory; bfloat16 rows are brought into
+        // fp16's range by a power of two
+        float unit = 1.f;
+        {
+            const T* q = (const T*)a.q + q_tok * a.q_row + (int64_t)head * a.q_head;
+            float inv = 1.f;
+            if constexpr (!std::is_same<T, __half>::value) {
+                float top = 0.f;
+                if (mine)
+                    for (int i = 0; i < dim / 8; ++i) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(q + 8 * i);
+                        const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(to_float(e[x])));
+                    }
+                const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+                unit = __uint_as_float(e << 23);
+                inv = __uint_as_float((254u - e) << 23);
+            }
+            uint8_t* to = smem + t * C::QT + tr * 128;
+            for (int i = 0; i < dim / 8; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (mine) {
+                    v = *reinterpret_cast<const uint4*>(q + 8 * i);
+                    if constexpr (!std::is_same<T, __half>::value) {
+                        const T* e = reinterpret_cast<const T*>(&v);
+                        uint32_t y[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            y[x] = h2bits(__floats2half2_rn(to_float(e[2 * x]) * inv, to_float(e[2 * x + 1]) * inv));
+                        v = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(to + (i >> 3) * C::BLK + (((i & 7) ^ (tr & 7)) << 4)) = v;
+            }
+            bspx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) bspx::mbar_arrive(q_full);
+        }
+        const float unit_scale = unit * (a.scale * 1.4426950408889634f);
+        const int pos = mine ? first + (int)(r / a.group) : -1;
+        const int tile_pos0 = first + (int)((row0 + 128 * t) / a.group);
+        const int tile_pos1 = first + (int)((row0 + min(128 * t + 127, n_rows - 1)) / a.group);
+        const uint32_t s_at = tmem + t * TOK + ((uint32_t)(32 * quad) << 16);
+        const uint32_t o_at = tmem + 2 * TOK + t * DP + ((uint32_t)(32 * quad) << 16);
+        float m = NONE, mw = NONE, l = 0.f, lift = LIFT;
+        const int my_tiles = t == 0 || two ? tiles : 0;
+        for (int j = 0; j < my_tiles; ++j) {
+            if (!wait(m_full + j % NM, (j / NM) & 1, cap) || !wait(s_full + t, j & 1, cap)) {
+                failed = true;
+                break;
+            }
+            tc_after();
+            const float* mt = meta + (j % NM) * C::META;
+            const uint32_t there = reinterpret_cast<const uint32_t*>(mt)[3 * GROUPS];
+            const int tok = t0 + j * TOK;
+            const bool edge = tok + TOK - 1 > tile_pos0 || (a.window && tok <= tile_pos1 - a.window) || there != 0xFFu;
+            // columns lo .. hi of this tile are this row's
+            const int hi = pos - tok, lo = (a.window ? max(pos - a.window + 1, 0) : 0) - tok;
+            uint32_t x[32];
+            // largest logits
+            float top = -INFINITY, topw = -INFINITY;
+#pragma unroll
+            for (int cb = 0; cb < TOK; cb += 32) {
+                __syncwarp();
+                tmem_ld32(s_at + cb, x);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float big = -INFINITY;
+                    if (edge) {
+                        const bool see = (there >> (cb / 16 + g)) & 1;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int col = cb + 16 * g + i;
+                            if (see && col <= hi && col >= lo) big = fmaxf(big, __uint_as_float(x[16 * g + i]));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) big = fmaxf(big, __uint_as_float(x[16 * g + i]));
+                    }
+                    const float kf = mt[cb / 16 + g] * unit_scale;
+                    big = big == -INFINITY ? big : big * kf;
+                    top = fmaxf(top, big);
+                    topw = fmaxf(topw, big + mt[2 * GROUPS + cb / 16 + g]);
+                }
+            }
+            if (__any_sync(FULL, top > m + LAZY || topw > mw + LAZY)) {
+                top = fmaxf(top, m);
+                topw = fmaxf(topw, mw);
+                l *= ex2(m - top);
+                if (j) {  // O is whole once the product of the tile before is done
+                    const float back = ex2(mw - topw);
+                    if (!wait(o_done + t, (j - 1) & 1, cap)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_after();
+                    for (int cb = 0; cb < DP; cb += 32) {
+                        uint32_t o[32];
+                        __syncwarp();
+                        tmem_ld32(o_at + cb, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * back);
+                        tmem_st32(o_at + cb, o);
+                    }
+                }
+                m = top;
+                mw = topw;
+                lift = ex2(fminf(m - mw, 120.f)) * LIFT;
+            }
+            // weights
+#pragma unroll
+            for (int cb = 0; cb < TOK; cb += 32) {
+                __syncwarp();
+                tmem_ld32(s_at + cb, x);
+                uint32_t y[16];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float kf = mt[cb / 16 + g] * unit_scale, vf = mt[GROUPS + cb / 16 + g] * lift;
+                    const bool see = (there >> (cb / 16 + g)) & 1;
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        float z[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int col = cb + 16 * g + i + e;
+                            z[e] = fmaf(__uint_as_float(x[16 * g + i + e]), kf, -m);
+                            if (edge && !(see && col <= hi && col >= lo)) z[e] = -INFINITY;
+                            z[e] = ex2(z[e]);
+                            l += z[e];
+                        }
+                        y[8 * g + i / 2] = h2bits(__floats2half2_rn(z[0] * vf, z[1] * vf));
+                    }
+                }
+                tmem_st16(s_at + cb / 2, y);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bspx::mbar_arrive(p_full + t);
+        }
+        // ---------------- the rows out
+        if (my_tiles && !failed && !wait(o_done + t, (my_tiles - 1) & 1, cap)) failed = true;
+        tc_after();
+        const float f = l > 0.f ? ex2(mw - m) / (l * LIFT) : 0.f;
+        T* out = (T*)a.out + q_tok * a.o_row + (int64_t)head * a.o_head;
+        if (!failed && (t == 0 || two)) {
+            for (int cb = 0; cb < dim; cb += 32) {
+                uint32_t x[32];
+                __syncwarp();
+                if (my_tiles) tmem_ld32(o_at + cb, x);
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    alignas(16) T y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] = from_float<T>(l > 0.f ? __uint_as_float(x[i + e]) * f : 0.f);
+                    if (mine && cb + i < dim)
+                        *reinterpret_cast<uint4*>(out + cb + i) = *reinterpret_cast<const uint4*>(y);
+                }
+            }
+            if (mine && a.lse)
+                a.lse[q_tok * a.heads + head] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+    }
+
+    if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
+    if (warp == 1) {  // no product in flight (after a wait ran out) when shared and tensor memory are given back
+        if (lane == 0) commit(drain);
+        __syncwarp();
+        wait(drain, 0, cap);
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_after();
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+template <class T, int DP>
+bsp_status_t launch(const bsp_kv* h, const PromptArgs& d, cudaStream_t s)
+{
+    using C = Cfg<DP>;
+    static bsp_attr_once attr_once;
+    if (!attr_once.run(h->device, [] {
+            return cudaFuncSetAttribute(kv_prompt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        }))
+        return BSP_ERR_CUDA;
+    const int64_t ctas = d.items * h->view.heads;
+    if (ctas > 0x7FFFFFFF) return BSP_ERR_INVALID_ARG;
+    kv_prompt_kernel<T, DP><<<(unsigned)ctas, THREADS, C::SMEM, s>>>(h->map_k, h->map_v, d);
+    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+}
+
+}  // namespace
+
+bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dtype_t dtype, int32_t few, cudaStream_t s)
+{
+    PromptArgs d = {a, h->err, bsp_spin_cap(), few, a.s.rows * a.group / ROWS + a.s.batch};
+    const bool wide = a.c.dim > 64;
+    if (dtype == BSP_FP16) return wide ? launch<__half, 128>(h, d, s) : launch<__half, 64>(h, d, s);
+    return wide ? launch<__nv_bfloat16, 128>(h, d, s) : launch<__nv_bfloat16, 64>(h, d, s);
+}

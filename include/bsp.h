@@ -554,14 +554,14 @@ bsp_status_t bsp_union_check(bsp_union_t h, bsp_stream_t stream);
  * The caller owns the cache (from its own allocator) and describes it once:
  *   k, v               int8 codes [pages][heads][page][dim], dim contiguous
  *   k_scale, v_scale   fp32 [pages][heads], one for each page and KV head
- * and a cached value is code * scale.  A request's rows fill the pages its
+ * and a cached value is code * scale (scales are not negative).  A request's rows fill the pages its
  * block table row names, `page` rows to a page, in order.
  *
  * A step brings new rows of several requests ("ragged"): request b has
  * new rows q_start[b] .. q_start[b + 1] - 1 and, with them, seq_len[b] rows
  * in all; the i-th of its n new rows has position seq_len[b] - n + i.  All
  * of it is device memory, so that a step can be captured in a graph and
- * replayed on other lengths.  Page numbers outside 0 .. pages - 1 (-1 by
+ * replayed on other lengths.  A call takes at most 2^30 rows.  Page numbers outside 0 .. pages - 1 (-1 by
  * convention) mean "no page": append drops rows that fall there, attention
  * does not see them.
  *
@@ -588,7 +588,7 @@ typedef struct {
 
 typedef struct {
     int32_t batch;            /* requests, 0 .. BSP_KV_MAX_BATCH               */
-    int32_t width;            /* entries of a block table row, >= 1            */
+    int32_t width;            /* entries of a block table row, 1 .. 2^30 / page */
     int64_t table_stride;     /* entries between rows, >= width                */
     const int32_t *block_table; /* device [batch][width] page numbers          */
     const int32_t *seq_len;   /* device [batch]                                */
