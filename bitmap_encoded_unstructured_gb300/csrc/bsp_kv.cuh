@@ -36,11 +36,10 @@ struct bsp_kv {
     CUtensorMap map_k, map_v;
     int* ticket;  // arrivals of a plan whose count is updated in place; zero between calls
     int* err;     // as bsp_handle::err
-    // decode: partial results of segments split between CTAs, two slots a
-    // CTA, and the arrivals of each split segment (zero between calls)
+    // few queries: parts of segments cut between warps, two slots a warp, and
+    // the arrivals of each such segment (zero between calls)
     float* parts;
     int* arrivals;
-    int decode_ctas;
 };
 
 namespace bspkv {

@@ -19,15 +19,19 @@ using namespace bspkv;
 // ------------------------------------------------------------ few queries
 //
 // One kernel for requests with few query rows per KV head (decoding,
-// drafts): bound by the bytes of the codes.  The CTAs share the cached rows
-// of all requests evenly ("units" of UNIT rows of one KV head, in order of
-// request, head and row group), so that neither ragged lengths nor few
-// requests leave SMs idle; a segment (request, head, row group) cut between
-// CTAs is joined by the last of them to arrive, in order.
+// drafts): bound by the bytes of the codes.  A segment is one request, KV
+// head and group of Q query rows; its cached rows are taken in sub-tiles of
+// 32.  The warps of the grid share all sub-tiles evenly, each a contiguous
+// run of them in order of request, head and group, so that neither ragged
+// lengths nor few requests leave SMs idle.  A segment counts OVER sub-tiles
+// more than it has, the price of starting and finishing one.
 //
-// Inside a CTA each warp streams 32 rows of every unit through a ring of
-// its own (TMA boxes of the paged codes, no block-wide barrier in the loop)
-// and works on them alone:
+// A warp works alone: it streams its sub-tiles through a ring of its own
+// (TMA boxes of the paged codes, across segment ends), with no block-wide
+// barrier until its run is done, and writes the segments that it has whole.
+// Of a segment cut between warps each leaves a part (the warps of a CTA add
+// theirs first); the last to arrive joins the parts, in order.
+//
 //   S^T[row][query] = codes_K . q     mma m16n8k16, A = codes as exact fp16
 //   O^T[dim][query] += codes_V^T . W  W = p * V scale
 // Codes become fp16 by a byte permute under the exponent of 1024 and one
@@ -35,9 +39,10 @@ using namespace bspkv;
 // are chosen so that its operands are whole 16-byte chunks: the k index of a
 // product may be permuted freely as long as both sides agree.
 constexpr int DEC_WARPS = 4;
-constexpr int SUB = 32;                  // rows of a unit that one warp takes
-constexpr int UNIT = DEC_WARPS * SUB;
-constexpr int PART_FLOATS = 4352;        // of one partial result: queries x (dims + 3), at most
+constexpr int SUB = 32;                  // rows of a sub-tile
+constexpr int OVER = 2;                  // sub-tiles a segment's start and end are worth
+constexpr int LEAST = 6;                 // a warp's run is at least this long, or joining costs more than it saves
+constexpr int RUN = 32, FILL = 16;       // entries of the run that a warp looks ahead, and fills at a time
 
 template <int DP, int NT>
 struct DecCfg {
@@ -49,11 +54,12 @@ struct DecCfg {
     static constexpr int RING = DEC_WARPS * STAGES * STAGE;
     static constexpr int Q = 8 * NT;                   // query rows of a segment
     static constexpr int OPAD = DP + 4;                // floats of a row of the joining buffer
-    static constexpr int OFF_STAT = RING;              // m, l, mw of each warp
+    static constexpr int PART = Q * (DP + 4);          // floats of a part: O, then m, l, mw of the rows
+    static constexpr int OFF_RUN = RING;               // entries of each warp's run
+    static constexpr int OFF_STAT = OFF_RUN + DEC_WARPS * RUN * 64;  // m, l, mw of each warp
     static constexpr int OFF_BAR = OFF_STAT + DEC_WARPS * Q * 3 * 4;
-    static constexpr int SMEM = OFF_BAR + DEC_WARPS * STAGES * 8 + 64 + 1024;
+    static constexpr int SMEM = OFF_BAR + DEC_WARPS * STAGES * 8 + 1024;
     static_assert(DEC_WARPS * Q * OPAD * 4 <= RING, "joining buffer in the idle ring");
-    static_assert(Q * (DP + 3) <= PART_FLOATS, "partial result");
 };
 
 struct DecodeArgs {
@@ -83,26 +89,107 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x)
 }
 
 // A request's share of the work: cached rows [lo, len) that some query sees
-// (lo rounded down to whole sub-tiles), in units; row groups of Q queries.
+// (lo rounded down to whole sub-tiles); row groups of Q queries.
 struct Share {
     Request r;
-    int seen, lo, units, groups;  // first cached row that a query sees, and the sub-tile it starts in
+    int seen, lo, subs, groups;  // first cached row that a query sees, and the sub-tile it starts in
+    __device__ int64_t cost(int heads) const { return (int64_t)groups * heads * (subs + OVER); }
 };
 
 template <int Q>
-__device__ __forceinline__ Share share_of(const DecodeArgs& d, int b)
+__device__ __forceinline__ Share share_of(const DecodeArgs& d, Request r)
 {
     const AttnArgs& a = d.a;
     Share s;
-    s.r = request_of(a.s, a.c.page_shift, b);
+    s.r = r;
     const int64_t rows = (int64_t)s.r.n * a.group;
     if (rows > d.most_rows) s.r.n = 0;
     const int first = s.r.len - s.r.n;
     s.seen = a.window ? max(0, first - a.window + 1) : 0;
     s.lo = s.seen & ~(SUB - 1);
     s.groups = s.r.n ? (int)((rows + Q - 1) / Q) : 0;
-    s.units = max(1, (s.r.len - s.lo + UNIT - 1) / UNIT);  // at least one: it writes the zeros of rows that see nothing
+    s.subs = max(1, (s.r.len - s.lo + SUB - 1) / SUB);  // at least one: it writes the zeros of rows that see nothing
     return s;
+}
+
+// One sub-tile of a warp's run (or a place that OVER reserves: tok < 0).
+struct Entry {
+    int tok, p0, p1, h;      // first row, its page and (pages of 16 rows) the next one's, KV head
+    int len, n, r0, rg;      // the request, the group of query rows
+    float ks[2], vs[2];
+    int i, subs, pad[2];     // which sub-tile of how many
+};
+static_assert(sizeof(Entry) == 64, "run entries");
+
+// The worker (warp) that has place x of the shared run.
+__device__ __forceinline__ int worker_of(int64_t x, int64_t total, int64_t P) { return (int)(((x + 1) * P - 1) / total); }
+
+// Parts of one segment: the first worker's, one of each further CTA's, and
+// the last worker's.
+struct Parts {
+    int first, last, per_cta, n;
+    __device__ Parts(int64_t x0, int subs, int64_t total, int64_t P, int wpc)
+    {
+        first = worker_of(x0, total, P);
+        last = worker_of(x0 + subs - 1, total, P);
+        per_cta = wpc;
+        n = (last - 1) / wpc - first / wpc + 2;
+    }
+    __device__ int64_t slot(int k) const
+    {
+        return k == n - 1 ? 2 * (int64_t)last + 1 : 2 * (int64_t)(k ? (first / per_cta + k) * per_cta : first);
+    }
+};
+
+// Four dims of one query row, joined: out = O 2^(mw - m) / l.
+template <class T>
+__device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int64_t head, int dim, float4 o, float top,
+                                          float topw, float sum)
+{
+    const float f = sum > 0.f ? ex2(topw - top) / sum : 0.f;
+    if (dim < a.c.dim) {
+        alignas(8) T y[4] = {from_float<T>(o.x * f), from_float<T>(o.y * f), from_float<T>(o.z * f),
+                             from_float<T>(o.w * f)};
+        *reinterpret_cast<uint2*>((T*)a.out + row * a.o_row + head * a.o_head + dim) = *reinterpret_cast<const uint2*>(y);
+    }
+    if (a.lse && dim == 0)
+        a.lse[row * a.heads + head] = sum > 0.f ? (top + __log2f(sum)) * 0.6931471805599453f : -INFINITY;
+}
+
+// The parts of a segment, joined by `threads` threads.
+template <class T, int DP, int NT>
+__device__ __forceinline__ void join_parts(const DecodeArgs& d, const Parts& ps, const Entry& e, int tid, int threads)
+{
+    using C = DecCfg<DP, NT>;
+    constexpr int Q = C::Q;
+    const AttnArgs& a = d.a;
+    for (int i = tid; i < Q * (DP / 4); i += threads) {
+        const int qr = i / (DP / 4), dim = i % (DP / 4) * 4;
+        const int r = e.rg * Q + qr;
+        if (r >= e.n * a.group) continue;
+        float top = NONE, topw = NONE;
+#pragma unroll 4
+        for (int k = 0; k < ps.n; ++k) {
+            const float* st = d.parts + ps.slot(k) * C::PART + Q * DP + qr;
+            top = fmaxf(top, __ldcg(st));
+            topw = fmaxf(topw, __ldcg(st + 2 * Q));
+        }
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < ps.n; ++k) {
+            const float* from = d.parts + ps.slot(k) * C::PART;
+            const float* st = from + Q * DP + qr;
+            sum += __ldcg(st + Q) * ex2(__ldcg(st) - top);
+            const float f = ex2(__ldcg(st + 2 * Q) - topw);
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(from + qr * DP + dim));
+            o.x += y.x * f;
+            o.y += y.y * f;
+            o.z += y.z * f;
+            o.w += y.w * f;
+        }
+        store_out<T>(a, e.r0 + r / a.group, e.h * a.group + r % a.group, dim, o, top, topw, sum);
+    }
 }
 
 template <class T, int DP, int NT>
@@ -119,8 +206,36 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const int H = a.c.heads, B = a.s.batch, sh = a.c.page_shift;
     float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT);  // [warp][3][Q]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * C::STAGES;
-    int* note = reinterpret_cast<int*>(smem + C::OFF_BAR + DEC_WARPS * C::STAGES * 8);
     uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
+    Entry* run = reinterpret_cast<Entry*>(smem + C::OFF_RUN) + warp * RUN;
+
+    // the shared run: each thread sums some requests; pre[i] is what comes
+    // before thread i's
+    __shared__ int64_t pre[DEC_WARPS * 32 + 1];
+    __shared__ int64_t sums[DEC_WARPS];
+    const int per = (B + DEC_WARPS * 32 - 1) / (DEC_WARPS * 32);
+    int64_t upto = 0;
+    for (int b = min(B, tid * per); b < min(B, (tid + 1) * per); ++b)
+        upto += share_of<Q>(d, request_of(a.s, sh, b)).cost(H);
+    const int64_t mine = upto;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+        const int64_t o = __shfl_up_sync(FULL, upto, i);
+        if (lane >= i) upto += o;
+    }
+    if (lane == 31) sums[warp] = upto;
+    if (lane < C::STAGES) bspx::mbar_init(full + lane, 1);
+    bspx::fence_mbar_init();
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < DEC_WARPS; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
+    }
+    pre[tid] = upto - mine;
+    if (tid == 0) pre[DEC_WARPS * 32] = total;
+    __syncthreads();
 
     // rows past the step's
     {
@@ -133,505 +248,507 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
     }
 
-    // this CTA's range of units: each thread sums a run of requests, and the
-    // one whose run holds the first unit says where it is
-    __shared__ int64_t scan[DEC_WARPS];
-    const int per = (B + DEC_WARPS * 32 - 1) / (DEC_WARPS * 32);
-    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) {
-        const Share s = share_of<Q>(d, b);
-        sum += (int64_t)s.units * s.groups * H;
-    }
-    int64_t upto = sum;
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) {
-        const int64_t o = __shfl_up_sync(FULL, upto, i);
-        if (lane >= i) upto += o;
-    }
-    if (lane == 31) scan[warp] = upto;
-    if (lane < C::STAGES) bspx::mbar_init(full + lane, 1);
-    bspx::fence_mbar_init();
-    __syncthreads();
-    int64_t total = 0;
-#pragma unroll
-    for (int w = 0; w < DEC_WARPS; ++w) {
-        if (w < warp) upto += scan[w];
-        total += scan[w];
-    }
-    const int64_t P = min((int64_t)gridDim.x, total);  // CTAs that have work
-    if ((int64_t)blockIdx.x >= P) return;
-    const int64_t u0 = total * blockIdx.x / P, u1 = total * (blockIdx.x + 1) / P;
-    if (upto - sum <= u0 && u0 < upto) {
-        int64_t at = upto - sum;
-        for (int b = b0; b < b1; ++b) {
-            const Share s = share_of<Q>(d, b);
-            const int64_t n = (int64_t)s.units * s.groups * H;
-            if (u0 < at + n) {
-                note[0] = b;
-                *reinterpret_cast<int64_t*>(note + 2) = u0 - at;
-                break;
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
-    int b = note[0];
-    int64_t off = *reinterpret_cast<int64_t*>(note + 2);  // unit within the request
-    uint32_t stage = 0, phase = 0;
-    uint32_t fill = 0;                                    // stage of the next load
-    bool failed = false;
+    // P workers; fewer than there are warps are spread over the CTAs
+    const int64_t P = max((int64_t)1, min((int64_t)gridDim.x * DEC_WARPS, total / LEAST));
+    const int wpc = (int)min((int64_t)DEC_WARPS, (P + gridDim.x - 1) / gridDim.x);
+    const int worker = blockIdx.x * wpc + warp;
+    const bool works = total > 0 && warp < wpc && worker < P;
+    const int64_t x0 = works ? total * worker / P : 0;
+    const int N = works ? (int)(total * (worker + 1) / P - x0) : 0;
 
-    for (int64_t u = u0; u < u1;) {
-        Share s = share_of<Q>(d, b);
-        while (off >= (int64_t)s.units * s.groups * H) {  // next request with work
-            off -= (int64_t)s.units * s.groups * H;
-            s = share_of<Q>(d, ++b);
+    // requests 32 at a time, one per lane: what lies before them, and up to
+    // each lane's end
+    int bw = 0;
+    int64_t before = 0, ends = 0;
+    Share sr = {};
+    auto requests = [&](int from, int64_t at) {
+        bw = from;
+        before = at;
+        Request r = {0, 0, 0};
+        if (bw + lane < B) r = request_of(a.s, sh, bw + lane);
+        sr = share_of<Q>(d, r);
+        ends = bw + lane < B ? sr.cost(H) : 0;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t o = __shfl_up_sync(FULL, ends, i);
+            if (lane >= i) ends += o;
         }
-        const int64_t seg = off / s.units;
-        const int t0 = (int)(off - seg * s.units), n_units = (int)min((int64_t)(s.units - t0), u1 - u);
-        const int h = (int)(seg / s.groups), rg = (int)(seg - (int64_t)h * s.groups);
-        const int first = s.r.len - s.r.n, rows = s.r.n * a.group;
-        const int32_t* table = a.s.table + (int64_t)b * a.s.table_stride;
-        const int tok0 = s.lo + t0 * UNIT + warp * SUB;  // this warp's first row; the next ones are UNIT apart
-
-        // queries: a thread's chunks of its row, the scale of its columns' logits
-        uint32_t qf[NT][CH][8];
-        float qs[NT][2];
-        int pos[NT][2];  // positions of the columns' queries
+        ends += before;
+    };
+    int filled = 0;
+    auto fill = [&]() {  // the next FILL entries of the run
+        const int64_t x = x0 + filled + lane;
+        bool todo = lane < FILL && filled + lane < N;
+        Entry e;
+        e.tok = e.p0 = e.p1 = -1;
+        e.ks[0] = e.ks[1] = e.vs[0] = e.vs[1] = 0.f;
+        while (true) {
+            const int64_t window_end = __shfl_sync(FULL, ends, 31);
+            const bool here = todo && x < window_end;
+            int r = 0;  // the first lane whose requests end beyond x
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = rg * Q + nt * 8 + g;
-            float top = 0.f, x[CH][16];
-#pragma unroll
-            for (int j = 0; j < CH; ++j) {
-                const int ch = DP == 64 ? c : 8 * (j >> 1) + 2 * c + (j & 1);
-                if (r < rows && ch * 16 < a.c.dim) {
-                    const T* q = (const T*)a.q + (int64_t)(s.r.r0 + r / a.group) * a.q_row +
-                                 (int64_t)(h * a.group + r % a.group) * a.q_head + ch * 16;
-                    const uint4 v0 = *reinterpret_cast<const uint4*>(q), v1 = *reinterpret_cast<const uint4*>(q + 8);
-                    const T* e0 = reinterpret_cast<const T*>(&v0);
-                    const T* e1 = reinterpret_cast<const T*>(&v1);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[j][e] = to_float(e0[e]);
-                        x[j][8 + e] = to_float(e1[e]);
+            for (int i = 16; i; i >>= 1)
+                if (__shfl_sync(FULL, ends, r + i - 1) <= x) r += i;
+            r = min(r, 31);
+            const int64_t end = __shfl_sync(FULL, ends, r);
+            const int len = __shfl_sync(FULL, sr.r.len, r), n = __shfl_sync(FULL, sr.r.n, r);
+            const int r0 = __shfl_sync(FULL, sr.r.r0, r), lo = __shfl_sync(FULL, sr.lo, r);
+            const int seen = __shfl_sync(FULL, sr.seen, r), subs = __shfl_sync(FULL, sr.subs, r);
+            const int groups = __shfl_sync(FULL, sr.groups, r);
+            if (here) {
+                const int64_t off = x - (end - (int64_t)groups * H * (subs + OVER));
+                const int64_t seg = off / (subs + OVER);
+                e.i = (int)(off - seg * (subs + OVER)) - OVER;
+                e.subs = subs;
+                e.h = (int)(seg / groups);
+                e.rg = (int)(seg - (int64_t)e.h * groups);
+                e.len = len;
+                e.n = n;
+                e.r0 = r0;
+                if (e.i >= 0) {
+                    e.tok = lo + e.i * SUB;
+                    const int32_t* table = a.s.table + (int64_t)(bw + r) * a.s.table_stride;
+                    if (e.tok < len && ((e.tok >> sh) + 1) << sh > seen) e.p0 = table[e.tok >> sh];
+                    if (sh == 4 && e.tok + 16 < len && e.tok + 32 > seen) e.p1 = table[(e.tok >> 4) + 1];
+                    if (e.p0 >= a.c.pages) e.p0 = -1;
+                    if (e.p1 >= a.c.pages) e.p1 = -1;
+                    if (sh != 4) e.p1 = e.p0;
+                    if (e.p0 >= 0) {
+                        e.ks[0] = a.c.k_scale[(int64_t)e.p0 * a.c.scale_stride + e.h];
+                        e.vs[0] = a.c.v_scale[(int64_t)e.p0 * a.c.scale_stride + e.h];
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[j][e] = 0.f;
+                    if (e.p1 >= 0) {
+                        e.ks[1] = a.c.k_scale[(int64_t)e.p1 * a.c.scale_stride + e.h];
+                        e.vs[1] = a.c.v_scale[(int64_t)e.p1 * a.c.scale_stride + e.h];
+                    }
                 }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[j][e]));
+                todo = false;
             }
-            // bfloat16 rows are brought into fp16's range by a power of two
-            // (exact but for values 2^-24 below the row's largest)
-            float unit = 1.f;
-            if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
-                top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
-                const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
-                unit = __uint_as_float(e << 23);
-                const float inv = __uint_as_float((254u - e) << 23);
-#pragma unroll
-                for (int j = 0; j < CH; ++j)
-#pragma unroll
-                    for (int e2 = 0; e2 < 16; ++e2) x[j][e2] *= inv;
-            }
-#pragma unroll
-            for (int j = 0; j < CH; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) qf[nt][j][e] = h2bits(__floats2half2_rn(x[j][2 * e], x[j][2 * e + 1]));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                qs[nt][e] = __shfl_sync(FULL, unit, (2 * c + e) * 4) * (a.scale * 1.4426950408889634f);
-                pos[nt][e] = first + (rg * Q + nt * 8 + 2 * c + e) / a.group;
-            }
+            if (!__any_sync(FULL, todo) || bw + 32 >= B) break;
+            requests(bw + 32, window_end);
         }
+        __syncwarp();
+        if (lane < FILL && filled + lane < N) run[(filled + lane) % RUN] = e;
+        __syncwarp();
+        filled += FILL;
+    };
+    if (works) {
+        int from = 0;
+        for (int i = lane; i < DEC_WARPS * 32; i += 32) {
+            const uint32_t hit = __ballot_sync(FULL, pre[i] <= x0 && x0 < pre[i + 1]);
+            if (hit) from = (i - lane) + __ffs(hit) - 1;
+        }
+        requests(from * per, pre[from]);
+        fill();
+        if (filled < N) fill();
+    }
 
-        float acc[MT][NT][4];
-        float m[NT][2], mw[NT][2], l[NT][2], lift[NT][2];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[nt][e] = mw[nt][e] = NONE;
-                l[nt][e] = 0.f;
-                lift[nt][e] = LIFT;
-            }
-
-        // pages and scales of this warp's next 32 sub-tiles, one per lane
-        // (two pages where a page holds 16 rows); -1: nothing to see there
-        int pg[2], npg[2];
-        float ks[2], vs[2];
-        auto pages_from = [&](int k, int (&p)[2]) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tok = tok0 + (k + lane) * UNIT + 16 * i;
-                p[i] = -1;
-                if (k + lane < n_units && tok < s.r.len && ((tok >> sh) + 1) << sh > s.seen) {
-                    const int v = table[tok >> sh];
-                    if (v >= 0 && v < a.c.pages) p[i] = v;
-                }
-            }
-        };
-        auto issue = [&](int k, int p0, int p1) {  // loads of sub-tile k into the next free stage
+    uint32_t stage = 0, phase = 0, next = 0;  // ring: stage being read, stage of the next load
+    int ahead = 0, loading = 0;               // entries looked at for loading; loads in flight
+    bool failed = false;
+    auto load = [&]() {
+        while (ahead < min(N, filled) && loading < C::STAGES) {
+            const Entry& e = run[ahead % RUN];
+            ++ahead;
+            if (e.tok < 0) continue;
             if (lane == 0) {
-                uint8_t* st = ring + fill * C::STAGE;
-                const bool two = sh == 4;
-                const uint32_t bytes = two ? ((p0 >= 0) + (p1 >= 0)) * 32u * DP : (p0 >= 0 ? 64u * DP : 0u);
-                if (bytes) bspx::mbar_arrive_expect_tx(full + fill, bytes);
-                else bspx::mbar_arrive(full + fill);
-                const int row = (tok0 + k * UNIT) & ((1 << sh) - 1);
+                uint8_t* st = ring + next * C::STAGE;
+                const int p0 = e.p0, p1 = sh == 4 ? e.p1 : -1;
+                const uint32_t rows = sh == 4 ? 16 * ((p0 >= 0) + (p1 >= 0)) : p0 >= 0 ? SUB : 0;
+                if (rows) bspx::mbar_arrive_expect_tx(full + next, rows * 2 * DP);
+                else bspx::mbar_arrive(full + next);
+                const int row = sh == 4 ? 0 : e.tok & ((1 << sh) - 1);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int p = i ? p1 : p0;
-                    if (p < 0 || (i && !two)) continue;
+                    if (p < 0) continue;
 #pragma unroll
                     for (int rgn = 0; rgn < C::REGIONS; ++rgn) {
                         uint8_t* to = st + rgn * SUB * C::BOX + i * 16 * C::BOX;
-                        tma_load_4d(to, &map_k, rgn * 128, two ? 0 : row, h, p, full + fill);
-                        tma_load_4d(to + C::HALF, &map_v, rgn * 128, two ? 0 : row, h, p, full + fill);
+                        tma_load_4d(to, &map_k, rgn * 128, row, e.h, p, full + next);
+                        tma_load_4d(to + C::HALF, &map_v, rgn * 128, row, e.h, p, full + next);
                     }
                 }
             }
-            __syncwarp();
-            if (++fill == C::STAGES) fill = 0;
-        };
-        pages_from(0, pg);
-        pages_from(32, npg);
-        auto scales = [&]() {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ks[i] = vs[i] = 0.f;
-                if (pg[i] >= 0) {
-                    ks[i] = a.c.k_scale[(int64_t)pg[i] * a.c.scale_stride + h];
-                    vs[i] = a.c.v_scale[(int64_t)pg[i] * a.c.scale_stride + h];
-                }
-            }
-        };
-        int issued = 0;
-        auto issue_next = [&](int k) {  // k: the sub-tile being worked on
-            const int w = issued - (k & ~31);
-            const int p0 = __shfl_sync(FULL, w < 32 ? pg[0] : npg[0], w & 31);
-            const int p1 = __shfl_sync(FULL, w < 32 ? pg[1] : npg[1], w & 31);
-            issue(issued, p0, p1);
-            ++issued;
-        };
-        while (issued < n_units && issued < C::STAGES) issue_next(0);
-        scales();
+            ++loading;
+            if (++next == C::STAGES) next = 0;
+        }
+        __syncwarp();
+    };
+    load();
 
-        for (int k = 0; k < n_units; ++k) {
-            if (k && (k & 31) == 0) {
-                pg[0] = npg[0];
-                pg[1] = npg[1];
-                pages_from(k + 32, npg);
-                scales();
+    // the segment being worked on
+    uint32_t qf[NT][CH][8];   // queries: a thread's chunks of its row
+    float qs[NT][2];          // scale of its columns' logits
+    int pos[NT][2];           // positions of the columns' queries
+    float acc[MT][NT][4];
+    float m[NT][2], mw[NT][2], l[NT][2], lift[NT][2];
+    bool open = false;        // a segment that goes on in the next worker's run
+    int begun = 0;            // its first sub-tile here
+    int last_at = 0;          // the place of its last entry here
+
+    for (int k = 0; k < N; ++k) {
+        if (filled < N && filled - k <= RUN - FILL) {
+            fill();
+            load();
+        }
+        const Entry& e = run[k % RUN];
+        const int tok = e.tok;
+        if (tok < 0) continue;
+        const int first = e.len - e.n, rows = e.n * a.group;
+        if (!open) {
+            open = true;
+            begun = e.i;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = e.rg * Q + nt * 8 + g;
+                float top = 0.f, x[CH][16];
+#pragma unroll
+                for (int j = 0; j < CH; ++j) {
+                    const int ch = DP == 64 ? c : 8 * (j >> 1) + 2 * c + (j & 1);
+                    if (r < rows && ch * 16 < a.c.dim) {
+                        const T* q = (const T*)a.q + (int64_t)(e.r0 + r / a.group) * a.q_row +
+                                     (int64_t)(e.h * a.group + r % a.group) * a.q_head + ch * 16;
+                        const uint4 v0 = *reinterpret_cast<const uint4*>(q), v1 = *reinterpret_cast<const uint4*>(q + 8);
+                        const T* e0 = reinterpret_cast<const T*>(&v0);
+                        const T* e1 = reinterpret_cast<const T*>(&v1);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) {
+                            x[j][y] = to_float(e0[y]);
+                            x[j][8 + y] = to_float(e1[y]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) x[j][y] = 0.f;
+                    }
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) top = fmaxf(top, fabsf(x[j][y]));
+                }
+                // bfloat16 rows are brought into fp16's range by a power of
+                // two (exact but for values 2^-24 below the row's largest)
+                float unit = 1.f;
+                if constexpr (!std::is_same<T, __half>::value) {
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(FULL, top, 2));
+                    const uint32_t ex = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+                    unit = __uint_as_float(ex << 23);
+                    const float inv = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+                    for (int j = 0; j < CH; ++j)
+#pragma unroll
+                        for (int y = 0; y < 16; ++y) x[j][y] *= inv;
+                }
+#pragma unroll
+                for (int j = 0; j < CH; ++j)
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) qf[nt][j][y] = h2bits(__floats2half2_rn(x[j][2 * y], x[j][2 * y + 1]));
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    qs[nt][y] = __shfl_sync(FULL, unit, (2 * c + y) * 4) * (a.scale * 1.4426950408889634f);
+                    pos[nt][y] = first + (e.rg * Q + nt * 8 + 2 * c + y) / a.group;
+                    m[nt][y] = mw[nt][y] = NONE;
+                    l[nt][y] = 0.f;
+                    lift[nt][y] = LIFT;
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) acc[i][nt][y] = 0.f;
             }
-            const int tok = tok0 + k * UNIT;
-            const int p0 = __shfl_sync(FULL, pg[0], k & 31), p1 = __shfl_sync(FULL, pg[1], k & 31);
-            float kscale[2], vscale[2];
+        }
+
+        if (!bspx::mbar_wait_bounded(full + stage, phase, failed ? 1u : d.spin_cap)) failed = true;
+        failed = __any_sync(FULL, failed);
+        const uint8_t* kt = ring + stage * C::STAGE;
+        const uint8_t* vt = kt + C::HALF;
+        const int p0 = e.p0, p1 = e.p1;
+        if (p0 >= 0 || p1 >= 0) {
+            const float kscale[2] = {e.ks[0], e.ks[1]}, vscale[2] = {e.vs[0], e.vs[1]};
+            // S^T
+            float sc[2][NT][4];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                kscale[i] = __shfl_sync(FULL, ks[i], k & 31);
-                vscale[i] = __shfl_sync(FULL, vs[i], k & 31);
-            }
-            if (!bspx::mbar_wait_bounded(full + stage, phase, failed ? 1u : d.spin_cap)) failed = true;
-            failed = __any_sync(FULL, failed);
-            const uint8_t* kt = ring + stage * C::STAGE;
-            const uint8_t* vt = kt + C::HALF;
-            if (p0 >= 0 || p1 >= 0) {
-                // S^T
-                float sc[2][NT][4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sc[i][nt][e] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) {
-                        const int ch = DP == 64 ? c : 2 * c + (j & 1);
-                        const int r0 = 16 * i + g, r1 = r0 + 8;
-                        const int sw0 = DP == 64 ? (r0 >> 1) & 3 : r0 & 7, sw1 = DP == 64 ? (r1 >> 1) & 3 : r1 & 7;
-                        const uint8_t* reg = kt + (j >> 1) * SUB * C::BOX;
-                        const uint4 w0 = *reinterpret_cast<const uint4*>(reg + r0 * C::BOX + ((ch ^ sw0) << 4));
-                        const uint4 w1 = *reinterpret_cast<const uint4*>(reg + r1 * C::BOX + ((ch ^ sw1) << 4));
-                        const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t y0 = x0[w] ^ 0x80808080u, y1 = x1[w] ^ 0x80808080u;
-                            const uint32_t a0 = widen(y0, 0x4140), a2 = widen(y0, 0x4342);
-                            const uint32_t a1 = widen(y1, 0x4140), a3 = widen(y1, 0x4342);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma16816(sc[i][nt], a0, a1, a2, a3, qf[nt][j][2 * w], qf[nt][j][2 * w + 1]);
-                        }
-                    }
-                }
-                // logits (in powers of two), masked where a query does not see the row
-                const bool edge = tok + SUB - 1 > first || (a.window && tok <= s.r.len - 1 - a.window) || p0 < 0 ||
-                                  (sh == 4 && p1 < 0);
-                float lv[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const bool there = sh == 4 ? (i ? p1 : p0) >= 0 : p0 >= 0;
-                    lv[i] = vscale[i] != 0.f ? __log2f(fabsf(vscale[i])) : NONE;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float x = sc[i][nt][e] * (kscale[i] * qs[nt][e & 1]);
-                            if (edge) {
-                                const int j = tok + 16 * i + g + (e >> 1) * 8, p = pos[nt][e & 1];
-                                if (!there || j > p || (a.window && j <= p - a.window)) x = -INFINITY;
-                            }
-                            sc[i][nt][e] = x;
-                        }
-                }
-                // running maxima, allowed to lag
-                bool lag = false;
-                float hi[NT][2][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int y = 0; y < 4; ++y) sc[i][nt][y] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) hi[nt][e][i] = fmaxf(sc[i][nt][e], sc[i][nt][e + 2]);
-                        lag |= fmaxf(hi[nt][e][0], hi[nt][e][1]) > m[nt][e] + LAZY;
-                        lag |= fmaxf(hi[nt][e][0] + lv[0], hi[nt][e][1] + lv[1]) > mw[nt][e] + LAZY;
-                    }
-                if (__any_sync(FULL, lag)) {
+                for (int j = 0; j < CH; ++j) {
+                    const int ch = DP == 64 ? c : 2 * c + (j & 1);
+                    const int r0 = 16 * i + g, r1 = r0 + 8;
+                    const int sw0 = DP == 64 ? (r0 >> 1) & 3 : r0 & 7, sw1 = DP == 64 ? (r1 >> 1) & 3 : r1 & 7;
+                    const uint8_t* reg = kt + (j >> 1) * SUB * C::BOX;
+                    const uint4 w0 = *reinterpret_cast<const uint4*>(reg + r0 * C::BOX + ((ch ^ sw0) << 4));
+                    const uint4 w1 = *reinterpret_cast<const uint4*>(reg + r1 * C::BOX + ((ch ^ sw1) << 4));
+                    const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t y0 = x0[w] ^ 0x80808080u, y1 = x1[w] ^ 0x80808080u;
+                        const uint32_t a0 = widen(y0, 0x4140), a2 = widen(y0, 0x4342);
+                        const uint32_t a1 = widen(y1, 0x4140), a3 = widen(y1, 0x4342);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float t = fmaxf(hi[nt][e][0], hi[nt][e][1]);
-                            float tw = fmaxf(hi[nt][e][0] + lv[0], hi[nt][e][1] + lv[1]);
-#pragma unroll
-                            for (int x = 4; x < 32; x <<= 1) {
-                                t = fmaxf(t, __shfl_xor_sync(FULL, t, x));
-                                tw = fmaxf(tw, __shfl_xor_sync(FULL, tw, x));
-                            }
-                            t = fmaxf(t, m[nt][e]);
-                            tw = fmaxf(tw, mw[nt][e]);
-                            l[nt][e] *= ex2(m[nt][e] - t);
-                            const float back = ex2(mw[nt][e] - tw);
-#pragma unroll
-                            for (int i = 0; i < MT; ++i) {
-                                acc[i][nt][e] *= back;
-                                acc[i][nt][e + 2] *= back;
-                            }
-                            m[nt][e] = t;
-                            mw[nt][e] = tw;
-                            lift[nt][e] = ex2(fminf(t - tw, 120.f)) * LIFT;
-                        }
-                }
-                // weights, as the B operand of the second product
-                uint32_t wf[2][NT][2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float p[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            p[e] = ex2(sc[i][nt][e] - m[nt][e & 1]);
-                            l[nt][e & 1] += p[e];
-                            p[e] *= lift[nt][e & 1] * vscale[i];
-                        }
-                        wf[i][nt][0] = movmatrix(h2bits(__floats2half2_rn(p[0], p[1])));
-                        wf[i][nt][1] = movmatrix(h2bits(__floats2half2_rn(p[2], p[3])));
-                    }
-                // O^T
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = 16 * i + 2 * c;
-#pragma unroll
-                    for (int rgn = 0; rgn < C::REGIONS; ++rgn) {
-                        constexpr int WORDS = DP == 64 ? 2 : 4;  // of each row, a thread's dims
-                        uint32_t t[4][4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const int row = r + (x & 1) + 8 * (x >> 1);
-                            const uint8_t* base = vt + rgn * SUB * C::BOX + row * C::BOX;
-                            if constexpr (DP == 64) {
-                                const uint2 v = *reinterpret_cast<const uint2*>(
-                                    base + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
-                                t[x][0] = v.x ^ 0x80808080u;
-                                t[x][1] = v.y ^ 0x80808080u;
-                            } else {
-                                const uint4 v = *reinterpret_cast<const uint4*>(base + ((g ^ (row & 7)) << 4));
-                                t[x][0] = v.x ^ 0x80808080u;
-                                t[x][1] = v.y ^ 0x80808080u;
-                                t[x][2] = v.z ^ 0x80808080u;
-                                t[x][3] = v.w ^ 0x80808080u;
-                            }
-                        }
-#pragma unroll
-                        for (int w = 0; w < WORDS; ++w)
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const uint32_t sel = half ? 0x7362 : 0x5140;
-                                const uint32_t z0 = __byte_perm(t[0][w], t[1][w], sel);
-                                const uint32_t z1 = __byte_perm(t[2][w], t[3][w], sel);
-                                const uint32_t a0 = widen(z0, 0x4140), a1 = widen(z0, 0x4342);
-                                const uint32_t a2 = widen(z1, 0x4140), a3 = widen(z1, 0x4342);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma16816(acc[rgn * 8 + 2 * w + half][nt], a0, a1, a2, a3, wf[i][nt][0],
-                                             wf[i][nt][1]);
-                            }
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816(sc[i][nt], a0, a1, a2, a3, qf[nt][j][2 * w], qf[nt][j][2 * w + 1]);
                     }
                 }
             }
-            __syncwarp();  // the stage is read: it may be filled again
-            if (++stage == C::STAGES) {
-                stage = 0;
-                phase ^= 1u;
+            // logits (in powers of two), masked where a query does not see the row
+            const bool edge = tok + SUB - 1 > first || (a.window && tok <= e.len - 1 - a.window) || p0 < 0 || p1 < 0;
+            float lv[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool there = (i ? p1 : p0) >= 0;
+                lv[i] = vscale[i] != 0.f ? __log2f(fabsf(vscale[i])) : NONE;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        float x = sc[i][nt][y] * (kscale[i] * qs[nt][y & 1]);
+                        if (edge) {
+                            const int j = tok + 16 * i + g + (y >> 1) * 8, p = pos[nt][y & 1];
+                            if (!there || j > p || (a.window && j <= p - a.window)) x = -INFINITY;
+                        }
+                        sc[i][nt][y] = x;
+                    }
             }
-            if (issued < n_units) issue_next(k);
+            // running maxima, allowed to lag
+            bool lag = false;
+            float hi[NT][2][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) hi[nt][y][i] = fmaxf(sc[i][nt][y], sc[i][nt][y + 2]);
+                    lag |= fmaxf(hi[nt][y][0], hi[nt][y][1]) > m[nt][y] + LAZY;
+                    lag |= fmaxf(hi[nt][y][0] + lv[0], hi[nt][y][1] + lv[1]) > mw[nt][y] + LAZY;
+                }
+            if (__any_sync(FULL, lag)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float t = fmaxf(hi[nt][y][0], hi[nt][y][1]);
+                        float tw = fmaxf(hi[nt][y][0] + lv[0], hi[nt][y][1] + lv[1]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) {
+                            t = fmaxf(t, __shfl_xor_sync(FULL, t, x));
+                            tw = fmaxf(tw, __shfl_xor_sync(FULL, tw, x));
+                        }
+                        t = fmaxf(t, m[nt][y]);
+                        tw = fmaxf(tw, mw[nt][y]);
+                        l[nt][y] *= ex2(m[nt][y] - t);
+                        const float back = ex2(mw[nt][y] - tw);
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            acc[i][nt][y] *= back;
+                            acc[i][nt][y + 2] *= back;
+                        }
+                        m[nt][y] = t;
+                        mw[nt][y] = tw;
+                        lift[nt][y] = ex2(fminf(t - tw, 120.f)) * LIFT;
+                    }
+            }
+            // weights, as the B operand of the second product
+            uint32_t wf[2][NT][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float p[4];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        p[y] = ex2(sc[i][nt][y] - m[nt][y & 1]);
+                        l[nt][y & 1] += p[y];
+                        p[y] *= lift[nt][y & 1] * vscale[i];
+                    }
+                    wf[i][nt][0] = movmatrix(h2bits(__floats2half2_rn(p[0], p[1])));
+                    wf[i][nt][1] = movmatrix(h2bits(__floats2half2_rn(p[2], p[3])));
+                }
+            // O^T
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 16 * i + 2 * c;
+#pragma unroll
+                for (int rgn = 0; rgn < C::REGIONS; ++rgn) {
+                    constexpr int WORDS = DP == 64 ? 2 : 4;  // of each row, a thread's dims
+                    uint32_t t[4][4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int row = r + (x & 1) + 8 * (x >> 1);
+                        const uint8_t* base = vt + rgn * SUB * C::BOX + row * C::BOX;
+                        if constexpr (DP == 64) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(
+                                base + (((g >> 1) ^ ((row >> 1) & 3)) << 4) + (g & 1) * 8);
+                            t[x][0] = v.x ^ 0x80808080u;
+                            t[x][1] = v.y ^ 0x80808080u;
+                        } else {
+                            const uint4 v = *reinterpret_cast<const uint4*>(base + ((g ^ (row & 7)) << 4));
+                            t[x][0] = v.x ^ 0x80808080u;
+                            t[x][1] = v.y ^ 0x80808080u;
+                            t[x][2] = v.z ^ 0x80808080u;
+                            t[x][3] = v.w ^ 0x80808080u;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < WORDS; ++w)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t sel = half ? 0x7362 : 0x5140;
+                            const uint32_t z0 = __byte_perm(t[0][w], t[1][w], sel);
+                            const uint32_t z1 = __byte_perm(t[2][w], t[3][w], sel);
+                            const uint32_t a0 = widen(z0, 0x4140), a1 = widen(z0, 0x4342);
+                            const uint32_t a2 = widen(z1, 0x4140), a3 = widen(z1, 0x4342);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(acc[rgn * 8 + 2 * w + half][nt], a0, a1, a2, a3, wf[i][nt][0], wf[i][nt][1]);
+                        }
+                }
+            }
         }
+        __syncwarp();  // the stage is read: it may be filled again
+        if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        --loading;
+        load();
+        last_at = k;
+        if (e.i + 1 < e.subs) continue;
 
-        // the warps' sums meet in shared memory (the ring is idle)
+        // the segment ends here: its rows out, or the last part of it
+        open = false;
+        const bool whole = begun == 0;
+        float* part = d.parts + (2 * (int64_t)worker + 1) * C::PART;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int y = 0; y < 2; ++y) {
+                float sum = l[nt][y];
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) l[nt][e] += __shfl_xor_sync(FULL, l[nt][e], x);
-                if (g == 0) {
-                    float* st = stat + warp * 3 * Q + nt * 8 + 2 * c + e;
-                    st[0] = m[nt][e];
-                    st[Q] = l[nt][e];
-                    st[2 * Q] = mw[nt][e];
+                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(FULL, sum, x);
+                const int qr = nt * 8 + 2 * c + y, r = e.rg * Q + qr;
+                const int64_t row = e.r0 + r / a.group, head = e.h * a.group + r % a.group;
+#pragma unroll
+                for (int i = 0; i < MT; i += 2) {
+                    const int dim = DP == 64 ? g * 8 + 2 * i : (i >> 3) * 128 + g * 16 + 2 * (i & 7);
+                    constexpr float f = 1.f / LIFT;
+                    const float4 o = make_float4(acc[i][nt][y] * f, acc[i][nt][y + 2] * f, acc[i + 1][nt][y] * f,
+                                                 acc[i + 1][nt][y + 2] * f);
+                    if (!whole) *reinterpret_cast<float4*>(part + qr * DP + dim) = o;
+                    else if (r < rows) store_out<T>(a, row, head, dim, o, m[nt][y], mw[nt][y], sum);
+                }
+                if (!whole && g == 0) {
+                    part[Q * DP + qr] = m[nt][y];
+                    part[Q * DP + Q + qr] = sum;
+                    part[Q * DP + 2 * Q + qr] = mw[nt][y];
                 }
             }
-        __syncthreads();
-        float* join = reinterpret_cast<float*>(smem);  // [warp][Q][OPAD]
+        if (!whole) {
+            const Parts ps(x0 + k - e.i, e.subs, total, P, wpc);
+            __threadfence();
+            __syncwarp();
+            int n = 0;
+            if (lane == 0) n = atomicAdd(d.arrivals + ps.first, 1);
+            n = __shfl_sync(FULL, n, 0);
+            if (n == ps.n - 1) {
+                if (lane == 0) d.arrivals[ps.first] = 0;
+                __threadfence();
+                join_parts<T, DP, NT>(d, ps, e, lane, 32);
+            }
+        }
+    }
+    if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
+
+    // Segments that go on beyond the warps' runs.  The warps of a CTA that
+    // are on the same one add their sums in shared memory (the ring is idle).
+    __shared__ int64_t seg_at[DEC_WARPS];  // place of the segment's first sub-tile, -1: none
+    __shared__ Entry seg_entry[DEC_WARPS];
+    __shared__ int arrived;
+    if (lane == 0) {
+        seg_at[warp] = -1;
+        if (open) {
+            seg_entry[warp] = run[last_at % RUN];
+            seg_at[warp] = x0 + last_at - seg_entry[warp].i;
+        }
+    }
+    if (open)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int qr = nt * 8 + 2 * c + e;
-                float top = NONE;
+            for (int y = 0; y < 2; ++y) {
+                float sum = l[nt][y];
 #pragma unroll
-                for (int w = 0; w < DEC_WARPS; ++w) top = fmaxf(top, stat[w * 3 * Q + 2 * Q + qr]);
-                const float f = ex2(mw[nt][e] - top) * (1.f / LIFT);
+                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(FULL, sum, x);
+                if (g == 0) {
+                    float* st = stat + warp * 3 * Q + nt * 8 + 2 * c + y;
+                    st[0] = m[nt][y];
+                    st[Q] = sum;
+                    st[2 * Q] = mw[nt][y];
+                }
+            }
+    __syncthreads();
+    float* join = reinterpret_cast<float*>(smem);  // [warp][Q][OPAD]
+    if (open)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int qr = nt * 8 + 2 * c + y;
+                float top = NONE;
+                for (int w = 0; w < DEC_WARPS; ++w)
+                    if (seg_at[w] == seg_at[warp]) top = fmaxf(top, stat[w * 3 * Q + 2 * Q + qr]);
+                const float f = ex2(mw[nt][y] - top) * (1.f / LIFT);
                 float* o = join + (warp * Q + qr) * C::OPAD;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     const int dim = DP == 64 ? g * 8 + 2 * i : (i >> 3) * 128 + g * 16 + 2 * (i & 7);
-                    *reinterpret_cast<float2*>(o + dim) = make_float2(acc[i][nt][e] * f, acc[i][nt][e + 2] * f);
+                    *reinterpret_cast<float2*>(o + dim) = make_float2(acc[i][nt][y] * f, acc[i][nt][y + 2] * f);
                 }
             }
-        __syncthreads();
-        const int64_t seg_u0 = u - t0;                         // first unit of the segment, of all
-        const int64_t c0 = ((seg_u0 + 1) * P - 1) / total, c1 = ((seg_u0 + s.units) * P - 1) / total;  // its CTAs
-        const bool whole = c0 == c1;
-        float* part = d.parts + (2 * (int64_t)blockIdx.x + (t0 ? 0 : 1)) * PART_FLOATS;  // begun earlier, or here
-        for (int i = tid; i < Q * (DP / 4); i += DEC_WARPS * 32) {
-            const int qr = i / (DP / 4), dim = i % (DP / 4) * 4;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float top = NONE, lsum = 0.f, topw = NONE;
-#pragma unroll
-            for (int w = 0; w < DEC_WARPS; ++w) {
-                const float4 x = *reinterpret_cast<const float4*>(join + (w * Q + qr) * C::OPAD + dim);
-                o.x += x.x;
-                o.y += x.y;
-                o.z += x.z;
-                o.w += x.w;
-                top = fmaxf(top, stat[w * 3 * Q + qr]);
-                topw = fmaxf(topw, stat[w * 3 * Q + 2 * Q + qr]);
-            }
-#pragma unroll
-            for (int w = 0; w < DEC_WARPS; ++w) lsum += stat[w * 3 * Q + Q + qr] * ex2(stat[w * 3 * Q + qr] - top);
-            if (!whole) {
+    __syncthreads();
+    for (int w0 = 0; w0 < wpc;) {
+        const int64_t at = seg_at[w0];
+        int w1 = w0 + 1;
+        while (w1 < wpc && seg_at[w1] == at) ++w1;
+        if (at >= 0) {
+            float* part = d.parts + 2 * (int64_t)(blockIdx.x * wpc + w0) * C::PART;
+            for (int i = tid; i < Q * (DP / 4); i += DEC_WARPS * 32) {
+                const int qr = i / (DP / 4), dim = i % (DP / 4) * 4;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                float top = NONE, sum = 0.f, topw = NONE;
+                for (int w = w0; w < w1; ++w) {
+                    const float4 x = *reinterpret_cast<const float4*>(join + (w * Q + qr) * C::OPAD + dim);
+                    o.x += x.x;
+                    o.y += x.y;
+                    o.z += x.z;
+                    o.w += x.w;
+                    top = fmaxf(top, stat[w * 3 * Q + qr]);
+                    topw = fmaxf(topw, stat[w * 3 * Q + 2 * Q + qr]);
+                }
+                for (int w = w0; w < w1; ++w) sum += stat[w * 3 * Q + Q + qr] * ex2(stat[w * 3 * Q + qr] - top);
                 *reinterpret_cast<float4*>(part + qr * DP + dim) = o;
                 if (dim == 0) {
                     part[Q * DP + qr] = top;
-                    part[Q * DP + Q + qr] = lsum;
+                    part[Q * DP + Q + qr] = sum;
                     part[Q * DP + 2 * Q + qr] = topw;
                 }
-                continue;
             }
-            const int r = rg * Q + qr;
-            if (r < rows) {
-                const int64_t row = s.r.r0 + r / a.group, head = h * a.group + r % a.group;
-                const float f = lsum > 0.f ? ex2(topw - top) / lsum : 0.f;
-                if (dim < a.c.dim) {
-                    alignas(8) T y[4] = {from_float<T>(o.x * f), from_float<T>(o.y * f), from_float<T>(o.z * f),
-                                         from_float<T>(o.w * f)};
-                    *reinterpret_cast<uint2*>((T*)a.out + row * a.o_row + head * a.o_head + dim) =
-                        *reinterpret_cast<const uint2*>(y);
-                }
-                if (a.lse && dim == 0)
-                    a.lse[row * a.heads + head] =
-                        lsum > 0.f ? (top + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
-            }
-        }
-        if (!whole) {
+            const Parts ps(at, seg_entry[w0].subs, total, P, wpc);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                const int n = atomicAdd(d.arrivals + c0, 1);
-                note[1] = n == (int)(c1 - c0);
-                if (note[1]) d.arrivals[c0] = 0;
+                arrived = atomicAdd(d.arrivals + ps.first, 1);
+                if (arrived == ps.n - 1) d.arrivals[ps.first] = 0;
             }
             __syncthreads();
-            if (note[1]) {  // the last part is here: join them all, in order
+            if (arrived == ps.n - 1) {
                 __threadfence();
-                for (int i = tid; i < Q * (DP / 4); i += DEC_WARPS * 32) {
-                    const int qr = i / (DP / 4), dim = i % (DP / 4) * 4;
-                    const int r = rg * Q + qr;
-                    if (r >= rows) continue;
-                    float top = NONE, topw = NONE;
-                    for (int64_t x = c0; x <= c1; ++x) {
-                        const float* st = d.parts + (2 * x + (x == c0 ? 1 : 0)) * PART_FLOATS + Q * DP + qr;
-                        top = fmaxf(top, __ldcg(st));
-                        topw = fmaxf(topw, __ldcg(st + 2 * Q));
-                    }
-                    float lsum = 0.f;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int64_t x = c0; x <= c1; ++x) {
-                        const float* from = d.parts + (2 * x + (x == c0 ? 1 : 0)) * PART_FLOATS;
-                        const float* st = from + Q * DP + qr;
-                        lsum += __ldcg(st + Q) * ex2(__ldcg(st) - top);
-                        const float f = ex2(__ldcg(st + 2 * Q) - topw);
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(from + qr * DP + dim));
-                        o.x += y.x * f;
-                        o.y += y.y * f;
-                        o.z += y.z * f;
-                        o.w += y.w * f;
-                    }
-                    const int64_t row = s.r.r0 + r / a.group, head = h * a.group + r % a.group;
-                    const float f = lsum > 0.f ? ex2(topw - top) / lsum : 0.f;
-                    if (dim < a.c.dim) {
-                        alignas(8) T y[4] = {from_float<T>(o.x * f), from_float<T>(o.y * f), from_float<T>(o.z * f),
-                                             from_float<T>(o.w * f)};
-                        *reinterpret_cast<uint2*>((T*)a.out + row * a.o_row + head * a.o_head + dim) =
-                            *reinterpret_cast<const uint2*>(y);
-                    }
-                    if (a.lse && dim == 0)
-                        a.lse[row * a.heads + head] =
-                            lsum > 0.f ? (top + __log2f(lsum)) * 0.6931471805599453f : -INFINITY;
-                }
+                join_parts<T, DP, NT>(d, ps, seg_entry[w0], tid, DEC_WARPS * 32);
             }
         }
-        // the joining buffer is the ring again: its next loads (async proxy)
-        // come after these reads and writes
-        bspx::fence_proxy_async_smem();
-        __syncthreads();
-        u += n_units;
-        off += n_units;
+        w0 = w1;
     }
-    if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
@@ -649,7 +766,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-constexpr int DECODE_CTAS_PER_SM = 3;  // at most
+constexpr int DECODE_CTAS_PER_SM = 2;
 
 template <class T, int DP, int NT>
 bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
@@ -667,35 +784,30 @@ bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
             return e;
         }))
         return BSP_ERR_CUDA;
-    const int grid = h->num_sms * std::clamp(per_sm[dev], 1, DECODE_CTAS_PER_SM);
+    const int grid = h->num_sms * std::min(std::max(per_sm[dev], 1), DECODE_CTAS_PER_SM);
     kv_decode_kernel<T, DP, NT><<<grid, DEC_WARPS * 32, C::SMEM, s>>>(h->map_k, h->map_v, d);
     return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
 template <class T>
-bsp_status_t run_decode(const bsp_kv* h, const DecodeArgs& d, int nt, cudaStream_t s)
-{
-    if (d.a.c.dim <= 64)
-        return nt == 1 ? launch_decode<T, 64, 1>(h, d, s) : nt == 2 ? launch_decode<T, 64, 2>(h, d, s)
-                                                                   : launch_decode<T, 64, 4>(h, d, s);
-    if (d.a.c.dim <= 128)
-        return nt == 1 ? launch_decode<T, 128, 1>(h, d, s) : nt == 2 ? launch_decode<T, 128, 2>(h, d, s)
-                                                                    : launch_decode<T, 128, 4>(h, d, s);
-    return nt == 1 ? launch_decode<T, 256, 1>(h, d, s) : launch_decode<T, 256, 2>(h, d, s);
-}
-
-template <class T>
 bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream_t s)
 {
-    const int64_t most = max_new * a.group;
-    // Query blocks of 8, 16 or 32 rows: the smallest that holds the largest
+    // Query blocks of 8, 16 or 24 rows: the smallest that holds the largest
     // request.  Requests with more rows are the prompt kernel's, whose row
     // tiles have 128 rows and whose dims end at 128.
-    const int few = a.c.dim > 128 ? INT32_MAX : 32;
-    const int nt = most <= 8 ? 1 : most <= 16 ? 2 : 4;
+    const int64_t most = max_new * a.group;
+    const int few = a.c.dim > 128 ? INT32_MAX : 24;
     const DecodeArgs d = {a, h->parts, h->arrivals, h->err, bsp_spin_cap(), few};
-    if (const bsp_status_t st = run_decode<T>(h, d, nt, s)) return st;
-    if (most <= few || !a.s.batch) return BSP_OK;
+    bsp_status_t st;
+    if (a.c.dim <= 64)
+        st = most <= 8 ? launch_decode<T, 64, 1>(h, d, s) : most <= 16 ? launch_decode<T, 64, 2>(h, d, s)
+                                                                       : launch_decode<T, 64, 3>(h, d, s);
+    else if (a.c.dim <= 128)
+        st = most <= 8 ? launch_decode<T, 128, 1>(h, d, s) : most <= 16 ? launch_decode<T, 128, 2>(h, d, s)
+                                                                        : launch_decode<T, 128, 3>(h, d, s);
+    else
+        st = most <= 8 ? launch_decode<T, 256, 1>(h, d, s) : launch_decode<T, 256, 2>(h, d, s);
+    if (st != BSP_OK || most <= few || !a.s.batch) return st;
     return bsp_run_kv_prompt(h, a, std::is_same<T, __half>::value ? BSP_FP16 : BSP_BF16, few, s);
 }
 
@@ -722,11 +834,12 @@ bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s)
                    CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return BSP_ERR_SHAPE;
-    h->decode_ctas = h->num_sms * DECODE_CTAS_PER_SM;
-    if (cudaMalloc(&h->parts, (size_t)2 * h->decode_ctas * PART_FLOATS * sizeof(float)) != cudaSuccess ||
-        cudaMalloc(&h->arrivals, (size_t)h->decode_ctas * sizeof(int)) != cudaSuccess)
+    const size_t workers = (size_t)h->num_sms * DECODE_CTAS_PER_SM * DEC_WARPS;
+    const size_t part = c.dim <= 64 ? DecCfg<64, 3>::PART : c.dim <= 128 ? DecCfg<128, 3>::PART : DecCfg<256, 2>::PART;
+    if (cudaMalloc(&h->parts, 2 * workers * part * sizeof(float)) != cudaSuccess ||
+        cudaMalloc(&h->arrivals, workers * sizeof(int)) != cudaSuccess)
         return BSP_ERR_OOM;
-    if (cudaMemsetAsync(h->arrivals, 0, (size_t)h->decode_ctas * sizeof(int), s) != cudaSuccess) return BSP_ERR_CUDA;
+    if (cudaMemsetAsync(h->arrivals, 0, workers * sizeof(int), s) != cudaSuccess) return BSP_ERR_CUDA;
     return BSP_OK;
 }
 
