@@ -50,15 +50,24 @@ struct DecCfg {
     static constexpr int REGIONS = DP / BOX;
     static constexpr int HALF = SUB * DP;              // K (or V) codes of a stage
     static constexpr int STAGE = 2 * HALF;
-    static constexpr int STAGES = DP == 64 ? 4 : 3;
+    // CTAs that an SM holds (by registers and shared memory), and stages of a
+    // warp's ring: with three CTAs two stages of 8 KB keep more bytes in
+    // flight than the memory needs
+    static constexpr int CTAS = NT == 1 && DP <= 128 ? 3 : 2;
+    // queries too many for the registers beside the sums wait in shared memory
+    static constexpr bool QSMEM = NT * DP > 256;
+    static constexpr int STAGES = DP == 64 ? 4 : CTAS == 3 || QSMEM ? 2 : 3;
+    static constexpr int QBYTES = QSMEM ? NT * DP * 16 : 0;  // of a warp
     static constexpr int RING = DEC_WARPS * STAGES * STAGE;
     static constexpr int Q = 8 * NT;                   // query rows of a segment
     static constexpr int OPAD = DP + 4;                // floats of a row of the joining buffer
     static constexpr int PART = Q * (DP + 4);          // floats of a part: O, then m, l, mw of the rows
     static constexpr int OFF_RUN = RING;               // entries of each warp's run
-    static constexpr int OFF_STAT = OFF_RUN + DEC_WARPS * RUN * 64;  // m, l, mw of each warp
+    static constexpr int OFF_Q = OFF_RUN + DEC_WARPS * RUN * 64;
+    static constexpr int OFF_STAT = OFF_Q + DEC_WARPS * QBYTES;  // m, l, mw of each warp
     static constexpr int OFF_BAR = OFF_STAT + DEC_WARPS * Q * 3 * 4;
     static constexpr int SMEM = OFF_BAR + DEC_WARPS * STAGES * 8 + 1024;
+    static_assert(SMEM <= 225 * 1024 / (DP == 256 ? 1 : CTAS), "shared memory of the resident CTAs");
     static_assert(DEC_WARPS * Q * OPAD * 4 <= RING, "joining buffer in the idle ring");
 };
 
@@ -117,7 +126,8 @@ struct Entry {
     int tok, p0, p1, h;      // first row, its page and (pages of 16 rows) the next one's, KV head
     int len, n, r0, rg;      // the request, the group of query rows
     float ks[2], vs[2];
-    int i, subs, pad[2];     // which sub-tile of how many
+    int i, subs;             // which sub-tile of how many
+    float lv[2];             // log2 vs
 };
 static_assert(sizeof(Entry) == 64, "run entries");
 
@@ -193,7 +203,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& d, const Parts& ps,
 }
 
 template <class T, int DP, int NT>
-__global__ void __launch_bounds__(DEC_WARPS * 32, 2)
+__global__ void __launch_bounds__(DEC_WARPS * 32, DecCfg<DP, NT>::CTAS)
 kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const DecodeArgs d)
 {
     using C = DecCfg<DP, NT>;
@@ -282,6 +292,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         Entry e;
         e.tok = e.p0 = e.p1 = -1;
         e.ks[0] = e.ks[1] = e.vs[0] = e.vs[1] = 0.f;
+        e.lv[0] = e.lv[1] = NONE;
         while (true) {
             const int64_t window_end = __shfl_sync(FULL, ends, 31);
             const bool here = todo && x < window_end;
@@ -321,6 +332,9 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                         e.ks[1] = a.c.k_scale[(int64_t)e.p1 * a.c.scale_stride + e.h];
                         e.vs[1] = a.c.v_scale[(int64_t)e.p1 * a.c.scale_stride + e.h];
                     }
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        if (e.vs[y] != 0.f) e.lv[y] = __log2f(fabsf(e.vs[y]));
                 }
                 todo = false;
             }
@@ -378,7 +392,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     load();
 
     // the segment being worked on
-    uint32_t qf[NT][CH][8];   // queries: a thread's chunks of its row
+    uint32_t qf[C::QSMEM ? 1 : NT][CH][8];  // queries: a thread's chunks of its row
+    uint2* qm = reinterpret_cast<uint2*>(smem + C::OFF_Q + warp * C::QBYTES) + lane;
     float qs[NT][2];          // scale of its columns' logits
     int pos[NT][2];           // positions of the columns' queries
     float acc[MT][NT][4];
@@ -441,7 +456,16 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 #pragma unroll
                 for (int j = 0; j < CH; ++j)
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) qf[nt][j][y] = h2bits(__floats2half2_rn(x[j][2 * y], x[j][2 * y + 1]));
+                    for (int y = 0; y < 4; ++y) {
+                        const uint2 v = make_uint2(h2bits(__floats2half2_rn(x[j][4 * y], x[j][4 * y + 1])),
+                                                   h2bits(__floats2half2_rn(x[j][4 * y + 2], x[j][4 * y + 3])));
+                        if constexpr (C::QSMEM) {
+                            qm[((nt * CH + j) * 4 + y) * 32] = v;  // read by the same thread only
+                        } else {
+                            qf[nt][j][2 * y] = v.x;
+                            qf[nt][j][2 * y + 1] = v.y;
+                        }
+                    }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     qs[nt][y] = __shfl_sync(FULL, unit, (2 * c + y) * 4) * (a.scale * 1.4426950408889634f);
@@ -467,50 +491,67 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             // S^T
             float sc[2][NT][4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int y = 0; y < 4; ++y) sc[i][nt][y] = 0.f;
 #pragma unroll
-                for (int j = 0; j < CH; ++j) {
-                    const int ch = DP == 64 ? c : 2 * c + (j & 1);
-                    const int r0 = 16 * i + g, r1 = r0 + 8;
-                    const int sw0 = DP == 64 ? (r0 >> 1) & 3 : r0 & 7, sw1 = DP == 64 ? (r1 >> 1) & 3 : r1 & 7;
-                    const uint8_t* reg = kt + (j >> 1) * SUB * C::BOX;
-                    const uint4 w0 = *reinterpret_cast<const uint4*>(reg + r0 * C::BOX + ((ch ^ sw0) << 4));
-                    const uint4 w1 = *reinterpret_cast<const uint4*>(reg + r1 * C::BOX + ((ch ^ sw1) << 4));
-                    const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+            for (int j = 0; j < CH; ++j) {
+                const int ch = DP == 64 ? c : 2 * c + (j & 1);
+                const uint8_t* reg = kt + (j >> 1) * SUB * C::BOX;
+                uint4 v[2][2];  // rows g and g + 8 of each half
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t y0 = x0[w] ^ 0x80808080u, y1 = x1[w] ^ 0x80808080u;
-                        const uint32_t a0 = widen(y0, 0x4140), a2 = widen(y0, 0x4342);
-                        const uint32_t a1 = widen(y1, 0x4140), a3 = widen(y1, 0x4342);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 8 * i + g, sw = DP == 64 ? (row >> 1) & 3 : row & 7;
+                    v[i >> 1][i & 1] = *reinterpret_cast<const uint4*>(reg + row * C::BOX + ((ch ^ sw) << 4));
+                }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816(sc[i][nt], a0, a1, a2, a3, qf[nt][j][2 * w], qf[nt][j][2 * w + 1]);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t z = (&v[i][y].x)[w] ^ 0x80808080u;
+                            f[i][y] = widen(z, 0x4140);
+                            f[i][2 + y] = widen(z, 0x4342);
+                        }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint2 q;
+                        if constexpr (C::QSMEM) q = qm[((nt * CH + j) * 4 + w) * 32];
+                        else q = make_uint2(qf[nt][j][2 * w], qf[nt][j][2 * w + 1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            mma16816(sc[i][nt], f[i][0], f[i][1], f[i][2], f[i][3], q.x, q.y);
                     }
                 }
             }
-            // logits (in powers of two), masked where a query does not see the row
+            // factors of the logits (in powers of two); where a query does not
+            // see every row the masked logits themselves, and a factor of one
             const bool edge = tok + SUB - 1 > first || (a.window && tok <= e.len - 1 - a.window) || p0 < 0 || p1 < 0;
-            float lv[2];
+            const float lv[2] = {e.lv[0], e.lv[1]};
+            float kf[2][NT][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool there = (i ? p1 : p0) >= 0;
-                lv[i] = vscale[i] != 0.f ? __log2f(fabsf(vscale[i])) : NONE;
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        float x = sc[i][nt][y] * (kscale[i] * qs[nt][y & 1]);
-                        if (edge) {
+                    for (int y = 0; y < 2; ++y) kf[i][nt][y] = kscale[i] * qs[nt][y];
+            if (edge)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
                             const int j = tok + 16 * i + g + (y >> 1) * 8, p = pos[nt][y & 1];
-                            if (!there || j > p || (a.window && j <= p - a.window)) x = -INFINITY;
+                            const bool see = (i ? p1 : p0) >= 0 && j <= p && (!a.window || j > p - a.window);
+                            sc[i][nt][y] = see ? sc[i][nt][y] * kf[i][nt][y & 1] : -INFINITY;
                         }
-                        sc[i][nt][y] = x;
+                        kf[i][nt][0] = kf[i][nt][1] = 1.f;
                     }
-            }
             // running maxima, allowed to lag
             bool lag = false;
             float hi[NT][2][2];
@@ -519,7 +560,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) hi[nt][y][i] = fmaxf(sc[i][nt][y], sc[i][nt][y + 2]);
+                    for (int i = 0; i < 2; ++i)
+                        hi[nt][y][i] = fmaxf(sc[i][nt][y], sc[i][nt][y + 2]) * kf[i][nt][y];
                     lag |= fmaxf(hi[nt][y][0], hi[nt][y][1]) > m[nt][y] + LAZY;
                     lag |= fmaxf(hi[nt][y][0] + lv[0], hi[nt][y][1] + lv[1]) > mw[nt][y] + LAZY;
                 }
@@ -558,7 +600,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     float p[4];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        p[y] = ex2(sc[i][nt][y] - m[nt][y & 1]);
+                        p[y] = ex2(fmaf(sc[i][nt][y], kf[i][nt][y & 1], -m[nt][y & 1]));
                         l[nt][y & 1] += p[y];
                         p[y] *= lift[nt][y & 1] * vscale[i];
                     }
@@ -766,8 +808,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-constexpr int DECODE_CTAS_PER_SM = 2;
-
 template <class T, int DP, int NT>
 bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
 {
@@ -784,7 +824,7 @@ bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
             return e;
         }))
         return BSP_ERR_CUDA;
-    const int grid = h->num_sms * std::min(std::max(per_sm[dev], 1), DECODE_CTAS_PER_SM);
+    const int grid = h->num_sms * std::min(std::max(per_sm[dev], 1), C::CTAS);
     kv_decode_kernel<T, DP, NT><<<grid, DEC_WARPS * 32, C::SMEM, s>>>(h->map_k, h->map_v, d);
     return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
@@ -834,9 +874,12 @@ bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s)
                    CU_TENSOR_MAP_INTERLEAVE_NONE, c.dim <= 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return BSP_ERR_SHAPE;
-    const size_t workers = (size_t)h->num_sms * DECODE_CTAS_PER_SM * DEC_WARPS;
-    const size_t part = c.dim <= 64 ? DecCfg<64, 3>::PART : c.dim <= 128 ? DecCfg<128, 3>::PART : DecCfg<256, 2>::PART;
-    if (cudaMalloc(&h->parts, 2 * workers * part * sizeof(float)) != cudaSuccess ||
+    const size_t workers = (size_t)h->num_sms * 3 * DEC_WARPS;  // at most
+    auto floats = [](auto cfg) { return (size_t)decltype(cfg)::CTAS * decltype(cfg)::PART; };
+    const size_t part = c.dim <= 64 ? std::max(floats(DecCfg<64, 1>{}), floats(DecCfg<64, 3>{}))
+                        : c.dim <= 128 ? std::max(floats(DecCfg<128, 1>{}), floats(DecCfg<128, 3>{}))
+                                       : floats(DecCfg<256, 2>{});
+    if (cudaMalloc(&h->parts, (size_t)h->num_sms * DEC_WARPS * 2 * part * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&h->arrivals, workers * sizeof(int)) != cudaSuccess)
         return BSP_ERR_OOM;
     if (cudaMemsetAsync(h->arrivals, 0, workers * sizeof(int), s) != cudaSuccess) return BSP_ERR_CUDA;
