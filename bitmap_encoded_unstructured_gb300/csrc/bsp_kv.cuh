@@ -27,6 +27,14 @@ struct KvStepView {
     int64_t rows;
 };
 
+// A segment (request, KV head, group of query rows) whose cached rows were
+// shared by warps from its own index to `last`, `per_cta` to a CTA.
+struct KvCut {
+    int32_t last, per_cta;
+    int32_t r0, n, h, rg;  // the request's first row and new rows, KV head, group
+    int32_t pad[2];
+};
+
 struct bsp_kv {
     uint32_t magic;
     int device, num_sms;
@@ -37,9 +45,9 @@ struct bsp_kv {
     int* ticket;  // arrivals of a plan whose count is updated in place; zero between calls
     int* err;     // as bsp_handle::err
     // few queries: parts of segments cut between warps, two slots a warp, and
-    // the arrivals of each such segment (zero between calls)
+    // the cut segments by the warp that begins them (last = 0 between calls)
     float* parts;
-    int* arrivals;
+    KvCut* cuts;
 };
 
 namespace bspkv {
@@ -148,6 +156,10 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bspx::smem_u32(bar))
         : "memory");
 }
+
+// Wait until the grids this one depends on (programmatic dependent launch)
+// have completed and their memory is visible; returns at once otherwise.
+__device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Encode the tensor maps and allocate the decode scratch of a new handle.
 bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s);

@@ -30,7 +30,8 @@ using namespace bspkv;
 // (TMA boxes of the paged codes, across segment ends), with no block-wide
 // barrier until its run is done, and writes the segments that it has whole.
 // Of a segment cut between warps each leaves a part (the warps of a CTA add
-// theirs first); the last to arrive joins the parts, in order.
+// theirs first), and a second kernel, one warp per query row, joins the
+// parts in order.
 //
 //   S^T[row][query] = codes_K . q     mma m16n8k16, A = codes as exact fp16
 //   O^T[dim][query] += codes_V^T . W  W = p * V scale
@@ -74,7 +75,7 @@ struct DecCfg {
 struct DecodeArgs {
     AttnArgs a;
     float* parts;
-    int* arrivals;
+    KvCut* cuts;
     int* err;
     uint32_t spin_cap;
     int32_t most_rows;  // requests with more query rows than this (per KV head) are not this kernel's
@@ -134,23 +135,6 @@ static_assert(sizeof(Entry) == 64, "run entries");
 // The worker (warp) that has place x of the shared run.
 __device__ __forceinline__ int worker_of(int64_t x, int64_t total, int64_t P) { return (int)(((x + 1) * P - 1) / total); }
 
-// Parts of one segment: the first worker's, one of each further CTA's, and
-// the last worker's.
-struct Parts {
-    int first, last, per_cta, n;
-    __device__ Parts(int64_t x0, int subs, int64_t total, int64_t P, int wpc)
-    {
-        first = worker_of(x0, total, P);
-        last = worker_of(x0 + subs - 1, total, P);
-        per_cta = wpc;
-        n = (last - 1) / wpc - first / wpc + 2;
-    }
-    __device__ int64_t slot(int k) const
-    {
-        return k == n - 1 ? 2 * (int64_t)last + 1 : 2 * (int64_t)(k ? (first / per_cta + k) * per_cta : first);
-    }
-};
-
 // Four dims of one query row, joined: out = O 2^(mw - m) / l.
 template <class T>
 __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int64_t head, int dim, float4 o, float top,
@@ -166,39 +150,92 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int64_
         a.lse[row * a.heads + head] = sum > 0.f ? (top + __log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-// The parts of a segment, joined by `threads` threads.
+constexpr int JOIN_WARPS = 8;
+
+// The parts of the segments that were cut, in order: the first worker's, one
+// of each further CTA's, and the last worker's.  A warp joins one query row;
+// a CTA looks after every gridDim-th worker that began a cut segment.
 template <class T, int DP, int NT>
-__device__ __forceinline__ void join_parts(const DecodeArgs& d, const Parts& ps, const Entry& e, int tid, int threads)
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const DecodeArgs d, int workers)
 {
     using C = DecCfg<DP, NT>;
-    constexpr int Q = C::Q;
+    constexpr int Q = C::Q, LANES = DP / 4 < 32 ? DP / 4 : 32, ROWS = 32 / LANES, V = DP / 4 / LANES;
     const AttnArgs& a = d.a;
-    for (int i = tid; i < Q * (DP / 4); i += threads) {
-        const int qr = i / (DP / 4), dim = i % (DP / 4) * 4;
-        const int r = e.rg * Q + qr;
-        if (r >= e.n * a.group) continue;
-        float top = NONE, topw = NONE;
-#pragma unroll 4
-        for (int k = 0; k < ps.n; ++k) {
-            const float* st = d.parts + ps.slot(k) * C::PART + Q * DP + qr;
-            top = fmaxf(top, __ldcg(st));
-            topw = fmaxf(topw, __ldcg(st + 2 * Q));
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    wait_prior_grids();  // launched before the other kernel is done
+    for (int w = blockIdx.x; w < workers; w += gridDim.x) {
+        const KvCut cut = d.cuts[w];
+        __syncthreads();
+        if (!cut.last) continue;
+        if (threadIdx.x == 0) d.cuts[w].last = 0;
+        const int n = (cut.last - 1) / cut.per_cta - w / cut.per_cta + 2;
+        auto part = [&](int k) {
+            const int64_t slot = k == n - 1 ? 2 * (int64_t)cut.last + 1
+                                            : 2 * (int64_t)(k ? (w / cut.per_cta + k) * cut.per_cta : w);
+            return d.parts + slot * C::PART;
+        };
+        for (int qr = warp * ROWS + lane / LANES; qr < Q; qr += JOIN_WARPS * ROWS) {
+            const int r = cut.rg * Q + qr, dim = lane % LANES * 4;
+            if (r >= cut.n * a.group) continue;
+            float top = NONE, topw = NONE, sum = 0.f;
+            float4 o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int AT_ONCE = 8;  // parts whose loads are in flight together
+            for (int k0 = 0; k0 < n; k0 += AT_ONCE) {
+                float pm[AT_ONCE], pl[AT_ONCE], pw[AT_ONCE];
+                float4 po[AT_ONCE][V];
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    pm[k] = pw[k] = NONE;
+                    pl[k] = 0.f;
+                    if (k0 + k < n) {
+                        const float* from = part(k0 + k);
+                        pm[k] = __ldcg(from + Q * DP + qr);
+                        pl[k] = __ldcg(from + Q * DP + Q + qr);
+                        pw[k] = __ldcg(from + Q * DP + 2 * Q + qr);
+#pragma unroll
+                        for (int v = 0; v < V; ++v)
+                            po[k][v] = __ldcg(reinterpret_cast<const float4*>(from + qr * DP + dim + v * 128));
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) po[k][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+                float t = top, tw = topw;
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    t = fmaxf(t, pm[k]);
+                    tw = fmaxf(tw, pw[k]);
+                }
+                sum *= ex2(top - t);
+                const float back = ex2(topw - tw);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    o[v].x *= back;
+                    o[v].y *= back;
+                    o[v].z *= back;
+                    o[v].w *= back;
+                }
+                top = t;
+                topw = tw;
+#pragma unroll
+                for (int k = 0; k < AT_ONCE; ++k) {
+                    sum += pl[k] * ex2(pm[k] - top);
+                    const float f = ex2(pw[k] - topw);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        o[v].x += po[k][v].x * f;
+                        o[v].y += po[k][v].y * f;
+                        o[v].z += po[k][v].z * f;
+                        o[v].w += po[k][v].w * f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                store_out<T>(a, cut.r0 + r / a.group, cut.h * a.group + r % a.group, dim + v * 128, o[v], top, topw, sum);
         }
-        float sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < ps.n; ++k) {
-            const float* from = d.parts + ps.slot(k) * C::PART;
-            const float* st = from + Q * DP + qr;
-            sum += __ldcg(st + Q) * ex2(__ldcg(st) - top);
-            const float f = ex2(__ldcg(st + 2 * Q) - topw);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(from + qr * DP + dim));
-            o.x += y.x * f;
-            o.y += y.y * f;
-            o.z += y.z * f;
-            o.w += y.w * f;
-        }
-        store_out<T>(a, e.r0 + r / a.group, e.h * a.group + r % a.group, dim, o, top, topw, sum);
     }
 }
 
@@ -686,27 +723,14 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     part[Q * DP + 2 * Q + qr] = mw[nt][y];
                 }
             }
-        if (!whole) {
-            const Parts ps(x0 + k - e.i, e.subs, total, P, wpc);
-            __threadfence();
-            __syncwarp();
-            int n = 0;
-            if (lane == 0) n = atomicAdd(d.arrivals + ps.first, 1);
-            n = __shfl_sync(FULL, n, 0);
-            if (n == ps.n - 1) {
-                if (lane == 0) d.arrivals[ps.first] = 0;
-                __threadfence();
-                join_parts<T, DP, NT>(d, ps, e, lane, 32);
-            }
-        }
     }
     if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, as SMs fall free
 
     // Segments that go on beyond the warps' runs.  The warps of a CTA that
     // are on the same one add their sums in shared memory (the ring is idle).
     __shared__ int64_t seg_at[DEC_WARPS];  // place of the segment's first sub-tile, -1: none
     __shared__ Entry seg_entry[DEC_WARPS];
-    __shared__ int arrived;
     if (lane == 0) {
         seg_at[warp] = -1;
         if (open) {
@@ -776,18 +800,11 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     part[Q * DP + 2 * Q + qr] = topw;
                 }
             }
-            const Parts ps(at, seg_entry[w0].subs, total, P, wpc);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                arrived = atomicAdd(d.arrivals + ps.first, 1);
-                if (arrived == ps.n - 1) d.arrivals[ps.first] = 0;
-            }
-            __syncthreads();
-            if (arrived == ps.n - 1) {
-                __threadfence();
-                join_parts<T, DP, NT>(d, ps, seg_entry[w0], tid, DEC_WARPS * 32);
-            }
+            // the worker that begins the segment says who ends it
+            const Entry& e = seg_entry[w0];
+            const int me = blockIdx.x * wpc + w0;
+            if (tid == 0 && worker_of(at, total, P) == me)
+                d.cuts[me] = {worker_of(at + e.subs - 1, total, P), wpc, e.r0, e.n, e.h, e.rg, {0, 0}};
         }
         w0 = w1;
     }
@@ -826,7 +843,18 @@ bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
         return BSP_ERR_CUDA;
     const int grid = h->num_sms * std::min(std::max(per_sm[dev], 1), C::CTAS);
     kv_decode_kernel<T, DP, NT><<<grid, DEC_WARPS * 32, C::SMEM, s>>>(h->map_k, h->map_v, d);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
+    // the joining kernel may be set up while the other one ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)h->num_sms * 4);
+    cfg.blockDim = dim3(JOIN_WARPS * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, DP, NT>, d, grid * DEC_WARPS) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
 template <class T>
@@ -837,7 +865,7 @@ bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream
     // tiles have 128 rows and whose dims end at 128.
     const int64_t most = max_new * a.group;
     const int few = a.c.dim > 128 ? INT32_MAX : 24;
-    const DecodeArgs d = {a, h->parts, h->arrivals, h->err, bsp_spin_cap(), few};
+    const DecodeArgs d = {a, h->parts, h->cuts, h->err, bsp_spin_cap(), few};
     bsp_status_t st;
     if (a.c.dim <= 64)
         st = most <= 8 ? launch_decode<T, 64, 1>(h, d, s) : most <= 16 ? launch_decode<T, 64, 2>(h, d, s)
@@ -880,16 +908,16 @@ bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s)
                         : c.dim <= 128 ? std::max(floats(DecCfg<128, 1>{}), floats(DecCfg<128, 3>{}))
                                        : floats(DecCfg<256, 2>{});
     if (cudaMalloc(&h->parts, (size_t)h->num_sms * DEC_WARPS * 2 * part * sizeof(float)) != cudaSuccess ||
-        cudaMalloc(&h->arrivals, workers * sizeof(int)) != cudaSuccess)
+        cudaMalloc(&h->cuts, workers * sizeof(KvCut)) != cudaSuccess)
         return BSP_ERR_OOM;
-    if (cudaMemsetAsync(h->arrivals, 0, workers * sizeof(int), s) != cudaSuccess) return BSP_ERR_CUDA;
+    if (cudaMemsetAsync(h->cuts, 0, workers * sizeof(KvCut), s) != cudaSuccess) return BSP_ERR_CUDA;
     return BSP_OK;
 }
 
 void attention_free(bsp_kv* h)
 {
     cudaFree(h->parts);
-    cudaFree(h->arrivals);
+    cudaFree(h->cuts);
 }
 
 }  // namespace bspkv
