@@ -74,6 +74,25 @@ struct DeviceGuard {
 // Rows of a call and rows a block table row can name: positions, and their
 // differences to a window, stay in 32 bits.
 constexpr int64_t MOST_ROWS = (int64_t)1 << 30;
+// Launch a kernel that may be set up while the kernel before it in the
+// stream ends (programmatic dependent launch).  It calls wait_prior_grids()
+// before it touches global memory, so nothing but the launch overlaps.
+template <class... P, class... A>
+bool launch_early(void (*kernel)(P...), dim3 grid, dim3 block, int smem, cudaStream_t s, const A&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute early[1];
+    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...) == cudaSuccess;
+}
+
 // Checks of a step, before any CUDA call.
 bsp_status_t check_step(const bsp_kv_step_t* st, int64_t rows, int page_shift);
 KvStepView view_of(const bsp_kv_step_t* st, int64_t rows);

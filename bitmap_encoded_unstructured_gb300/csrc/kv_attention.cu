@@ -42,7 +42,7 @@ using namespace bspkv;
 constexpr int DEC_WARPS = 4;
 constexpr int SUB = 32;                  // rows of a sub-tile
 constexpr int OVER = 2;                  // sub-tiles a segment's start and end are worth
-constexpr int LEAST = 6;                 // a warp's run is at least this long, or joining costs more than it saves
+constexpr int LEAST = 3;                 // a warp's run is at least this long (more than OVER)
 constexpr int RUN = 32, FILL = 16;       // entries of the run that a warp looks ahead, and fills at a time
 
 template <int DP, int NT>
@@ -67,8 +67,14 @@ struct DecCfg {
     static constexpr int OFF_Q = OFF_RUN + DEC_WARPS * RUN * 64;
     static constexpr int OFF_STAT = OFF_Q + DEC_WARPS * QBYTES;  // m, l, mw of each warp
     static constexpr int OFF_BAR = OFF_STAT + DEC_WARPS * Q * 3 * 4;
-    static constexpr int SMEM = OFF_BAR + DEC_WARPS * STAGES * 8 + 1024;
-    static_assert(SMEM <= 225 * 1024 / (DP == 256 ? 1 : CTAS), "shared memory of the resident CTAs");
+    // (all of it dynamic: static arrays would be rounded up to its alignment)
+    static constexpr int OFF_PRE = OFF_BAR + DEC_WARPS * STAGES * 8;         // what comes before each thread's requests
+    static constexpr int OFF_SEG = OFF_PRE + (DEC_WARPS * 32 + 2) * 8;       // the warps' open segments
+    static constexpr int OFF_SUMS = OFF_SEG + DEC_WARPS * 64;
+    static constexpr int OFF_AT = OFF_SUMS + DEC_WARPS * 8;
+    static constexpr int SMEM = OFF_AT + DEC_WARPS * 8 + 1024;
+    static_assert(OFF_SEG % 16 == 0, "alignment of the entries");
+    static_assert(SMEM + 1024 + 128 <= 228 * 1024 / (DP == 256 ? 1 : CTAS), "shared memory of the resident CTAs");
     static_assert(DEC_WARPS * Q * OPAD * 4 <= RING, "joining buffer in the idle ring");
 };
 
@@ -132,8 +138,29 @@ struct Entry {
 };
 static_assert(sizeof(Entry) == 64, "run entries");
 
-// The worker (warp) that has place x of the shared run.
-__device__ __forceinline__ int worker_of(int64_t x, int64_t total, int64_t P) { return (int)(((x + 1) * P - 1) / total); }
+// x / y for x >= 0, y > 0: 64-bit division is a long subroutine, and the
+// numbers nearly always fit 32 bits.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y)
+{
+    return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
+// The shared run of `total` places among P workers (warps): the first
+// `longer` have one place more than the others.
+struct Split {
+    int64_t each, longer;
+    __device__ Split(int64_t total, int64_t P)
+    {
+        each = quotient(total, P);
+        longer = total - each * P;
+    }
+    __device__ int64_t begin(int64_t w) const { return w * each + min(w, longer); }
+    __device__ int worker(int64_t x) const
+    {
+        const int64_t head = longer * (each + 1);
+        return (int)(x < head ? quotient(x, each + 1) : longer + quotient(x - head, each));
+    }
+};
 
 // Four dims of one query row, joined: out = O 2^(mw - m) / l.
 template <class T>
@@ -162,7 +189,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const DecodeAr
     constexpr int Q = C::Q, LANES = DP / 4 < 32 ? DP / 4 : 32, ROWS = 32 / LANES, V = DP / 4 / LANES;
     const AttnArgs& a = d.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    wait_prior_grids();  // launched before the other kernel is done
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_prior_grids();
     for (int w = blockIdx.x; w < workers; w += gridDim.x) {
         const KvCut cut = d.cuts[w];
         __syncthreads();
@@ -256,10 +284,14 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     uint8_t* ring = smem + warp * C::STAGES * C::STAGE;
     Entry* run = reinterpret_cast<Entry*>(smem + C::OFF_RUN) + warp * RUN;
 
+    if (lane < C::STAGES) bspx::mbar_init(full + lane, 1);
+    bspx::fence_mbar_init();
+    wait_prior_grids();  // launched before the kernel ahead of it is done
+
     // the shared run: each thread sums some requests; pre[i] is what comes
     // before thread i's
-    __shared__ int64_t pre[DEC_WARPS * 32 + 1];
-    __shared__ int64_t sums[DEC_WARPS];
+    int64_t* pre = reinterpret_cast<int64_t*>(smem + C::OFF_PRE);
+    int64_t* sums = reinterpret_cast<int64_t*>(smem + C::OFF_SUMS);
     const int per = (B + DEC_WARPS * 32 - 1) / (DEC_WARPS * 32);
     int64_t upto = 0;
     for (int b = min(B, tid * per); b < min(B, (tid + 1) * per); ++b)
@@ -271,8 +303,6 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         if (lane >= i) upto += o;
     }
     if (lane == 31) sums[warp] = upto;
-    if (lane < C::STAGES) bspx::mbar_init(full + lane, 1);
-    bspx::fence_mbar_init();
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
@@ -296,12 +326,13 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     }
 
     // P workers; fewer than there are warps are spread over the CTAs
-    const int64_t P = max((int64_t)1, min((int64_t)gridDim.x * DEC_WARPS, total / LEAST));
-    const int wpc = (int)min((int64_t)DEC_WARPS, (P + gridDim.x - 1) / gridDim.x);
+    const int P = (int)max((int64_t)1, min((int64_t)gridDim.x * DEC_WARPS, quotient(total, LEAST)));
+    const int wpc = min(DEC_WARPS, (P + (int)gridDim.x - 1) / (int)gridDim.x);
+    const Split split(total, P);
     const int worker = blockIdx.x * wpc + warp;
     const bool works = total > 0 && warp < wpc && worker < P;
-    const int64_t x0 = works ? total * worker / P : 0;
-    const int N = works ? (int)(total * (worker + 1) / P - x0) : 0;
+    const int64_t x0 = works ? split.begin(worker) : 0;
+    const int N = works ? (int)(split.begin(worker + 1) - x0) : 0;
 
     // requests 32 at a time, one per lane: what lies before them, and up to
     // each lane's end
@@ -323,77 +354,6 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         ends += before;
     };
     int filled = 0;
-    auto fill = [&]() {  // the next FILL entries of the run
-        const int64_t x = x0 + filled + lane;
-        bool todo = lane < FILL && filled + lane < N;
-        Entry e;
-        e.tok = e.p0 = e.p1 = -1;
-        e.ks[0] = e.ks[1] = e.vs[0] = e.vs[1] = 0.f;
-        e.lv[0] = e.lv[1] = NONE;
-        while (true) {
-            const int64_t window_end = __shfl_sync(FULL, ends, 31);
-            const bool here = todo && x < window_end;
-            int r = 0;  // the first lane whose requests end beyond x
-#pragma unroll
-            for (int i = 16; i; i >>= 1)
-                if (__shfl_sync(FULL, ends, r + i - 1) <= x) r += i;
-            r = min(r, 31);
-            const int64_t end = __shfl_sync(FULL, ends, r);
-            const int len = __shfl_sync(FULL, sr.r.len, r), n = __shfl_sync(FULL, sr.r.n, r);
-            const int r0 = __shfl_sync(FULL, sr.r.r0, r), lo = __shfl_sync(FULL, sr.lo, r);
-            const int seen = __shfl_sync(FULL, sr.seen, r), subs = __shfl_sync(FULL, sr.subs, r);
-            const int groups = __shfl_sync(FULL, sr.groups, r);
-            if (here) {
-                const int64_t off = x - (end - (int64_t)groups * H * (subs + OVER));
-                const int64_t seg = off / (subs + OVER);
-                e.i = (int)(off - seg * (subs + OVER)) - OVER;
-                e.subs = subs;
-                e.h = (int)(seg / groups);
-                e.rg = (int)(seg - (int64_t)e.h * groups);
-                e.len = len;
-                e.n = n;
-                e.r0 = r0;
-                if (e.i >= 0) {
-                    e.tok = lo + e.i * SUB;
-                    const int32_t* table = a.s.table + (int64_t)(bw + r) * a.s.table_stride;
-                    if (e.tok < len && ((e.tok >> sh) + 1) << sh > seen) e.p0 = table[e.tok >> sh];
-                    if (sh == 4 && e.tok + 16 < len && e.tok + 32 > seen) e.p1 = table[(e.tok >> 4) + 1];
-                    if (e.p0 >= a.c.pages) e.p0 = -1;
-                    if (e.p1 >= a.c.pages) e.p1 = -1;
-                    if (sh != 4) e.p1 = e.p0;
-                    if (e.p0 >= 0) {
-                        e.ks[0] = a.c.k_scale[(int64_t)e.p0 * a.c.scale_stride + e.h];
-                        e.vs[0] = a.c.v_scale[(int64_t)e.p0 * a.c.scale_stride + e.h];
-                    }
-                    if (e.p1 >= 0) {
-                        e.ks[1] = a.c.k_scale[(int64_t)e.p1 * a.c.scale_stride + e.h];
-                        e.vs[1] = a.c.v_scale[(int64_t)e.p1 * a.c.scale_stride + e.h];
-                    }
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        if (e.vs[y] != 0.f) e.lv[y] = __log2f(fabsf(e.vs[y]));
-                }
-                todo = false;
-            }
-            if (!__any_sync(FULL, todo) || bw + 32 >= B) break;
-            requests(bw + 32, window_end);
-        }
-        __syncwarp();
-        if (lane < FILL && filled + lane < N) run[(filled + lane) % RUN] = e;
-        __syncwarp();
-        filled += FILL;
-    };
-    if (works) {
-        int from = 0;
-        for (int i = lane; i < DEC_WARPS * 32; i += 32) {
-            const uint32_t hit = __ballot_sync(FULL, pre[i] <= x0 && x0 < pre[i + 1]);
-            if (hit) from = (i - lane) + __ffs(hit) - 1;
-        }
-        requests(from * per, pre[from]);
-        fill();
-        if (filled < N) fill();
-    }
-
     uint32_t stage = 0, phase = 0, next = 0;  // ring: stage being read, stage of the next load
     int ahead = 0, loading = 0;               // entries looked at for loading; loads in flight
     bool failed = false;
@@ -426,7 +386,80 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
         __syncwarp();
     };
-    load();
+    auto fill = [&]() {  // the next FILL entries of the run
+        const int64_t x = x0 + filled + lane;
+        bool todo = lane < FILL && filled + lane < N;
+        Entry e;
+        e.tok = e.p0 = e.p1 = -1;
+        e.ks[0] = e.ks[1] = e.vs[0] = e.vs[1] = 0.f;
+        e.lv[0] = e.lv[1] = NONE;
+        while (true) {
+            const int64_t window_end = __shfl_sync(FULL, ends, 31);
+            const bool here = todo && x < window_end;
+            int r = 0;  // the first lane whose requests end beyond x
+#pragma unroll
+            for (int i = 16; i; i >>= 1)
+                if (__shfl_sync(FULL, ends, r + i - 1) <= x) r += i;
+            r = min(r, 31);
+            const int64_t end = __shfl_sync(FULL, ends, r);
+            const int len = __shfl_sync(FULL, sr.r.len, r), n = __shfl_sync(FULL, sr.r.n, r);
+            const int r0 = __shfl_sync(FULL, sr.r.r0, r), lo = __shfl_sync(FULL, sr.lo, r);
+            const int seen = __shfl_sync(FULL, sr.seen, r), subs = __shfl_sync(FULL, sr.subs, r);
+            const int groups = __shfl_sync(FULL, sr.groups, r);
+            if (here) {
+                const int64_t off = x - (end - (int64_t)groups * H * (subs + OVER));
+                const int64_t seg = quotient(off, subs + OVER);
+                e.i = (int)(off - seg * (subs + OVER)) - OVER;
+                e.subs = subs;
+                e.h = (int)quotient(seg, groups);
+                e.rg = (int)(seg - (int64_t)e.h * groups);
+                e.len = len;
+                e.n = n;
+                e.r0 = r0;
+                if (e.i >= 0) {
+                    e.tok = lo + e.i * SUB;
+                    const int32_t* table = a.s.table + (int64_t)(bw + r) * a.s.table_stride;
+                    if (e.tok < len && ((e.tok >> sh) + 1) << sh > seen) e.p0 = table[e.tok >> sh];
+                    if (sh == 4 && e.tok + 16 < len && e.tok + 32 > seen) e.p1 = table[(e.tok >> 4) + 1];
+                    if (e.p0 >= a.c.pages) e.p0 = -1;
+                    if (e.p1 >= a.c.pages) e.p1 = -1;
+                    if (sh != 4) e.p1 = e.p0;
+                }
+                todo = false;
+            }
+            if (!__any_sync(FULL, todo) || bw + 32 >= B) break;
+            requests(bw + 32, window_end);
+        }
+        Entry* to = run + (filled + lane) % RUN;
+        const bool keep = lane < FILL && filled + lane < N;
+        __syncwarp();
+        if (keep) *to = e;
+        __syncwarp();
+        filled += FILL;
+        load();  // before the scales, whose addresses also wait for the pages
+        if (keep && e.tok >= 0) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int p = y ? e.p1 : e.p0;
+                if (p < 0) continue;
+                to->ks[y] = a.c.k_scale[(int64_t)p * a.c.scale_stride + e.h];
+                const float vs = a.c.v_scale[(int64_t)p * a.c.scale_stride + e.h];
+                to->vs[y] = vs;
+                if (vs != 0.f) to->lv[y] = __log2f(fabsf(vs));
+            }
+        }
+        __syncwarp();
+    };
+    if (works) {
+        int from = 0;
+        for (int i = lane; i < DEC_WARPS * 32; i += 32) {
+            const uint32_t hit = __ballot_sync(FULL, pre[i] <= x0 && x0 < pre[i + 1]);
+            if (hit) from = (i - lane) + __ffs(hit) - 1;
+        }
+        requests(from * per, pre[from]);
+        fill();
+        if (filled < N) fill();
+    }
 
     // the segment being worked on
     uint32_t qf[C::QSMEM ? 1 : NT][CH][8];  // queries: a thread's chunks of its row
@@ -440,10 +473,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     int last_at = 0;          // the place of its last entry here
 
     for (int k = 0; k < N; ++k) {
-        if (filled < N && filled - k <= RUN - FILL) {
-            fill();
-            load();
-        }
+        if (filled < N && filled - k <= RUN - FILL) fill();
         const Entry& e = run[k % RUN];
         const int tok = e.tok;
         if (tok < 0) continue;
@@ -729,8 +759,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 
     // Segments that go on beyond the warps' runs.  The warps of a CTA that
     // are on the same one add their sums in shared memory (the ring is idle).
-    __shared__ int64_t seg_at[DEC_WARPS];  // place of the segment's first sub-tile, -1: none
-    __shared__ Entry seg_entry[DEC_WARPS];
+    int64_t* seg_at = reinterpret_cast<int64_t*>(smem + C::OFF_AT);  // place of the segment's first sub-tile, -1: none
+    Entry* seg_entry = reinterpret_cast<Entry*>(smem + C::OFF_SEG);
     if (lane == 0) {
         seg_at[warp] = -1;
         if (open) {
@@ -803,8 +833,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             // the worker that begins the segment says who ends it
             const Entry& e = seg_entry[w0];
             const int me = blockIdx.x * wpc + w0;
-            if (tid == 0 && worker_of(at, total, P) == me)
-                d.cuts[me] = {worker_of(at + e.subs - 1, total, P), wpc, e.r0, e.n, e.h, e.rg, {0, 0}};
+            if (tid == 0 && split.worker(at) == me)
+                d.cuts[me] = {split.worker(at + e.subs - 1), wpc, e.r0, e.n, e.h, e.rg, {0, 0}};
         }
         w0 = w1;
     }
@@ -842,19 +872,13 @@ bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
         }))
         return BSP_ERR_CUDA;
     const int grid = h->num_sms * std::min(std::max(per_sm[dev], 1), C::CTAS);
-    kv_decode_kernel<T, DP, NT><<<grid, DEC_WARPS * 32, C::SMEM, s>>>(h->map_k, h->map_v, d);
-    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
-    // the joining kernel may be set up while the other one ends
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)h->num_sms * 4);
-    cfg.blockDim = dim3(JOIN_WARPS * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute early[1];
-    early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<T, DP, NT>, d, grid * DEC_WARPS) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    if (!launch_early(kv_decode_kernel<T, DP, NT>, dim3((unsigned)grid), dim3(DEC_WARPS * 32), C::SMEM, s, h->map_k,
+                      h->map_v, d))
+        return BSP_ERR_CUDA;
+    return launch_early(kv_join_kernel<T, DP, NT>, dim3((unsigned)h->num_sms * 4), dim3(JOIN_WARPS * 32), 0, s, d,
+                        grid * DEC_WARPS)
+               ? BSP_OK
+               : BSP_ERR_CUDA;
 }
 
 template <class T>
