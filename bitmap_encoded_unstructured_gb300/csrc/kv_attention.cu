@@ -43,7 +43,7 @@ constexpr int DEC_WARPS = 4;
 constexpr int SUB = 32;                  // rows of a sub-tile
 constexpr int OVER = 2;                  // sub-tiles a segment's start and end are worth
 constexpr int LEAST = 3;                 // a warp's run is at least this long (more than OVER)
-constexpr int RUN = 32, FILL = 16;       // entries of the run that a warp looks ahead, and fills at a time
+constexpr int RUN = 32, FILL = 16;       // entries of the run that a warp looks ahead, and fills at a time later
 
 template <int DP, int NT>
 struct DecCfg {
@@ -314,17 +314,6 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     if (tid == 0) pre[DEC_WARPS * 32] = total;
     __syncthreads();
 
-    // rows past the step's
-    {
-        const int64_t live = B ? min((int64_t)max(a.s.q_start[B], 0), a.s.rows) : (int64_t)0;
-        const int64_t vec = a.c.dim / 8, all = (a.s.rows - live) * a.heads * vec;
-        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + tid; i < all; i += (int64_t)gridDim.x * blockDim.x) {
-            const int64_t row = live + i / (a.heads * vec), head = i / vec % a.heads;
-            *reinterpret_cast<uint4*>((T*)a.out + row * a.o_row + head * a.o_head + i % vec * 8) = make_uint4(0, 0, 0, 0);
-            if (a.lse && i % vec == 0) a.lse[row * a.heads + head] = -INFINITY;
-        }
-    }
-
     // P workers; fewer than there are warps are spread over the CTAs
     const int P = (int)max((int64_t)1, min((int64_t)gridDim.x * DEC_WARPS, quotient(total, LEAST)));
     const int wpc = min(DEC_WARPS, (P + (int)gridDim.x - 1) / (int)gridDim.x);
@@ -334,25 +323,6 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const int64_t x0 = works ? split.begin(worker) : 0;
     const int N = works ? (int)(split.begin(worker + 1) - x0) : 0;
 
-    // requests 32 at a time, one per lane: what lies before them, and up to
-    // each lane's end
-    int bw = 0;
-    int64_t before = 0, ends = 0;
-    Share sr = {};
-    auto requests = [&](int from, int64_t at) {
-        bw = from;
-        before = at;
-        Request r = {0, 0, 0};
-        if (bw + lane < B) r = request_of(a.s, sh, bw + lane);
-        sr = share_of<Q>(d, r);
-        ends = bw + lane < B ? sr.cost(H) : 0;
-#pragma unroll
-        for (int i = 1; i < 32; i <<= 1) {
-            const int64_t o = __shfl_up_sync(FULL, ends, i);
-            if (lane >= i) ends += o;
-        }
-        ends += before;
-    };
     int filled = 0;
     uint32_t stage = 0, phase = 0, next = 0;  // ring: stage being read, stage of the next load
     int ahead = 0, loading = 0;               // entries looked at for loading; loads in flight
@@ -386,56 +356,48 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
         __syncwarp();
     };
-    auto fill = [&]() {  // the next FILL entries of the run
-        const int64_t x = x0 + filled + lane;
-        bool todo = lane < FILL && filled + lane < N;
+    auto fill = [&](int count) {  // the next entries of the run, one per lane
+        const bool keep = lane < count && filled + lane < N;
         Entry e;
         e.tok = e.p0 = e.p1 = -1;
         e.ks[0] = e.ks[1] = e.vs[0] = e.vs[1] = 0.f;
         e.lv[0] = e.lv[1] = NONE;
-        while (true) {
-            const int64_t window_end = __shfl_sync(FULL, ends, 31);
-            const bool here = todo && x < window_end;
-            int r = 0;  // the first lane whose requests end beyond x
+        if (keep) {
+            const int64_t x = x0 + filled + lane;
+            int t = 0;  // the thread whose requests hold place x, then the request
 #pragma unroll
-            for (int i = 16; i; i >>= 1)
-                if (__shfl_sync(FULL, ends, r + i - 1) <= x) r += i;
-            r = min(r, 31);
-            const int64_t end = __shfl_sync(FULL, ends, r);
-            const int len = __shfl_sync(FULL, sr.r.len, r), n = __shfl_sync(FULL, sr.r.n, r);
-            const int r0 = __shfl_sync(FULL, sr.r.r0, r), lo = __shfl_sync(FULL, sr.lo, r);
-            const int seen = __shfl_sync(FULL, sr.seen, r), subs = __shfl_sync(FULL, sr.subs, r);
-            const int groups = __shfl_sync(FULL, sr.groups, r);
-            if (here) {
-                const int64_t off = x - (end - (int64_t)groups * H * (subs + OVER));
-                const int64_t seg = quotient(off, subs + OVER);
-                e.i = (int)(off - seg * (subs + OVER)) - OVER;
-                e.subs = subs;
-                e.h = (int)quotient(seg, groups);
-                e.rg = (int)(seg - (int64_t)e.h * groups);
-                e.len = len;
-                e.n = n;
-                e.r0 = r0;
-                if (e.i >= 0) {
-                    e.tok = lo + e.i * SUB;
-                    const int32_t* table = a.s.table + (int64_t)(bw + r) * a.s.table_stride;
-                    if (e.tok < len && ((e.tok >> sh) + 1) << sh > seen) e.p0 = table[e.tok >> sh];
-                    if (sh == 4 && e.tok + 16 < len && e.tok + 32 > seen) e.p1 = table[(e.tok >> 4) + 1];
-                    if (e.p0 >= a.c.pages) e.p0 = -1;
-                    if (e.p1 >= a.c.pages) e.p1 = -1;
-                    if (sh != 4) e.p1 = e.p0;
-                }
-                todo = false;
+            for (int i = DEC_WARPS * 16; i; i >>= 1)
+                if (pre[t + i] <= x) t += i;
+            int b = t * per;
+            int64_t off = x - pre[t];
+            Share s = share_of<Q>(d, request_of(a.s, sh, b));
+            while (off >= s.cost(H) && b + 1 < B) {
+                off -= s.cost(H);
+                s = share_of<Q>(d, request_of(a.s, sh, ++b));
             }
-            if (!__any_sync(FULL, todo) || bw + 32 >= B) break;
-            requests(bw + 32, window_end);
+            const int64_t seg = quotient(off, s.subs + OVER);
+            e.i = (int)(off - seg * (s.subs + OVER)) - OVER;
+            e.subs = s.subs;
+            e.h = (int)quotient(seg, max(s.groups, 1));
+            e.rg = (int)(seg - (int64_t)e.h * s.groups);
+            e.len = s.r.len;
+            e.n = s.r.n;
+            e.r0 = s.r.r0;
+            if (e.i >= 0 && e.h < H) {
+                e.tok = s.lo + e.i * SUB;
+                const int32_t* table = a.s.table + (int64_t)b * a.s.table_stride;
+                if (e.tok < s.r.len && ((e.tok >> sh) + 1) << sh > s.seen) e.p0 = table[e.tok >> sh];
+                if (sh == 4 && e.tok + 16 < s.r.len && e.tok + 32 > s.seen) e.p1 = table[(e.tok >> 4) + 1];
+                if (e.p0 >= a.c.pages) e.p0 = -1;
+                if (e.p1 >= a.c.pages) e.p1 = -1;
+                if (sh != 4) e.p1 = e.p0;
+            }
         }
         Entry* to = run + (filled + lane) % RUN;
-        const bool keep = lane < FILL && filled + lane < N;
         __syncwarp();
         if (keep) *to = e;
         __syncwarp();
-        filled += FILL;
+        filled += count;
         load();  // before the scales, whose addresses also wait for the pages
         if (keep && e.tok >= 0) {
 #pragma unroll
@@ -450,16 +412,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
         __syncwarp();
     };
-    if (works) {
-        int from = 0;
-        for (int i = lane; i < DEC_WARPS * 32; i += 32) {
-            const uint32_t hit = __ballot_sync(FULL, pre[i] <= x0 && x0 < pre[i + 1]);
-            if (hit) from = (i - lane) + __ffs(hit) - 1;
-        }
-        requests(from * per, pre[from]);
-        fill();
-        if (filled < N) fill();
-    }
+    if (works) fill(RUN);
 
     // the segment being worked on
     uint32_t qf[C::QSMEM ? 1 : NT][CH][8];  // queries: a thread's chunks of its row
@@ -473,7 +426,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     int last_at = 0;          // the place of its last entry here
 
     for (int k = 0; k < N; ++k) {
-        if (filled < N && filled - k <= RUN - FILL) fill();
+        if (filled < N && filled - k <= RUN - FILL) fill(FILL);
         const Entry& e = run[k % RUN];
         const int tok = e.tok;
         if (tok < 0) continue;
@@ -756,6 +709,17 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     }
     if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel, as SMs fall free
+
+    // rows past the step's
+    {
+        const int64_t live = B ? min((int64_t)max(a.s.q_start[B], 0), a.s.rows) : (int64_t)0;
+        const int64_t vec = a.c.dim / 8, all = (a.s.rows - live) * a.heads * vec;
+        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + tid; i < all; i += (int64_t)gridDim.x * blockDim.x) {
+            const int64_t row = live + i / (a.heads * vec), head = i / vec % a.heads;
+            *reinterpret_cast<uint4*>((T*)a.out + row * a.o_row + head * a.o_head + i % vec * 8) = make_uint4(0, 0, 0, 0);
+            if (a.lse && i % vec == 0) a.lse[row * a.heads + head] = -INFINITY;
+        }
+    }
 
     // Segments that go on beyond the warps' runs.  The warps of a CTA that
     // are on the same one add their sums in shared memory (the ring is idle).
