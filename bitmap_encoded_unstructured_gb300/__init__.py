@@ -168,6 +168,8 @@ def lib() -> C.CDLL:
     global _lib
     if _use_test:
         return testing_lib()
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             _lib = _load(LIB_PATH, SIGNATURES)
@@ -631,13 +633,26 @@ class UnionMatrix:
         return Y
 
 
+_ROW_DTYPES = {}  # torch dtype -> BSP_FP16 / BSP_BF16
+
+
 def _row_dtype(dtype):
-    import torch
-    if dtype is torch.float16:
-        return BSP_FP16
-    if dtype is torch.bfloat16:
-        return BSP_BF16
-    raise TypeError("rows must be float16 or bfloat16")
+    if not _ROW_DTYPES:
+        import torch
+        _ROW_DTYPES.update({torch.float16: BSP_FP16, torch.bfloat16: BSP_BF16})
+    try:
+        return _ROW_DTYPES[dtype]
+    except KeyError:
+        raise TypeError("rows must be float16 or bfloat16") from None
+
+
+def _raw_stream(stream, index: int):
+    """The stream's handle; None: the device's current stream (read without
+    building a Stream object, which costs as much as a launch)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _int32(name, t, shape, device):
@@ -721,6 +736,7 @@ class KvCache:
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.page, self.dim = k.shape
         self.device = k.device
+        self._index = k.get_device()
         d = bsp_kv_desc_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), self.pages, self.heads,
                           self.page, self.dim, k.stride(0), k.stride(1), k.stride(2), k_scale.stride(0))
         h = C.c_void_p()
@@ -761,59 +777,69 @@ class KvCache:
         served; ``tokens`` is the row capacity of the step.  The step also
         carries ``granted``, ``slots``, ``positions`` and the new
         ``free_count``."""
-        batch, width = block_table.shape
-        dev = block_table.device
-        step = KvStep.empty(batch, tokens, dev) if out is None else out
+        step = KvStep.empty(block_table.shape[0], tokens, block_table.device) if out is None else out
         if step.block_table is not block_table:
             step._bind(block_table, max_new)
-        step._c.max_new = int(max_new)
-        if step.slots is None or step.slots.shape[0] != tokens or step._c.batch != batch:
-            raise ValueError("out does not have this batch and these tokens (KvStep.empty)")
+        c = step._c
+        c.max_new = max_new
+        batch, dev = c.batch, step.device
+        if step.slots is None or step.slots.shape[0] != tokens:
+            raise ValueError("out does not have these tokens (KvStep.empty)")
         seq_len, q_start, granted, slots, positions, count = step._out
-        _check("bsp_kv_plan", lib().bsp_kv_plan(
+        pages = free_list.shape
+        st = lib().bsp_kv_plan(
             self.h, _int32("ctx_len", ctx_len, (batch,), dev), _int32("new_len", new_len, (batch,), dev), batch,
-            step._c.block_table, width, step._c.table_stride,
-            _int32("free_list", free_list, free_list.shape[:1], dev), free_list.shape[0],
+            c.block_table, c.width, c.table_stride, _int32("free_list", free_list, pages[:1], dev), pages[0],
             _int32("free_count", free_count, (1,), dev), tokens, seq_len, q_start, granted, slots, positions, count,
-            _stream(stream)))
+            _raw_stream(stream, self._index))
+        if st:
+            raise BspError("bsp_kv_plan", st)
         return step
 
     def _rows(self, name, x, heads=None):
-        """(pointer, row stride, head stride) of rows [n][heads][dim]."""
-        shape = x.shape
-        if (x.device != self.device or len(shape) != 3 or shape[2] != self.dim or (heads and shape[1] != heads)
-                or (shape[2] > 1 and x.stride(2) != 1)):
+        """(pointer, rows, heads, row stride, head stride) of rows [n][heads][dim]."""
+        shape, strides = x.shape, x.stride()
+        if (len(shape) != 3 or shape[2] != self.dim or strides[2] != 1 or (heads and shape[1] != heads)
+                or x.get_device() != self._index):
             raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, dim contiguous")
-        return x.data_ptr(), x.stride(0), x.stride(1)
+        return x.data_ptr(), shape[0], shape[1], strides[0], strides[1]
 
     def append(self, step, k, v, stream=None):
         """Quantise new rows ``k``, ``v`` [rows][heads][dim] (float16 or
         bfloat16, views of a QKV output allowed) into the step's pages."""
         dt = _row_dtype(k.dtype)
-        if v.dtype is not k.dtype or v.shape != k.shape:
+        pk, rows, _, kr, kh = self._rows("k", k, self.heads)
+        pv, vrows, _, vr, vh = self._rows("v", v, self.heads)
+        if v.dtype is not k.dtype or vrows != rows:
             raise ValueError("k and v must have the same shape and type")
-        pk, kr, kh = self._rows("k", k, self.heads)
-        pv, vr, vh = self._rows("v", v, self.heads)
-        _check("bsp_kv_append", lib().bsp_kv_append(self.h, step._ref, pk, pv, dt, k.shape[0], kr, kh, vr, vh,
-                                                    _stream(stream)))
+        st = lib().bsp_kv_append(self.h, step._ref, pk, pv, dt, rows, kr, kh, vr, vh, _raw_stream(stream, self._index))
+        if st:
+            raise BspError("bsp_kv_append", st)
 
     def read(self, slots, dtype=None, out=None, stream=None):
         """Cached rows of int64 ``slots``: (k, v) [n][heads][dim]; zeros for a
         slot outside the cache."""
         import torch
-        if slots.dtype is not torch.int64 or slots.device != self.device or slots.dim() != 1 or not slots.is_contiguous():
+        if (slots.dtype is not torch.int64 or slots.get_device() != self._index or slots.dim() != 1
+                or not slots.is_contiguous()):
             raise ValueError(f"slots must be a contiguous int64 vector on {self.device}")
         n = slots.shape[0]
         dtype = torch.float16 if dtype is None else dtype
         dt = _row_dtype(dtype)
         if out is None:
-            out = torch.empty((2, n, self.heads, self.dim), dtype=dtype, device=self.device).unbind(0)
-        k, v = out
-        for t in (k, v):
-            if t.dtype is not dtype or t.shape != (n, self.heads, self.dim) or not t.is_contiguous():
-                raise ValueError("out must be two contiguous tensors [n][heads][dim] of the type")
-        _check("bsp_kv_read", lib().bsp_kv_read(self.h, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt,
-                                                _stream(stream)))
+            both = torch.empty((2, n, self.heads, self.dim), dtype=dtype, device=self.device)
+            k, v = both.unbind(0)
+            pk = both.data_ptr()
+            pv = pk + n * self.heads * self.dim * 2
+        else:
+            k, v = out
+            for t in (k, v):
+                if t.dtype is not dtype or t.shape != (n, self.heads, self.dim) or not t.is_contiguous():
+                    raise ValueError("out must be two contiguous tensors [n][heads][dim] of the type")
+            pk, pv = k.data_ptr(), v.data_ptr()
+        st = lib().bsp_kv_read(self.h, slots.data_ptr(), n, pk, pv, dt, _raw_stream(stream, self._index))
+        if st:
+            raise BspError("bsp_kv_read", st)
         return k, v
 
     def attention(self, step, q, scale=None, window: int = 0, out=None, with_lse: bool = False, stream=None):
@@ -824,15 +850,18 @@ class KvCache:
         [rows][heads]."""
         import torch
         dt = _row_dtype(q.dtype)
-        pq, qr, qh = self._rows("q", q)
-        rows, heads = q.shape[0], q.shape[1]
+        pq, rows, heads, qr, qh = self._rows("q", q)
         if out is None:
             out = torch.empty((rows, heads, self.dim), dtype=q.dtype, device=self.device)
-        elif out.dtype is not q.dtype or out.shape != q.shape:
-            raise ValueError("out must have q's shape and type")
-        po, orow, oh = self._rows("out", out)
+            po, orow, oh = out.data_ptr(), heads * self.dim, self.dim
+        else:
+            if out.dtype is not q.dtype or out.shape != q.shape:
+                raise ValueError("out must have q's shape and type")
+            po, _, _, orow, oh = self._rows("out", out)
         lse = torch.empty((rows, heads), dtype=torch.float32, device=self.device) if with_lse else None
-        _check("bsp_kv_attention", lib().bsp_kv_attention(
+        st = lib().bsp_kv_attention(
             self.h, step._ref, pq, dt, rows, heads, qr, qh, self.dim ** -0.5 if scale is None else scale, window, po,
-            orow, oh, lse.data_ptr() if with_lse else None, _stream(stream)))
+            orow, oh, lse.data_ptr() if with_lse else None, _raw_stream(stream, self._index))
+        if st:
+            raise BspError("bsp_kv_attention", st)
         return (out, lse) if with_lse else out
