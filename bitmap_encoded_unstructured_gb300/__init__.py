@@ -827,17 +827,16 @@ class KvCache:
         dtype = torch.float16 if dtype is None else dtype
         dt = _row_dtype(dtype)
         if out is None:
-            both = torch.empty((2, n, self.heads, self.dim), dtype=dtype, device=self.device)
-            k, v = both.unbind(0)
-            pk = both.data_ptr()
-            pv = pk + n * self.heads * self.dim * 2
+            shape = (n, self.heads, self.dim)  # two allocations cost less than two views of one
+            k = torch.empty(shape, dtype=dtype, device=self.device)
+            v = torch.empty(shape, dtype=dtype, device=self.device)
         else:
             k, v = out
             for t in (k, v):
                 if t.dtype is not dtype or t.shape != (n, self.heads, self.dim) or not t.is_contiguous():
                     raise ValueError("out must be two contiguous tensors [n][heads][dim] of the type")
-            pk, pv = k.data_ptr(), v.data_ptr()
-        st = lib().bsp_kv_read(self.h, slots.data_ptr(), n, pk, pv, dt, _raw_stream(stream, self._index))
+        st = lib().bsp_kv_read(self.h, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt,
+                               _raw_stream(stream, self._index))
         if st:
             raise BspError("bsp_kv_read", st)
         return k, v

@@ -37,6 +37,10 @@ constexpr int GROUPS = TOK / 16;
 constexpr int NC = 4, NF = 3, NM = 4;  // rings: codes, fp16 tiles, scales
 constexpr int THREADS = 512;
 constexpr uint32_t kSleepNs = 200;     // suspend hint of a waiting poll
+// Registers of a thread after the roles part, from 128 of each at launch: the
+// softmax keeps a row of 128 logits.
+constexpr int REG_CONTROL = 48, REG_CONVERT = 48, REG_SOFTMAX = 208;
+static_assert(REG_CONTROL + REG_CONVERT + 2 * REG_SOFTMAX == 4 * 128, "shares of the launch's registers");
 
 template <int DP>
 struct Cfg {
@@ -49,7 +53,7 @@ struct Cfg {
     static constexpr int OFF_META = OFF_C + NC * CT;    // per scale slot: ks, vs, log2 vs [8] each, mask
     static constexpr int META = 3 * GROUPS + 4;         // floats
     static constexpr int OFF_BAR = OFF_META + NM * META * 4;
-    static constexpr int NBAR = 2 * NC + 2 * NF + NM + 1 + 3 * 2 + 1;
+    static constexpr int NBAR = 2 * NC + 2 * NF + NM + 1 + 3 * 2 + 2;
     static constexpr int END = OFF_BAR + NBAR * 8 + 16;
     // one CTA per SM: it may take all of the tensor memory
     static constexpr int SMEM = (END > 120 * 1024 ? END : 120 * 1024) + 1024;
@@ -116,8 +120,9 @@ __device__ __forceinline__ void commit(uint64_t* bar)
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-// 32 consecutive tensor-memory columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32])
+// 32 consecutive tensor-memory columns of this thread's lane; they are there
+// after tmem_wait_ld().
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -128,10 +133,49 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t (&r)[32])
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(at));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
+// The loaded registers pass through, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_wait_ld(uint32_t* r, int n)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < n; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Two fp32 at a time.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r)
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -141,7 +185,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16])
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r)
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -206,7 +250,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     uint64_t* p_full = s_full + 2;
     uint64_t* o_done = p_full + 2;
     uint64_t* drain = o_done + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* read = drain + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(read + 1);
     float* meta = reinterpret_cast<float*>(smem + C::OFF_META);
 
     if (warp == 1) {
@@ -234,6 +279,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             bspx::mbar_init(o_done + i, 1);
         }
         bspx::mbar_init(drain, 1);
+        bspx::mbar_init(read, 8);
         bspx::fence_mbar_init();
     }
     tc_before();
@@ -242,6 +288,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const uint32_t tmem = *tmem_slot;
     bool failed = false;
 
+    if (warp < 4) fewer_registers<REG_CONTROL>();
     if (warp == 0) {
         // ---------------- codes and scales: lane l < 8 looks after rows 16 l ..
         const int32_t* table = a.s.table + (int64_t)b * a.s.table_stride;
@@ -296,7 +343,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
         for (int i = std::max(0, n - NC); i < n; ++i)  // no copy may land after the CTA is gone
             bspx::mbar_wait_bounded(c_full + i % NC, (i / NC) & 1, cap);
-    } else if (warp == 1) {
+        if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
+        return;
+    }
+    if (warp == 1) {
         // ---------------- MMA issuer
         const int ks_steps = dim / 16;
         const uint32_t q_at = bspx::smem_u32(smem), f_at = bspx::smem_u32(smem + C::OFF_F);
@@ -355,7 +405,21 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 }
             }
         }
-    } else if (warp >= 4 && warp < 8) {
+        // no product in flight (after a wait ran out) and nobody reading when
+        // the tensor memory is given back
+        if (lane == 0) commit(drain);
+        __syncwarp();
+        if (!wait(drain, 0, cap)) failed = true;
+        if (!wait(read, 0, cap)) failed = true;
+        if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
+        tc_after();
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        return;
+    }
+    if (warp < 4) return;
+    if (warp < 8) {
+        fewer_registers<REG_CONVERT>();
         // ---------------- codes -> fp16.  A thread's chunk of 16 codes and the
         // rows of its eight-lane phase (r and r ^ 5) are such that both the
         // loads and the two stores of a phase fall into distinct banks.
@@ -392,7 +456,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 bspx::mbar_arrive(c_empty + from);
             }
         }
-    } else if (warp >= 8) {
+        if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
+        return;
+    }
+    more_registers<REG_SOFTMAX>();
+    {
         // ---------------- softmax of one row per thread
         const int t = (warp - 8) >> 2, quad = warp & 3;
         const int tr = 32 * quad + lane;                     // row of the tile
@@ -459,39 +527,50 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             const bool edge = tok + TOK - 1 > tile_pos0 || (a.window && tok <= tile_pos1 - a.window) || there != 0xFFu;
             // columns lo .. hi of this tile are this row's
             const int hi = pos - tok, lo = (a.window ? max(pos - a.window + 1, 0) : 0) - tok;
-            uint32_t x[32];
+            uint32_t x[TOK];
+            __syncwarp();
+#pragma unroll
+            for (int cb = 0; cb < TOK; cb += 32) tmem_ld32(s_at + cb, x + cb);
+            float kf[GROUPS];
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) kf[g] = fmaxf(mt[g] * unit_scale, 1e-30f);  // a masked -inf stays one
+            tmem_wait_ld(x, TOK);
+            if (edge) {
+#pragma unroll
+                for (int w = 0; w < TOK / 32; ++w) {
+                    // bits lo .. hi of this word, and the pages that are there
+                    const int h = hi - 32 * w, o = lo - 32 * w;
+                    uint32_t see = h < 0 ? 0u : h >= 31 ? FULL : (2u << h) - 1u;
+                    see &= o <= 0 ? FULL : o >= 32 ? 0u : FULL << o;
+                    see &= ((there >> (2 * w)) & 1u ? 0x0000FFFFu : 0u) | ((there >> (2 * w + 1)) & 1u ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        asm volatile("{\n\t.reg .pred p;\n\t.reg .b32 t;\n\tand.b32 t, %1, %2;\n\t"
+                                     "setp.eq.u32 p, t, 0;\n\t@p mov.b32 %0, 0xFF800000;\n\t}"
+                                     : "+r"(x[32 * w + i])
+                                     : "r"(see), "r"(1u << i));  // -inf
+                }
+            }
             // largest logits
             float top = -INFINITY, topw = -INFINITY;
 #pragma unroll
-            for (int cb = 0; cb < TOK; cb += 32) {
-                __syncwarp();
-                tmem_ld32(s_at + cb, x);
+            for (int g = 0; g < GROUPS; ++g) {
+                float big[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float big = -INFINITY;
-                    if (edge) {
-                        const bool see = (there >> (cb / 16 + g)) & 1;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int col = cb + 16 * g + i;
-                            if (see && col <= hi && col >= lo) big = fmaxf(big, __uint_as_float(x[16 * g + i]));
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) big = fmaxf(big, __uint_as_float(x[16 * g + i]));
-                    }
-                    const float kf = mt[cb / 16 + g] * unit_scale;
-                    big = big == -INFINITY ? big : big * kf;
-                    top = fmaxf(top, big);
-                    topw = fmaxf(topw, big + mt[2 * GROUPS + cb / 16 + g]);
+                for (int i = 0; i < 16; i += 4) {
+                    big[0] = fmaxf(fmaxf(big[0], __uint_as_float(x[16 * g + i])), __uint_as_float(x[16 * g + i + 1]));
+                    big[1] = fmaxf(fmaxf(big[1], __uint_as_float(x[16 * g + i + 2])), __uint_as_float(x[16 * g + i + 3]));
                 }
+                const float b = fmaxf(big[0], big[1]) * kf[g];
+                top = fmaxf(top, b);
+                topw = fmaxf(topw, b + mt[2 * GROUPS + g]);
             }
             if (__any_sync(FULL, top > m + LAZY || topw > mw + LAZY)) {
                 top = fmaxf(top, m);
                 topw = fmaxf(topw, mw);
-                l *= ex2(m - top);
+                const float fade = ex2(m - top), back = ex2(mw - topw);
+                l *= fade;
                 if (j) {  // O is whole once the product of the tile before is done
-                    const float back = ex2(mw - topw);
                     if (!wait(o_done + t, (j - 1) & 1, cap)) {
                         failed = true;
                         break;
@@ -501,6 +580,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                         uint32_t o[32];
                         __syncwarp();
                         tmem_ld32(o_at + cb, o);
+                        tmem_wait_ld(o, 32);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * back);
                         tmem_st32(o_at + cb, o);
@@ -510,31 +590,32 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 mw = topw;
                 lift = ex2(fminf(m - mw, 120.f)) * LIFT;
             }
-            // weights
+            // weights, two at a time, over the logits' registers and columns
+            const uint64_t minus = pair(-m, -m);
+            uint64_t part[4] = {0, 0, 0, 0};
+            uint32_t y[16];
 #pragma unroll
-            for (int cb = 0; cb < TOK; cb += 32) {
-                __syncwarp();
-                tmem_ld32(s_at + cb, x);
-                uint32_t y[16];
+            for (int g = 0; g < GROUPS; ++g) {
+                const float v = mt[GROUPS + g] * lift;
+                const uint64_t kk = pair(kf[g], kf[g]), vv = pair(v, v);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float kf = mt[cb / 16 + g] * unit_scale, vf = mt[GROUPS + cb / 16 + g] * lift;
-                    const bool see = (there >> (cb / 16 + g)) & 1;
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float z[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int col = cb + 16 * g + i + e;
-                            z[e] = fmaf(__uint_as_float(x[16 * g + i + e]), kf, -m);
-                            if (edge && !(see && col <= hi && col >= lo)) z[e] = -INFINITY;
-                            z[e] = ex2(z[e]);
-                            l += z[e];
-                        }
-                        y[8 * g + i / 2] = h2bits(__floats2half2_rn(z[0] * vf, z[1] * vf));
-                    }
+                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                    float a0, a1;
+                    unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kk, minus), a0, a1);
+                    const uint64_t p = pair(ex2(a0), ex2(a1));
+                    part[(i / 2) & 3] = add2(part[(i / 2) & 3], p);
+                    unpair(mul2(p, vv), a0, a1);
+                    y[(i / 2) % 16] = h2bits(__floats2half2_rn(a0, a1));
                 }
-                tmem_st16(s_at + cb / 2, y);
+                if (g & 1) {
+                    __syncwarp();
+                    tmem_st16(s_at + 8 * (g - 1), y);
+                }
+            }
+            {
+                float a0, a1;
+                unpair(add2(add2(part[0], part[1]), add2(part[2], part[3])), a0, a1);
+                l += a0 + a1;
             }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_before();
@@ -550,7 +631,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             for (int cb = 0; cb < dim; cb += 32) {
                 uint32_t x[32];
                 __syncwarp();
-                if (my_tiles) tmem_ld32(o_at + cb, x);
+                if (my_tiles) {
+                    tmem_ld32(o_at + cb, x);
+                    tmem_wait_ld(x, 32);
+                }
 #pragma unroll
                 for (int i = 0; i < 32; i += 8) {
                     alignas(16) T y[8];
@@ -565,19 +649,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
     }
 
-    if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
-    if (warp == 1) {  // no product in flight (after a wait ran out) when shared and tensor memory are given back
-        if (lane == 0) commit(drain);
-        __syncwarp();
-        wait(drain, 0, cap);
-    }
     tc_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_after();
-        __syncwarp();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
-    }
+    __syncwarp();
+    if (lane == 0) bspx::mbar_arrive(read);
+    if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
 }
 
 template <class T, int DP>
