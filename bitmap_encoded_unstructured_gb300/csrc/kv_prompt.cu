@@ -15,12 +15,14 @@
 // Warps: 0 loads codes (TMA boxes of the paged cache) and scales; 1 issues
 // the MMAs; 4-7 turn codes into fp16 tiles; 8-11 and 12-15 are the softmax
 // of row tiles 0 and 1 (a warp reaches the 32 tensor-memory lanes 32 (w % 4)
-// .. + 31).  Rings: codes (K and V tiles in turn, four deep), fp16 tiles
-// (three deep: V of a tile and K of the next are live while the next V is
-// made).  Both fp16 tiles have one layout, rows of 64 dims swizzled by 128
-// bytes: K-major for the first product, MN-major for the second.
+// .. + 31).  Rings of tiles in the order the products need them, K0 V0 K1 V1
+// ..: codes (four deep) and fp16 tiles (three: V of a tile and K of the next
+// are live while the next V is made).  Both fp16 tiles have one layout, rows
+// of 64 dims swizzled by 128 bytes: K-major for the first product, MN-major
+// for the second.
 // Tensor memory: S0, S1 (128 fp32 columns each; W takes the lower half of
-// its own S), O0, O1.
+// its own S), O0, O1.  Products of one thread run in order, so the next S
+// may be asked for right after the product that reads W.
 #include "bsp_kv.cuh"
 
 #include <algorithm>
@@ -34,9 +36,8 @@ constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr int ROWS = 256;      // query rows of a CTA
 constexpr int TOK = 128;       // cached rows of a tile
 constexpr int GROUPS = TOK / 16;
-constexpr int NC = 4, NF = 3, NM = 4;  // rings: codes, fp16 tiles, scales
+constexpr int NC = 4, NF = 3, NM = 8;  // rings: codes, fp16 tiles, scales
 constexpr int THREADS = 512;
-constexpr uint32_t kSleepNs = 200;     // suspend hint of a waiting poll
 // Registers of a thread after the roles part, from 128 of each at launch: the
 // softmax keeps a row of 128 logits.
 constexpr int REG_CONTROL = 48, REG_CONVERT = 48, REG_SOFTMAX = 208;
@@ -44,8 +45,8 @@ static_assert(REG_CONTROL + REG_CONVERT + 2 * REG_SOFTMAX == 4 * 128, "shares of
 
 template <int DP>
 struct Cfg {
-    static constexpr int BLK = TOK * 128;               // 128 rows x 64 dims fp16 (or a Q block)
-    static constexpr int QT = BLK * (DP / 64);          // Q of a row tile
+    static constexpr int QBLK = 128 * 128, BLK = TOK * 128;  // 64 dims of a row tile's Q, of an fp16 tile
+    static constexpr int QT = QBLK * (DP / 64);         // Q of a row tile
     static constexpr int FT = BLK * (DP / 64);          // fp16 K or V tile
     static constexpr int CT = TOK * DP;                 // codes of a tile
     static constexpr int OFF_F = 2 * QT;
@@ -200,7 +201,7 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r)
 // The whole warp waits; false if the wait ran out.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t cap)
 {
-    return __all_sync(FULL, bspx::mbar_wait_sleep(bar, parity, cap, kSleepNs));
+    return __all_sync(FULL, bspx::mbar_wait_bounded(bar, parity, cap));
 }
 
 template <class T, int DP>
@@ -302,34 +303,36 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             }
             return p;
         };
-        int p = page_of(0);
-        int n = 0;  // tiles issued, K and V counted apart
-        for (int j = 0; j < tiles && !failed; ++j) {
-            const int next = page_of(j + 1);
-            const int tok = t0 + j * TOK + 16 * lane;
+        int n = 0;  // tiles issued
+        auto load = [&](const CUtensorMap* map, int j, int p) {
+            const int slot = n % NC;
+            if (failed || (n >= NC && !wait(c_empty + slot, (n / NC - 1) & 1, cap))) {
+                failed = true;
+                return;
+            }
             const bool mine = p >= 0 && (box == 16 || (lane & 1) == 0);
             const uint32_t bytes = __popc(__ballot_sync(FULL, mine)) * box * DP;
-            for (int v = 0; v < 2; ++v, ++n) {
-                const int slot = n % NC;
-                if (n >= NC && !wait(c_empty + slot, (n / NC - 1) & 1, cap)) {
-                    failed = true;
-                    break;
-                }
-                if (lane == 0) {
-                    if (bytes) bspx::mbar_arrive_expect_tx(c_full + slot, bytes);
-                    else bspx::mbar_arrive(c_full + slot);
-                }
-                __syncwarp();
-                if (mine)
-                    tma_load_4d(smem + C::OFF_C + slot * C::CT + 16 * lane * DP, v ? &map_v : &map_k, 0,
-                                tok & ((1 << sh) - 1), h, p, c_full + slot);
+            if (lane == 0) {
+                if (bytes) bspx::mbar_arrive_expect_tx(c_full + slot, bytes);
+                else bspx::mbar_arrive(c_full + slot);
             }
-            if (failed) break;
-            // slot j % NM was last read for tile j - NM, whose products are done:
-            // the codes of tile j could not have been asked for otherwise
+            __syncwarp();
+            if (mine)
+                tma_load_4d(smem + C::OFF_C + slot * C::CT + 16 * lane * DP, map, 0,
+                            (t0 + j * TOK + 16 * lane) & ((1 << sh) - 1), h, p, c_full + slot);
+            ++n;
+        };
+        // what is looked up for a tile travels ahead of its loads, so that no
+        // step waits for the table or the scales
+        auto scale_of = [&](const float* scale, int p) {
+            return p >= 0 ? scale[(int64_t)p * a.c.scale_stride + h] : 0.f;
+        };
+        auto load_k = [&](int j, int p, float ks, float vs) {
+            load(&map_k, j, p);
+            if (failed) return;
+            // slot j % NM was last read for tile j - NM, whose products are
+            // done: the codes of tile j could not have been asked for otherwise
             float* mt = meta + (j % NM) * C::META;
-            const float ks = p >= 0 ? a.c.k_scale[(int64_t)p * a.c.scale_stride + h] : 0.f;
-            const float vs = p >= 0 ? a.c.v_scale[(int64_t)p * a.c.scale_stride + h] : 0.f;
             const uint32_t there = __ballot_sync(FULL, p >= 0);
             if (lane < GROUPS) {
                 mt[lane] = ks;
@@ -339,7 +342,22 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             if (lane == 0) reinterpret_cast<uint32_t*>(mt)[3 * GROUPS] = there;
             __syncwarp();
             if (lane == 0) bspx::mbar_arrive(m_full + j % NM);
-            p = next;
+        };
+        int p0 = page_of(0), p1 = page_of(1), p2 = page_of(2);  // of tiles j .. j + 2
+        float ks0 = scale_of(a.c.k_scale, p0), vs0 = scale_of(a.c.v_scale, p0);  // of tiles j, j + 1
+        float ks1 = scale_of(a.c.k_scale, p1), vs1 = scale_of(a.c.v_scale, p1);
+        for (int j = 0; j < tiles && !failed; ++j) {
+            const int p3 = page_of(j + 3);
+            const float ks2 = scale_of(a.c.k_scale, p2), vs2 = scale_of(a.c.v_scale, p2);
+            load_k(j, p0, ks0, vs0);
+            load(&map_v, j, p0);
+            p0 = p1;
+            p1 = p2;
+            p2 = p3;
+            ks0 = ks1;
+            vs0 = vs1;
+            ks1 = ks2;
+            vs1 = vs2;
         }
         for (int i = std::max(0, n - NC); i < n; ++i)  // no copy may land after the CTA is gone
             bspx::mbar_wait_bounded(c_full + i % NC, (i / NC) & 1, cap);
@@ -347,64 +365,73 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         return;
     }
     if (warp == 1) {
-        // ---------------- MMA issuer
-        const int ks_steps = dim / 16;
-        const uint32_t q_at = bspx::smem_u32(smem), f_at = bspx::smem_u32(smem + C::OFF_F);
-        const uint32_t id_s = idesc(TOK, false), id_o = idesc(dim, true);
-        auto product_s = [&](int t, int n) {  // S of row tile t from K tile n of the fp16 ring
-            if (lane == 0) {
-                for (int k = 0; k < ks_steps; ++k) {
-                    const uint32_t at = (k >> 2) * C::BLK + (k & 3) * 32;
-                    mma_ss(tmem + t * TOK, smem_desc(q_at + t * C::QT + at, 16),
-                           smem_desc(f_at + (n % NF) * C::FT + at, 16), id_s, k ? 1u : 0u);
-                }
+        // ---------------- MMA issuer: one thread, so that a step costs little
+        // beside its products
+        if (lane == 0 && tiles) {
+            const uint64_t q_desc = smem_desc(bspx::smem_u32(smem), 16);
+            const uint64_t k_desc = smem_desc(bspx::smem_u32(smem + C::OFF_F), 16);
+            const uint64_t v_desc = smem_desc(bspx::smem_u32(smem + C::OFF_F), C::BLK);
+            const uint32_t id_s = idesc(TOK, false), id_o = idesc(dim, true);
+            auto ready = [&](uint64_t* bar, uint32_t parity) {
+                if (!bspx::mbar_wait_bounded(bar, parity, cap)) failed = true;
+                tc_after();
+                return !failed;
+            };
+            auto product_s = [&](int t, int slot) {  // S of row tile t, from a slot of the fp16 ring
+                const uint64_t qd = q_desc + t * (C::QT >> 4), kd = k_desc + slot * (C::FT >> 4);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k)  // dims past dim are zeros
+                    mma_ss(tmem + t * TOK, qd + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2),
+                           kd + ((k >> 2) * (C::BLK >> 4) + (k & 3) * 2), id_s, k ? 1u : 0u);
                 commit(s_full + t);
-            }
-            __syncwarp();
-        };
-        auto product_o = [&](int t, int n, bool more) {
-            if (lane == 0) {
+            };
+            auto product_o = [&](int t, int j, int slot) {
+                const uint64_t vd = v_desc + slot * (C::FT >> 4);
 #pragma unroll
                 for (int k = 0; k < TOK / 16; ++k)
-                    mma_ts(tmem + 2 * TOK + t * DP, tmem + t * TOK + 8 * k,
-                           smem_desc(f_at + (n % NF) * C::FT + k * 2048, C::BLK), id_o, (more || k) ? 1u : 0u);
-                commit(o_done + t);
-            }
-            __syncwarp();
-        };
-        auto release = [&](int n) {
-            if (lane == 0) commit(f_empty + n % NF);
-            __syncwarp();
-        };
-        auto ready = [&](uint64_t* bar, uint32_t parity) {
-            if (!failed && !wait(bar, parity, cap)) failed = true;
-            tc_after();
-            return !failed;
-        };
-        if (tiles && ready(q_full, 0) && ready(f_full, 0)) {
-            product_s(0, 0);
-            if (two) product_s(1, 0);
-            release(0);
-            for (int j = 0; j < tiles; ++j) {
-                const int v = 2 * j + 1, k = 2 * j + 2;
-                const bool more = j + 1 < tiles;
-                if (!ready(f_full + v % NF, (v / NF) & 1) || !ready(p_full, j & 1)) break;
-                product_o(0, v, j > 0);
-                if (more) {
-                    if (!ready(f_full + k % NF, (k / NF) & 1)) break;
-                    product_s(0, k);
+                    mma_ts(tmem + 2 * TOK + t * DP, tmem + t * TOK + 8 * k, vd + k * (2048 >> 4), id_o,
+                           (j || k) ? 1u : 0u);
+                // earlier products of O are known to be done by the S after them
+                if (j == tiles - 1) commit(o_done + t);
+            };
+            int slot = 0;           // of the fp16 ring
+            uint32_t phase = 0;     // and its phase
+            auto next = [&]() {
+                if (++slot == NF) {
+                    slot = 0;
+                    phase ^= 1u;
                 }
-                if (two) {
-                    if (!ready(p_full + 1, j & 1)) break;
-                    product_o(1, v, j > 0);
-                }
-                release(v);
-                if (more) {
-                    if (two) product_s(1, k);
-                    release(k);
+            };
+            if (ready(q_full, 0) && ready(f_full, 0)) {
+                product_s(0, 0);
+                if (two) product_s(1, 0);
+                commit(f_empty);
+                next();
+                for (int j = 0; j < tiles; ++j) {
+                    const bool more = j + 1 < tiles;
+                    const int v = slot;
+                    if (!ready(f_full + v, phase) || !ready(p_full, j & 1)) break;
+                    product_o(0, j, v);
+                    next();
+                    if (more) {
+                        if (!ready(f_full + slot, phase)) break;
+                        product_s(0, slot);
+                    }
+                    if (two) {
+                        if (!ready(p_full + 1, j & 1)) break;
+                        product_o(1, j, v);
+                    }
+                    commit(f_empty + v);
+                    if (more) {
+                        if (two) product_s(1, slot);
+                        commit(f_empty + slot);
+                        next();
+                    }
                 }
             }
         }
+        __syncwarp();
+        failed = __any_sync(FULL, failed);
         // no product in flight (after a wait ran out) and nobody reading when
         // the tensor memory is given back
         if (lane == 0) commit(drain);
@@ -423,7 +450,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         // ---------------- codes -> fp16.  A thread's chunk of 16 codes and the
         // rows of its eight-lane phase (r and r ^ 5) are such that both the
         // loads and the two stores of a phase fall into distinct banks.
-        const int w = warp - 4, c = lane & 3, r8 = ((lane >> 3) & 3) ^ ((lane & 4) ? 5 : 0);
+        const int w = warp & 3, c = lane & 3, r8 = ((lane >> 3) & 3) ^ ((lane & 4) ? 5 : 0);
         for (int n = 0; n < 2 * tiles; ++n) {
             const int from = n % NC, to = n % NF;
             if (!wait(c_full + from, (n / NC) & 1, cap) || (n >= NF && !wait(f_empty + to, (n / NF - 1) & 1, cap))) {
@@ -433,7 +460,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             const uint8_t* src = smem + C::OFF_C + from * C::CT;
             uint8_t* dst = smem + C::OFF_F + to * C::FT;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < TOK / 32; ++i) {
                 const int row = 8 * (w + 4 * i) + r8;
 #pragma unroll
                 for (int half = 0; half < DP / 64; ++half) {
@@ -468,40 +495,45 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         const bool mine = 128 * t + tr < n_rows;
         const int64_t q_tok = rq.r0 + r / a.group;
         const int head = h * a.group + (int)(r % a.group);
-        // the query row to shared memory; bfloat16 rows are brought into
-        // fp16's range by a power of two
+        // the warp's 32 query rows to shared memory, DP / 8 lanes to a row;
+        // bfloat16 rows are brought into fp16's range by a power of two
         float unit = 1.f;
         {
-            const T* q = (const T*)a.q + q_tok * a.q_row + (int64_t)head * a.q_head;
-            float inv = 1.f;
-            if constexpr (!std::is_same<T, __half>::value) {
-                float top = 0.f;
-                if (mine)
-                    for (int i = 0; i < dim / 8; ++i) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(q + 8 * i);
-                        const T* e = reinterpret_cast<const T*>(&v);
+            constexpr int LANES = DP / 8, STEP = 32 / LANES;
+            const int col = lane % LANES;
+            const int64_t at = q_tok * a.q_row + (int64_t)head * a.q_head;  // of this thread's row
+            uint4 v[32 / STEP];
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(to_float(e[x])));
-                    }
-                const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
-                unit = __uint_as_float(e << 23);
-                inv = __uint_as_float((254u - e) << 23);
+            for (int i = 0; i < 32 / STEP; ++i) {
+                const int src = STEP * i + lane / LANES;  // row of the warp
+                const int64_t from = __shfl_sync(FULL, at, src);
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (128 * t + 32 * quad + src < n_rows && 8 * col < dim)
+                    v[i] = *reinterpret_cast<const uint4*>((const T*)a.q + from + 8 * col);
             }
-            uint8_t* to = smem + t * C::QT + tr * 128;
-            for (int i = 0; i < dim / 8; ++i) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (mine) {
-                    v = *reinterpret_cast<const uint4*>(q + 8 * i);
-                    if constexpr (!std::is_same<T, __half>::value) {
-                        const T* e = reinterpret_cast<const T*>(&v);
-                        uint32_t y[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            y[x] = h2bits(__floats2half2_rn(to_float(e[2 * x]) * inv, to_float(e[2 * x + 1]) * inv));
-                        v = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
+            for (int i = 0; i < 32 / STEP; ++i) {
+                const int src = STEP * i + lane / LANES, row = 32 * quad + src;
+                if constexpr (!std::is_same<T, __half>::value) {
+                    const T* e = reinterpret_cast<const T*>(&v[i]);
+                    float top = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) top = fmaxf(top, fabsf(to_float(e[x])));
+#pragma unroll
+                    for (int x = 1; x < LANES; x <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL, top, x));
+                    const uint32_t ex = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+                    const float inv = __uint_as_float((254u - ex) << 23);
+                    uint32_t y[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        y[x] = h2bits(__floats2half2_rn(to_float(e[2 * x]) * inv, to_float(e[2 * x + 1]) * inv));
+                    v[i] = make_uint4(y[0], y[1], y[2], y[3]);
+                    // row src's unit to its thread
+                    const float u = __shfl_sync(FULL, __uint_as_float(ex << 23), (lane % STEP) * LANES);
+                    if (lane / STEP == i) unit = u;
                 }
-                *reinterpret_cast<uint4*>(to + (i >> 3) * C::BLK + (((i & 7) ^ (tr & 7)) << 4)) = v;
+                *reinterpret_cast<uint4*>(smem + t * C::QT + (col >> 3) * C::QBLK + row * 128 +
+                                          (((col & 7) ^ (row & 7)) << 4)) = v[i];
             }
             bspx::fence_proxy_async_smem();
             __syncwarp();
@@ -524,7 +556,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             const float* mt = meta + (j % NM) * C::META;
             const uint32_t there = reinterpret_cast<const uint32_t*>(mt)[3 * GROUPS];
             const int tok = t0 + j * TOK;
-            const bool edge = tok + TOK - 1 > tile_pos0 || (a.window && tok <= tile_pos1 - a.window) || there != 0xFFu;
+            const bool edge = tok + TOK - 1 > tile_pos0 || (a.window && tok <= tile_pos1 - a.window) || there != (1u << GROUPS) - 1u;
             // columns lo .. hi of this tile are this row's
             const int hi = pos - tok, lo = (a.window ? max(pos - a.window + 1, 0) : 0) - tok;
             uint32_t x[TOK];
@@ -570,12 +602,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 topw = fmaxf(topw, mw);
                 const float fade = ex2(m - top), back = ex2(mw - topw);
                 l *= fade;
-                if (j) {  // O is whole once the product of the tile before is done
-                    if (!wait(o_done + t, (j - 1) & 1, cap)) {
-                        failed = true;
-                        break;
-                    }
-                    tc_after();
+                if (j) {  // the product of the tile before is done: this S was asked for after it
                     for (int cb = 0; cb < DP; cb += 32) {
                         uint32_t o[32];
                         __syncwarp();
@@ -623,7 +650,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             if (lane == 0) bspx::mbar_arrive(p_full + t);
         }
         // ---------------- the rows out
-        if (my_tiles && !failed && !wait(o_done + t, (my_tiles - 1) & 1, cap)) failed = true;
+        if (my_tiles && !failed && !wait(o_done + t, 0, cap)) failed = true;
         tc_after();
         const float f = l > 0.f ? ex2(mw - m) / (l * LIFT) : 0.f;
         T* out = (T*)a.out + q_tok * a.o_row + (int64_t)head * a.o_head;
