@@ -372,10 +372,16 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             const uint64_t k_desc = smem_desc(bspx::smem_u32(smem + C::OFF_F), 16);
             const uint64_t v_desc = smem_desc(bspx::smem_u32(smem + C::OFF_F), C::BLK);
             const uint32_t id_s = idesc(TOK, false), id_o = idesc(dim, true);
+            // (the fence orders products after other threads' tensor-memory
+            // accesses, and stops their overlap: only where there are some)
             auto ready = [&](uint64_t* bar, uint32_t parity) {
                 if (!bspx::mbar_wait_bounded(bar, parity, cap)) failed = true;
-                tc_after();
                 return !failed;
+            };
+            auto ready_w = [&](int t, int j) {
+                const bool ok = ready(p_full + t, j & 1);
+                tc_after();
+                return ok;
             };
             auto product_s = [&](int t, int slot) {  // S of row tile t, from a slot of the fp16 ring
                 const uint64_t qd = q_desc + t * (C::QT >> 4), kd = k_desc + slot * (C::FT >> 4);
@@ -410,7 +416,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 for (int j = 0; j < tiles; ++j) {
                     const bool more = j + 1 < tiles;
                     const int v = slot;
-                    if (!ready(f_full + v, phase) || !ready(p_full, j & 1)) break;
+                    if (!ready(f_full + v, phase) || !ready_w(0, j)) break;
                     product_o(0, j, v);
                     next();
                     if (more) {
@@ -418,7 +424,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                         product_s(0, slot);
                     }
                     if (two) {
-                        if (!ready(p_full + 1, j & 1)) break;
+                        if (!ready_w(1, j)) break;
                         product_o(1, j, v);
                     }
                     commit(f_empty + v);
