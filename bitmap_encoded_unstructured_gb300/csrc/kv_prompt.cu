@@ -91,12 +91,17 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t leading)
     return d;
 }
 
+// Products and commits are written for the whole warp, with the one thread
+// that issues them elected inside: the operands then stay in uniform
+// registers.  Issued under a branch on the lane, each product would wait for
+// its descriptors to be moved there (86 cycles a product, more than it takes).
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(accum)
         : "memory");
 }
@@ -104,18 +109,22 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(id), "r"(accum)
         : "memory");
 }
 
 __device__ __forceinline__ void commit(uint64_t* bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bspx::smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xFFFFFFFF;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            bspx::smem_u32(bar))
+        : "memory");
 }
 
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -365,9 +374,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         return;
     }
     if (warp == 1) {
-        // ---------------- MMA issuer: one thread, so that a step costs little
-        // beside its products
-        if (lane == 0 && tiles) {
+        // ---------------- MMA issuer (control flow and operands uniform)
+        const int n_tiles = __shfl_sync(FULL, tiles, 0);
+        const bool pair_of = __any_sync(FULL, two);
+        const uint32_t tm = __shfl_sync(FULL, tmem, 0);
+        if (n_tiles) {
             const uint64_t q_desc = smem_desc(bspx::smem_u32(smem), 16);
             const uint64_t k_desc = smem_desc(bspx::smem_u32(smem + C::OFF_F), 16);
             const uint64_t v_desc = smem_desc(bspx::smem_u32(smem + C::OFF_F), C::BLK);
@@ -375,7 +386,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             // (the fence orders products after other threads' tensor-memory
             // accesses, and stops their overlap: only where there are some)
             auto ready = [&](uint64_t* bar, uint32_t parity) {
-                if (!bspx::mbar_wait_bounded(bar, parity, cap)) failed = true;
+                if (!wait(bar, parity, cap)) failed = true;
                 return !failed;
             };
             auto ready_w = [&](int t, int j) {
@@ -387,7 +398,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 const uint64_t qd = q_desc + t * (C::QT >> 4), kd = k_desc + slot * (C::FT >> 4);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)  // dims past dim are zeros
-                    mma_ss(tmem + t * TOK, qd + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2),
+                    mma_ss(tm + t * TOK, qd + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2),
                            kd + ((k >> 2) * (C::BLK >> 4) + (k & 3) * 2), id_s, k ? 1u : 0u);
                 commit(s_full + t);
             };
@@ -395,10 +406,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 const uint64_t vd = v_desc + slot * (C::FT >> 4);
 #pragma unroll
                 for (int k = 0; k < TOK / 16; ++k)
-                    mma_ts(tmem + 2 * TOK + t * DP, tmem + t * TOK + 8 * k, vd + k * (2048 >> 4), id_o,
+                    mma_ts(tm + 2 * TOK + t * DP, tm + t * TOK + 8 * k, vd + k * (2048 >> 4), id_o,
                            (j || k) ? 1u : 0u);
                 // earlier products of O are known to be done by the S after them
-                if (j == tiles - 1) commit(o_done + t);
+                if (j == n_tiles - 1) commit(o_done + t);
             };
             int slot = 0;           // of the fp16 ring
             uint32_t phase = 0;     // and its phase
@@ -410,11 +421,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             };
             if (ready(q_full, 0) && ready(f_full, 0)) {
                 product_s(0, 0);
-                if (two) product_s(1, 0);
+                if (pair_of) product_s(1, 0);
                 commit(f_empty);
                 next();
-                for (int j = 0; j < tiles; ++j) {
-                    const bool more = j + 1 < tiles;
+                for (int j = 0; j < n_tiles; ++j) {
+                    const bool more = j + 1 < n_tiles;
                     const int v = slot;
                     if (!ready(f_full + v, phase) || !ready_w(0, j)) break;
                     product_o(0, j, v);
@@ -423,25 +434,23 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                         if (!ready(f_full + slot, phase)) break;
                         product_s(0, slot);
                     }
-                    if (two) {
+                    if (pair_of) {
                         if (!ready_w(1, j)) break;
                         product_o(1, j, v);
                     }
                     commit(f_empty + v);
                     if (more) {
-                        if (two) product_s(1, slot);
+                        if (pair_of) product_s(1, slot);
                         commit(f_empty + slot);
                         next();
                     }
                 }
             }
         }
-        __syncwarp();
-        failed = __any_sync(FULL, failed);
         // no product in flight (after a wait ran out) and nobody reading when
         // the tensor memory is given back
-        if (lane == 0) commit(drain);
         __syncwarp();
+        commit(drain);
         if (!wait(drain, 0, cap)) failed = true;
         if (!wait(read, 0, cap)) failed = true;
         if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
