@@ -130,6 +130,16 @@ __device__ __forceinline__ void commit(uint64_t* bar)
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+}
+
 // 32 consecutive tensor-memory columns of this thread's lane; they are there
 // after tmem_wait_ld().
 __device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t* r)
@@ -192,18 +202,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t* r)
         "%15, %16};" ::"r"(at),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
 
@@ -598,67 +596,71 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                                      : "r"(see), "r"(1u << i));  // -inf
                 }
             }
-            // largest logits
-            float top = -INFINITY, topw = -INFINITY;
+            // weights with the maxima of the tiles before, two at a time; the
+            // sum of the tile then tells whether the maxima lagged too far
+            float most_v = 0.f;
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                float big[2] = {-INFINITY, -INFINITY};
+            for (int g = 0; g < GROUPS; ++g) most_v = fmaxf(most_v, fabsf(mt[GROUPS + g]));
+            float sum;
+            auto weigh = [&]() {
+                const uint64_t minus = pair(-m, -m);
+                uint64_t part[4] = {0, 0, 0, 0};
+                uint32_t y[16];
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    big[0] = fmaxf(fmaxf(big[0], __uint_as_float(x[16 * g + i])), __uint_as_float(x[16 * g + i + 1]));
-                    big[1] = fmaxf(fmaxf(big[1], __uint_as_float(x[16 * g + i + 2])), __uint_as_float(x[16 * g + i + 3]));
-                }
-                const float b = fmaxf(big[0], big[1]) * kf[g];
-                top = fmaxf(top, b);
-                topw = fmaxf(topw, b + mt[2 * GROUPS + g]);
-            }
-            if (__any_sync(FULL, top > m + LAZY || topw > mw + LAZY)) {
-                top = fmaxf(top, m);
-                topw = fmaxf(topw, mw);
-                const float fade = ex2(m - top), back = ex2(mw - topw);
-                l *= fade;
-                if (j) {  // the product of the tile before is done: this S was asked for after it
-                    for (int cb = 0; cb < DP; cb += 32) {
-                        uint32_t o[32];
+                for (int g = 0; g < GROUPS; ++g) {
+                    const float v = mt[GROUPS + g] * lift;
+                    const uint64_t kk = pair(kf[g], kf[g]), vv = pair(v, v);
+#pragma unroll
+                    for (int i = 16 * g; i < 16 * g + 16; i += 2) {
+                        float a0, a1;
+                        unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kk, minus), a0, a1);
+                        const uint64_t p = pair(ex2(a0), ex2(a1));
+                        part[(i / 2) & 3] = add2(part[(i / 2) & 3], p);
+                        unpair(mul2(p, vv), a0, a1);
+                        y[(i / 2) % 16] = h2bits(__floats2half2_rn(a0, a1));
+                    }
+                    if (g & 1) {
                         __syncwarp();
-                        tmem_ld32(o_at + cb, o);
-                        tmem_wait_ld(o, 32);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * back);
-                        tmem_st32(o_at + cb, o);
+                        tmem_st16(s_at + 8 * (g - 1), y);
                     }
                 }
+                float a0, a1;
+                unpair(add2(add2(part[0], part[1]), add2(part[2], part[3])), a0, a1);
+                sum = a0 + a1;
+            };
+            weigh();
+            // every p is at most the sum, every weight at most the sum times the
+            // largest V scale times lift, which must stay within fp16
+            if (__any_sync(FULL, !(sum <= 256.f) || !(sum * (most_v * lift) <= 32768.f))) {
+                float top = m, topw = mw;
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    float big = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) big = fmaxf(big, __uint_as_float(x[16 * g + i]));
+                    big *= kf[g];
+                    top = fmaxf(top, big);
+                    topw = fmaxf(topw, big + mt[2 * GROUPS + g]);
+                }
+                const float fade = ex2(m - top), back = ex2(mw - topw);
+                l *= fade;
                 m = top;
                 mw = topw;
                 lift = ex2(fminf(m - mw, 120.f)) * LIFT;
-            }
-            // weights, two at a time, over the logits' registers and columns
-            const uint64_t minus = pair(-m, -m);
-            uint64_t part[4] = {0, 0, 0, 0};
-            uint32_t y[16];
+                if (j) {  // the product of the tile before is done: this S was asked for after it
+                    for (int cb = 0; cb < DP; cb += 16) {
+                        uint32_t o[16];
+                        __syncwarp();
+                        tmem_ld16(o_at + cb, o);
+                        tmem_wait_ld(o, 16);
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-                const float v = mt[GROUPS + g] * lift;
-                const uint64_t kk = pair(kf[g], kf[g]), vv = pair(v, v);
-#pragma unroll
-                for (int i = 16 * g; i < 16 * g + 16; i += 2) {
-                    float a0, a1;
-                    unpair(fma2(pair(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), kk, minus), a0, a1);
-                    const uint64_t p = pair(ex2(a0), ex2(a1));
-                    part[(i / 2) & 3] = add2(part[(i / 2) & 3], p);
-                    unpair(mul2(p, vv), a0, a1);
-                    y[(i / 2) % 16] = h2bits(__floats2half2_rn(a0, a1));
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * back);
+                        tmem_st16(o_at + cb, o);
+                    }
                 }
-                if (g & 1) {
-                    __syncwarp();
-                    tmem_st16(s_at + 8 * (g - 1), y);
-                }
+                weigh();
             }
-            {
-                float a0, a1;
-                unpair(add2(add2(part[0], part[1]), add2(part[2], part[3])), a0, a1);
-                l += a0 + a1;
-            }
+            l += sum;
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_before();
             __syncwarp();
