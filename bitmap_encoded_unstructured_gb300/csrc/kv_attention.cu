@@ -85,6 +85,7 @@ struct DecodeArgs {
     int* err;
     uint32_t spin_cap;
     int32_t most_rows;  // requests with more query rows than this (per KV head) are not this kernel's
+    bool beside;        // runs beside the prompt kernel, which waited for what came before
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -286,7 +287,9 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 
     if (lane < C::STAGES) bspx::mbar_init(full + lane, 1);
     bspx::fence_mbar_init();
-    wait_prior_grids();  // launched before the kernel ahead of it is done
+    // launched before the kernel ahead of it is done; beside the prompt kernel
+    // it only has to end after it
+    if (!d.beside) wait_prior_grids();
 
     // the shared run: each thread sums some requests; pre[i] is what comes
     // before thread i's
@@ -802,6 +805,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
         w0 = w1;
     }
+    if (d.beside) wait_prior_grids();
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
@@ -850,21 +854,25 @@ bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream
 {
     // Query blocks of 8, 16 or 24 rows: the smallest that holds the largest
     // request.  Requests with more rows are the prompt kernel's, whose row
-    // tiles have 128 rows and whose dims end at 128.
+    // tiles have 128 rows and whose dims end at 128; a step that has some is
+    // taken for one of prompts and single tokens, and the block for a single
+    // token's rows.
     const int64_t most = max_new * a.group;
-    const int few = a.c.dim > 128 ? INT32_MAX : 24;
-    const DecodeArgs d = {a, h->parts, h->cuts, h->err, bsp_spin_cap(), few};
-    bsp_status_t st;
+    const bool prompts = most > 24 && a.c.dim <= 128 && a.s.batch > 0;
+    const int64_t block = prompts ? std::min<int64_t>(a.group, 24) : most;
+    const int few = block <= 8 ? 8 : block <= 16 ? 16 : 24;
+    if (prompts) {
+        const bsp_status_t st = bsp_run_kv_prompt(h, a, std::is_same<T, __half>::value ? BSP_FP16 : BSP_BF16, few, s);
+        if (st != BSP_OK) return st;
+    }
+    const DecodeArgs d = {a, h->parts, h->cuts, h->err, bsp_spin_cap(), prompts ? few : INT32_MAX, prompts};
     if (a.c.dim <= 64)
-        st = most <= 8 ? launch_decode<T, 64, 1>(h, d, s) : most <= 16 ? launch_decode<T, 64, 2>(h, d, s)
+        return few == 8 ? launch_decode<T, 64, 1>(h, d, s) : few == 16 ? launch_decode<T, 64, 2>(h, d, s)
                                                                        : launch_decode<T, 64, 3>(h, d, s);
-    else if (a.c.dim <= 128)
-        st = most <= 8 ? launch_decode<T, 128, 1>(h, d, s) : most <= 16 ? launch_decode<T, 128, 2>(h, d, s)
+    if (a.c.dim <= 128)
+        return few == 8 ? launch_decode<T, 128, 1>(h, d, s) : few == 16 ? launch_decode<T, 128, 2>(h, d, s)
                                                                         : launch_decode<T, 128, 3>(h, d, s);
-    else
-        st = most <= 8 ? launch_decode<T, 256, 1>(h, d, s) : launch_decode<T, 256, 2>(h, d, s);
-    if (st != BSP_OK || most <= few || !a.s.batch) return st;
-    return bsp_run_kv_prompt(h, a, std::is_same<T, __half>::value ? BSP_FP16 : BSP_BF16, few, s);
+    return few == 8 ? launch_decode<T, 256, 1>(h, d, s) : launch_decode<T, 256, 2>(h, d, s);
 }
 
 }  // namespace

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <climits>
 #include <new>
+#include <type_traits>
 
 namespace {
 
@@ -71,6 +72,7 @@ __device__ __forceinline__ int holder(const int* P, int n, int x)
 // block table row, which nobody writes, not from the stack.
 __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_kernel(const PlanArgs a)
 {
+    wait_prior_grids();
     extern __shared__ int sm[];
     const int B = a.batch, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int* rows = sm;              // [B + 1] rows asked for before request b
@@ -184,27 +186,78 @@ struct AppendArgs {
 // Work items of a step, one per page that receives rows.  Request b's items
 // start at F(b) = q_start[b] / page + 2 b: it touches at most n / page + 2
 // pages, so F leaves room for them without a scan of the batch; items past a
-// request's last page have nothing to do.
-__device__ __forceinline__ int item_request(const KvStepView& s, int page_shift, int item)
+// request's last page have nothing to do.  The warp looks 32 requests at a
+// time, so that a search costs one or two loads.
+__device__ __forceinline__ int item_request(const KvStepView& s, int page_shift, int item, int lane)
 {
-    int lo = 0, hi = s.batch;  // F(lo) <= item < F(hi), or hi = batch
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((s.q_start[mid] >> page_shift) + 2 * mid <= item) lo = mid;
-        else hi = mid;
+    int lo = 0, n = s.batch;  // F(lo) <= item, among lo .. lo + n - 1
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lane * step;
+        const bool below = at < n && (s.q_start[lo + at] >> page_shift) + 2 * (lo + at) <= item;
+        const uint32_t set = __ballot_sync(0xFFFFFFFFu, below || lane == 0);
+        const int last = 31 - __clz(set);
+        lo += last * step;
+        n = min(step, n - last * step);
     }
     return lo;
 }
 
-// One warp per (page that receives rows, head, K or V).
-template <class T>
-__global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs a)
+constexpr int APPEND_THREADS = 128, CACHED = 8;
+
+__device__ __forceinline__ __half2 larger(__half2 a, uint32_t b) { return __hmax2(a, __habs2(*reinterpret_cast<__half2*>(&b))); }
+__device__ __forceinline__ __nv_bfloat162 larger(__nv_bfloat162 a, uint32_t b)
 {
-    const int unit = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    return __hmax2(a, __habs2(*reinterpret_cast<__nv_bfloat162*>(&b)));
+}
+__device__ __forceinline__ float larger_of(__half2 a) { return fmaxf(__low2float(a), __high2float(a)); }
+__device__ __forceinline__ float larger_of(__nv_bfloat162 a) { return fmaxf(__low2float(a), __high2float(a)); }
+
+// Eight codes round(x / scale), as the IEEE quotient rounds, from products
+// with the reciprocal: adding 1.5 2^23 rounds them to even.  Where one is near
+// a tie (the product is off by less than 3e-5 at 127) or not finite, the
+// eight are divided.
+template <class T>
+__device__ __forceinline__ uint2 codes_of(const uint4& raw, float scale, float inv)
+{
+    constexpr float ROUND = 12582912.f;
+    const T* e = reinterpret_cast<const T*>(&raw);
+    uint32_t q[8];
+    bool fine = true;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const float t = __fmul_rn(to_float(e[c]), inv), r = __fadd_rn(t, ROUND);
+        fine = fine && fabsf(__fsub_rn(t, __fsub_rn(r, ROUND))) <= 0.49995f;  // false for NaN
+        q[c] = __float_as_uint(r);
+    }
+    if (!fine) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float t = __fdiv_rn(to_float(e[c]), scale);
+            q[c] = t != t ? 0u : (uint32_t)__float2int_rn(fminf(fmaxf(t, -127.f), 127.f));
+        }
+    }
+    uint2 o;
+    o.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+    o.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+    return o;
+}
+
+// WARPS warps (1 or 4) per unit: a page that receives rows, a head, K or V.
+// Two passes over the unit's rows, its largest value and its codes; the first
+// CACHED vectors of a thread stay in registers between them.  1 << lane_shift
+// threads share a row, one 16-byte vector each.
+template <class T, int WARPS>
+__global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendArgs a, const int lane_shift)
+{
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    constexpr int THREADS = WARPS * 32;
+    wait_prior_grids();
+    const int lane = threadIdx.x & 31, tid = threadIdx.x % THREADS;
+    const int unit = blockIdx.y * (APPEND_THREADS / THREADS) + threadIdx.x / THREADS;
     if (unit >= 2 * a.c.heads) return;
     const int head = unit >> 1, sh = a.c.page_shift, page = 1 << sh;
     const bool is_v = unit & 1;
-    const int b = item_request(a.s, sh, blockIdx.x);
+    const int b = item_request(a.s, sh, blockIdx.x, lane);
     const Request r = request_of(a.s, sh, b);
     const int start = r.len - r.n, from = max(start, 0);  // position of the first new row; of the first stored
     const int64_t jj = (from >> sh) + (int64_t)blockIdx.x - ((a.s.q_start[b] >> sh) + 2 * (int64_t)b);
@@ -214,32 +267,59 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs a)
     if (lo >= hi) return;
     const int p = a.s.table[(int64_t)b * a.s.table_stride + j];
     if (p < 0 || p >= a.c.pages) return;
-    const int vecs = a.c.dim / 8;                        // 16-byte vectors of a row
     const int64_t row_step = is_v ? a.v_row : a.k_row;
+    const int kept = lo & (page - 1), rows = hi - lo;    // earlier rows of the page; new ones
+    const int col = (tid & ((1 << lane_shift) - 1)) * 8, row0 = tid >> lane_shift, step = THREADS >> lane_shift;
+    const bool mine = col < a.c.dim;
     const T* x = (const T*)(is_v ? a.v : a.k) + (int64_t)(r.r0 + lo - start) * row_step +
-                 (int64_t)head * (is_v ? a.v_head : a.k_head);
+                 (int64_t)head * (is_v ? a.v_head : a.k_head) + col;
     int8_t* codes = (is_v ? a.c.v : a.c.k) + (int64_t)p * a.c.page_stride + (int64_t)head * a.c.head_stride;
     float* scale = (is_v ? a.c.v_scale : a.c.k_scale) + (int64_t)p * a.c.scale_stride + head;
-    const int total = (hi - lo) * vecs;
-
-    float top = 0.f;
-    for (int i = lane; i < total; i += 32) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(x + (i / vecs) * row_step + (i % vecs) * 8);
-        const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float f = fabsf(to_float(e[c]));
-            if (f < INFINITY) top = fmaxf(top, f);       // false for NaN and infinities
-        }
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const int kept = lo & (page - 1);                    // earlier rows of the page
     const float old = kept ? *scale : 0.f;
+    auto load = [&](int row) {
+        return mine && row < rows ? *reinterpret_cast<const uint4*>(x + row * row_step) : make_uint4(0, 0, 0, 0);
+    };
+    auto most = [&](float f) {  // over the unit's threads
+#pragma unroll
+        for (int d = 16; d; d >>= 1) f = fmaxf(f, __shfl_xor_sync(0xFFFFFFFFu, f, d));
+        if constexpr (WARPS > 1) {
+            __shared__ float tops[WARPS];
+            __syncthreads();
+            if (lane == 0) tops[tid >> 5] = f;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) f = fmaxf(f, tops[w]);
+        }
+        return f;
+    };
+
+    uint4 held[CACHED];
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c) held[c] = load(row0 + c * step);
+    T2 big;
+    big.x = big.y = from_float<T>(0.f);
+    auto look = [&](const uint4& v) { big = larger(larger(larger(larger(big, v.x), v.y), v.z), v.w); };
+#pragma unroll
+    for (int c = 0; c < CACHED; ++c) look(held[c]);
+    for (int row = row0 + CACHED * step; row < rows; row += step) look(load(row));
+    float top = most(larger_of(big));
+    if (top == INFINITY) {  // again, without the infinities
+        top = 0.f;
+        for (int row = row0; row < rows; row += step) {
+            const uint4 v = load(row);
+            const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float f = fabsf(to_float(e[c]));
+                if (f < INFINITY) top = fmaxf(top, f);   // false for NaN too
+            }
+        }
+        top = most(top);
+    }
     const float now = fmaxf(old, __fdiv_rn(top, 127.f));
     if (kept && now != old) {
         const float ratio = now > 0.f ? __fdiv_rn(old, now) : 0.f;
-        for (int i = lane; i < kept * (a.c.dim / 16); i += 32) {
+        for (int i = tid; i < kept * (a.c.dim / 16); i += THREADS) {
             int4* at = reinterpret_cast<int4*>(codes + (i / (a.c.dim / 16)) * a.c.row_stride + (i % (a.c.dim / 16)) * 16);
             int4 w = *at;
             int8_t* e = reinterpret_cast<int8_t*>(&w);
@@ -248,62 +328,89 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const AppendArgs a)
             *at = w;
         }
     }
-    for (int i = lane; i < total; i += 32) {
-        const uint4 raw = *reinterpret_cast<const uint4*>(x + (i / vecs) * row_step + (i % vecs) * 8);
-        const T* e = reinterpret_cast<const T*>(&raw);
-        alignas(8) int8_t q[8];
+    // no reciprocal of a scale below 2^-126: NaN makes every code a quotient
+    const float inv = now < 1.2e-38f ? __int_as_float(0x7FC00000) : __fdiv_rn(1.f, now);
+    auto store = [&](int row, const uint4& v) {
+        if (mine && row < rows)
+            *reinterpret_cast<uint2*>(codes + (kept + row) * a.c.row_stride + col) =
+                now > 0.f ? codes_of<T>(v, now, inv) : make_uint2(0, 0);
+    };
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float f = to_float(e[c]);
-            // NaN converts to 0; infinities meet the clamp
-            const float t = now > 0.f ? __fdiv_rn(f, now) : 0.f;
-            q[c] = (int8_t)(t != t ? 0 : __float2int_rn(fminf(fmaxf(t, -127.f), 127.f)));
-        }
-        *reinterpret_cast<int2*>(codes + ((lo & (page - 1)) + i / vecs) * a.c.row_stride + (i % vecs) * 8) =
-            *reinterpret_cast<const int2*>(q);
-    }
-    __syncwarp();
-    if (lane == 0) *scale = now;
+    for (int c = 0; c < CACHED; ++c) store(row0 + c * step, held[c]);
+    for (int row = row0 + CACHED * step; row < rows; row += step) store(row, load(row));
+    if (tid == 0) *scale = now;
 }
 
 // ------------------------------------------------------------------- read
+
+// x / d for x < 2^31 by a multiplication: with 2^s the power of two at or
+// above d, q = (floor(x m / 2^32) + x) / 2^s where m = floor(2^32 (2^s - d) / d) + 1
+// (division by an invariant integer, Granlund and Montgomery 1994).
+struct Divide {
+    uint32_t d, m, s;
+    explicit Divide(uint32_t by = 1) : d(by), s(0)
+    {
+        while ((1u << s) < d) ++s;
+        m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - d)) / d + 1);
+    }
+    __device__ uint32_t operator()(uint32_t x) const { return (__umulhi(x, m) + x) >> s; }
+};
 
 struct ReadArgs {
     KvView c;
     const int64_t* slots;
     void *k, *v;
-    int64_t n;
+    int64_t n;       // rows
+    uint32_t units;  // of 8 values in a row of all heads
+    Divide by_units, by_head;
+    int rows;        // of a CTA's piece: rows * units < 2^31
 };
 
-// One thread per 16 codes of a row, K and V by blockIdx.y.
+constexpr int READ_AT_ONCE = 4;  // units of a thread in flight
+
+// A thread takes units of 8 values, so that a warp's loads and stores are
+// whole lines; K and V by blockIdx.y.  CTA x takes
+// pieces x, x + gridDim.x, ... of `rows` rows each.
 template <class T>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadArgs a)
 {
-    const int per = a.c.dim / 16;                        // threads of a row
-    const int64_t all = a.n * a.c.heads * per;
+    wait_prior_grids();
     const int8_t* codes = blockIdx.y ? a.c.v : a.c.k;
     const float* scales = blockIdx.y ? a.c.v_scale : a.c.k_scale;
-    T* out = (T*)(blockIdx.y ? a.v : a.k);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / per;
-        const int part = (int)(i - row * per), head = (int)(row % a.c.heads);
-        const int64_t slot = a.slots[row / a.c.heads], p = slot >> a.c.page_shift;
-        alignas(16) T o[16];
-        if (slot >= 0 && p < a.c.pages) {
-            const int64_t off = slot - (p << a.c.page_shift);
-            const int4 w = *reinterpret_cast<const int4*>(codes + p * a.c.page_stride + head * a.c.head_stride +
-                                                          off * a.c.row_stride + part * 16);
-            const float s = scales[p * a.c.scale_stride + head];
-            const int8_t* e = reinterpret_cast<const int8_t*>(&w);
+    for (int64_t r0 = (int64_t)blockIdx.x * a.rows; r0 < a.n; r0 += (int64_t)gridDim.x * a.rows) {
+        const uint32_t all = (uint32_t)min((int64_t)a.rows, a.n - r0) * a.units;
+        T* out = (T*)(blockIdx.y ? a.v : a.k) + r0 * a.units * 8;
+        for (uint32_t u0 = threadIdx.x; u0 < all; u0 += 256 * READ_AT_ONCE) {
+            int2 w[READ_AT_ONCE];
+            float sc[READ_AT_ONCE];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = from_float<T>((float)e[c] * s);
-        } else {
+            for (int x = 0; x < READ_AT_ONCE; ++x) {
+                const uint32_t u = u0 + 256 * x;
+                w[x] = make_int2(0, 0);
+                sc[x] = 0.f;
+                if (u < all) {
+                    const uint32_t row = a.by_units(u), unit = u - row * a.units, head = a.by_head(unit);
+                    const int64_t slot = a.slots[r0 + row], p = slot >> a.c.page_shift;
+                    if (slot >= 0 && p < a.c.pages) {
+                        const int64_t off = slot - (p << a.c.page_shift);
+                        w[x] = *reinterpret_cast<const int2*>(codes + p * a.c.page_stride + head * a.c.head_stride +
+                                                              off * a.c.row_stride + (unit - head * a.by_head.d) * 8);
+                        sc[x] = scales[p * a.c.scale_stride + head];
+                    }
+                }
+            }
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] = from_float<T>(0.f);
+            for (int x = 0; x < READ_AT_ONCE; ++x) {
+                const uint32_t u = u0 + 256 * x;
+                if (u < all) {
+                    alignas(16) T o[8];
+                    const int8_t* e = reinterpret_cast<const int8_t*>(&w[x]);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) o[c] = from_float<T>((float)e[c] * sc[x]);
+                    *reinterpret_cast<uint4*>(out + (int64_t)u * 8) = *reinterpret_cast<const uint4*>(o);
+                }
+            }
         }
-        uint4* to = reinterpret_cast<uint4*>(out + i * 16);
-        to[0] = reinterpret_cast<const uint4*>(o)[0];
-        to[1] = reinterpret_cast<const uint4*>(o)[1];
     }
 }
 
@@ -435,8 +542,10 @@ bsp_status_t bsp_kv_plan(bsp_kv_t h, const int32_t* ctx_len, const int32_t* new_
                         h->view.page_shift, free_count == free_count_out ? h->ticket : nullptr};
     const int64_t want = (std::max<int64_t>(tokens, batch) + PLAN_THREADS - 1) / PLAN_THREADS;
     const int grid = (int)std::clamp<int64_t>(want, 1, h->num_sms);
-    kv_plan_kernel<<<grid, PLAN_THREADS, 3 * (batch + 1) * sizeof(int), (cudaStream_t)stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    return launch_early(kv_plan_kernel, dim3(grid), dim3(PLAN_THREADS), 3 * (batch + 1) * (int)sizeof(int),
+                        (cudaStream_t)stream, a)
+               ? BSP_OK
+               : BSP_ERR_CUDA;
 }
 
 bsp_status_t bsp_kv_append(bsp_kv_t h, const bsp_kv_step_t* step, const void* k, const void* v, bsp_dtype_t dtype,
@@ -456,11 +565,19 @@ bsp_status_t bsp_kv_append(bsp_kv_t h, const bsp_kv_step_t* step, const void* k,
     if (!g.ok) return BSP_ERR_CUDA;
     const AppendArgs a = {h->view, view_of(step, rows), k, v, k_row, k_head, v_row, v_head};
     const int64_t items = (rows >> h->view.page_shift) + 2 * (int64_t)step->batch;
-    const dim3 grid((unsigned)items, (unsigned)((2 * h->view.heads + 3) / 4));
+    int lane_shift = 1;
+    while ((8 << lane_shift) < h->view.dim) ++lane_shift;
+    // a block a unit where units are large on average (more rows than a warp
+    // holds in registers), a warp a unit where they are single rows
+    const bool large = std::min<int64_t>(rows / step->batch, 1 << h->view.page_shift) > CACHED * (32 >> lane_shift);
+    const dim3 grid((unsigned)items, (unsigned)(large ? 2 * h->view.heads : (2 * h->view.heads + 3) / 4));
+    const dim3 block(APPEND_THREADS);
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == BSP_FP16) kv_append_kernel<__half><<<grid, 128, 0, s>>>(a);
-    else kv_append_kernel<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    auto go = [&](auto kernel) { return launch_early(kernel, grid, block, 0, s, a, lane_shift); };
+    const bool ok = dtype == BSP_FP16 ? large ? go(kv_append_kernel<__half, 4>) : go(kv_append_kernel<__half, 1>)
+                    : large           ? go(kv_append_kernel<__nv_bfloat16, 4>)
+                                      : go(kv_append_kernel<__nv_bfloat16, 1>);
+    return ok ? BSP_OK : BSP_ERR_CUDA;
 }
 
 bsp_status_t bsp_kv_read(bsp_kv_t h, const int64_t* slots, int64_t n, void* k, void* v, bsp_dtype_t dtype,
@@ -473,13 +590,16 @@ bsp_status_t bsp_kv_read(bsp_kv_t h, const int64_t* slots, int64_t n, void* k, v
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8)) return BSP_ERR_ALIGN;
     DeviceGuard g(h->device);
     if (!g.ok) return BSP_ERR_CUDA;
-    const ReadArgs a = {h->view, slots, k, v, n};
-    const int64_t want = (n * h->view.heads * (h->view.dim / 16) + 255) / 256;
-    const dim3 grid((unsigned)std::min<int64_t>(want, (int64_t)h->num_sms * 8), 2);
+    const uint32_t per_head = (uint32_t)h->view.dim / 8, units = (uint32_t)h->view.heads * per_head;
+    // pieces of about 4096 units: enough CTAs for a small call, and few
+    // searches for a large one
+    const int piece = (int)std::max<uint32_t>(1, 4096 / units);
+    const ReadArgs a = {h->view, slots, k, v, n, units, Divide(units), Divide(per_head), piece};
+    const dim3 grid((unsigned)std::min<int64_t>((n + piece - 1) / piece, (int64_t)h->num_sms * 16), 2);
     cudaStream_t s = (cudaStream_t)stream;
-    if (dtype == BSP_FP16) kv_read_kernel<__half><<<grid, 256, 0, s>>>(a);
-    else kv_read_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    const bool ok = dtype == BSP_FP16 ? launch_early(kv_read_kernel<__half>, grid, dim3(256), 0, s, a)
+                                      : launch_early(kv_read_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a);
+    return ok ? BSP_OK : BSP_ERR_CUDA;
 }
 
 bsp_status_t bsp_kv_attention(bsp_kv_t h, const bsp_kv_step_t* step, const void* q, bsp_dtype_t dtype, int64_t rows,

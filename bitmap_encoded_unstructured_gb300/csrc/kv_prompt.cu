@@ -222,6 +222,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sh = a.c.page_shift, dim = a.c.dim;
     const int H = a.c.heads;
 
+    wait_prior_grids();
+    // what comes next (the kernel of the other requests) may fill the SMs
+    // that this one leaves idle
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
     // the item: long rows first (later rows of a causal prompt see more),
     // the heads of one row tile side by side
     const int h = (int)(blockIdx.x % H);
@@ -710,8 +715,9 @@ bsp_status_t launch(const bsp_kv* h, const PromptArgs& d, cudaStream_t s)
         return BSP_ERR_CUDA;
     const int64_t ctas = d.items * h->view.heads;
     if (ctas > 0x7FFFFFFF) return BSP_ERR_INVALID_ARG;
-    kv_prompt_kernel<T, DP><<<(unsigned)ctas, THREADS, C::SMEM, s>>>(h->map_k, h->map_v, d);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    return launch_early(kv_prompt_kernel<T, DP>, dim3((unsigned)ctas), dim3(THREADS), C::SMEM, s, h->map_k, h->map_v, d)
+               ? BSP_OK
+               : BSP_ERR_CUDA;
 }
 
 }  // namespace
