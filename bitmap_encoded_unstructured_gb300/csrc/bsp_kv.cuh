@@ -45,8 +45,9 @@ struct bsp_kv {
     int* ticket;  // arrivals of a plan whose count is updated in place; zero between calls
     int* err;     // as bsp_handle::err
     // few queries: parts of segments cut between warps, two slots a warp, and
-    // the cut segments by the warp that begins them (last = 0 between calls)
+    // the cut segments by the warp that begins them (last = -1: none)
     float* parts;
+    size_t part_floats;
     KvCut* cuts;
 };
 

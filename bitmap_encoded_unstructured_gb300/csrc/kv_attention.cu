@@ -178,92 +178,137 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int64_
         a.lse[row * a.heads + head] = sum > 0.f ? (top + __log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, ROW_WARPS = JOIN_WARPS / JOIN_ROWS;
+constexpr int MANY = 16;  // parts of a segment from which several warps share a row
 
-// The parts of the segments that were cut, in order: the first worker's, one
-// of each further CTA's, and the last worker's.  A warp joins one query row;
-// a CTA looks after every gridDim-th worker that began a cut segment.
-template <class T, int DP, int NT>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const DecodeArgs d, int workers)
-{
-    using C = DecCfg<DP, NT>;
-    constexpr int Q = C::Q, LANES = DP / 4 < 32 ? DP / 4 : 32, ROWS = 32 / LANES, V = DP / 4 / LANES;
-    const AttnArgs& a = d.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    wait_prior_grids();
-    for (int w = blockIdx.x; w < workers; w += gridDim.x) {
-        const KvCut cut = d.cuts[w];
-        __syncthreads();
-        if (!cut.last) continue;
-        if (threadIdx.x == 0) d.cuts[w].last = 0;
-        const int n = (cut.last - 1) / cut.per_cta - w / cut.per_cta + 2;
-        auto part = [&](int k) {
-            const int64_t slot = k == n - 1 ? 2 * (int64_t)cut.last + 1
-                                            : 2 * (int64_t)(k ? (w / cut.per_cta + k) * cut.per_cta : w);
-            return d.parts + slot * C::PART;
-        };
-        for (int qr = warp * ROWS + lane / LANES; qr < Q; qr += JOIN_WARPS * ROWS) {
-            const int r = cut.rg * Q + qr, dim = lane % LANES * 4;
-            if (r >= cut.n * a.group) continue;
-            float top = NONE, topw = NONE, sum = 0.f;
-            float4 o[V];
+// The parts of a row of one cut segment: the first worker's, one of each
+// further CTA's, and the last worker's.  Lane i adds up dims 4 i .. (and
+// 128 + 4 i ..) of every step-th part from `from` on.
+template <class C, int DP>
+struct RowSum {
+    static constexpr int V = DP > 128 ? 2 : 1, AT_ONCE = 8 / V;  // parts whose loads are in flight together
+    float top = NONE, topw = NONE, sum = 0.f;
+    float4 o[V];
+
+    __device__ void add(float m, float l, float mw, const float4 (&x)[V])
+    {
+        const float t = fmaxf(top, m), tw = fmaxf(topw, mw);
+        sum = sum * ex2(top - t) + l * ex2(m - t);
+        const float f = ex2(topw - tw), g = ex2(mw - tw);
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int AT_ONCE = 8;  // parts whose loads are in flight together
-            for (int k0 = 0; k0 < n; k0 += AT_ONCE) {
-                float pm[AT_ONCE], pl[AT_ONCE], pw[AT_ONCE];
-                float4 po[AT_ONCE][V];
+        for (int v = 0; v < V; ++v)
+            o[v] = make_float4(o[v].x * f + x[v].x * g, o[v].y * f + x[v].y * g, o[v].z * f + x[v].z * g,
+                               o[v].w * f + x[v].w * g);
+        top = t;
+        topw = tw;
+    }
+
+    __device__ RowSum(const float* parts, const KvCut& cut, int w, int n, int qr, int dim, int from, int step)
+    {
+        constexpr int Q = C::Q;
 #pragma unroll
-                for (int k = 0; k < AT_ONCE; ++k) {
-                    pm[k] = pw[k] = NONE;
-                    pl[k] = 0.f;
-                    if (k0 + k < n) {
-                        const float* from = part(k0 + k);
-                        pm[k] = __ldcg(from + Q * DP + qr);
-                        pl[k] = __ldcg(from + Q * DP + Q + qr);
-                        pw[k] = __ldcg(from + Q * DP + 2 * Q + qr);
+        for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = from; k0 < n; k0 += AT_ONCE * step) {
+            float pm[AT_ONCE], pl[AT_ONCE], pw[AT_ONCE];
+            float4 po[AT_ONCE][V];
 #pragma unroll
-                        for (int v = 0; v < V; ++v)
-                            po[k][v] = __ldcg(reinterpret_cast<const float4*>(from + qr * DP + dim + v * 128));
-                    } else {
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int k = k0 + i * step;
+                pm[i] = pw[i] = NONE;
+                pl[i] = 0.f;
 #pragma unroll
-                        for (int v = 0; v < V; ++v) po[k][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                }
-                float t = top, tw = topw;
+                for (int v = 0; v < V; ++v) po[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < n) {
+                    const int64_t slot = k == n - 1 ? 2 * (int64_t)cut.last + 1
+                                                    : 2 * (int64_t)(k ? (w / cut.per_cta + k) * cut.per_cta : w);
+                    const float* p = parts + slot * C::PART;
+                    pm[i] = __ldcg(p + Q * DP + qr);
+                    pl[i] = __ldcg(p + Q * DP + Q + qr);
+                    pw[i] = __ldcg(p + Q * DP + 2 * Q + qr);
 #pragma unroll
-                for (int k = 0; k < AT_ONCE; ++k) {
-                    t = fmaxf(t, pm[k]);
-                    tw = fmaxf(tw, pw[k]);
-                }
-                sum *= ex2(top - t);
-                const float back = ex2(topw - tw);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    o[v].x *= back;
-                    o[v].y *= back;
-                    o[v].z *= back;
-                    o[v].w *= back;
-                }
-                top = t;
-                topw = tw;
-#pragma unroll
-                for (int k = 0; k < AT_ONCE; ++k) {
-                    sum += pl[k] * ex2(pm[k] - top);
-                    const float f = ex2(pw[k] - topw);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        o[v].x += po[k][v].x * f;
-                        o[v].y += po[k][v].y * f;
-                        o[v].z += po[k][v].z * f;
-                        o[v].w += po[k][v].w * f;
-                    }
+                    for (int v = 0; v < V; ++v)
+                        if (dim < DP) po[i][v] = __ldcg(reinterpret_cast<const float4*>(p + qr * DP + dim + v * 128));
                 }
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                store_out<T>(a, cut.r0 + r / a.group, cut.h * a.group + r % a.group, dim + v * 128, o[v], top, topw, sum);
+            for (int i = 0; i < AT_ONCE; ++i) add(pm[i], pl[i], pw[i], po[i]);
+        }
+    }
+};
+
+// Joins the parts of the segments that were cut, in order.  The first `ones`
+// CTAs take a segment each and a warp for a row; the others take JOIN_ROWS
+// rows of segments of many parts, ROW_WARPS warps for a row, added up in
+// shared memory.
+template <class T, int DP, int NT>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const DecodeArgs d, int workers, int ones)
+{
+    using C = DecCfg<DP, NT>;
+    using Sum = RowSum<C, DP>;
+    constexpr int Q = C::Q, V = Sum::V, GROUPS = Q / JOIN_ROWS;
+    const AttnArgs& a = d.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = lane * 4;
+    const bool shared = (int)blockIdx.x >= ones;
+    const int x = shared ? ((int)blockIdx.x - ones) / GROUPS : (int)blockIdx.x;      // this CTA's entries of the
+    const int step = shared ? ((int)gridDim.x - ones) / GROUPS : ones;               // list: x, x + step, ...
+    const int group = ((int)blockIdx.x - ones) % GROUPS, ri = warp / ROW_WARPS, rw = warp % ROW_WARPS;
+    __shared__ float stat[JOIN_ROWS][ROW_WARPS][3];
+    __shared__ float4 sums[JOIN_ROWS][ROW_WARPS][V][32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_prior_grids();
+    for (int w0 = x; w0 < workers; w0 += 32 * step) {  // 32 entries at a time
+        const int wl = w0 + lane * step;
+        KvCut c;
+        c.last = -1;
+        c.per_cta = 1;
+        if (wl < workers) {
+            c.last = d.cuts[wl].last;
+            c.per_cta = d.cuts[wl].per_cta;
+        }
+        const int nl = c.last < 0 ? 0 : (c.last - 1) / c.per_cta - wl / c.per_cta + 2;
+        uint32_t todo = __ballot_sync(0xFFFFFFFFu, shared ? nl > MANY : nl > 0 && nl <= MANY);
+        for (; todo; todo &= todo - 1) {
+            const int e = __ffs(todo) - 1, w = w0 + e * step, n = __shfl_sync(0xFFFFFFFFu, nl, e);
+            const KvCut cut = d.cuts[w];
+            const int rows = cut.n * a.group - cut.rg * Q;  // of the segment
+            if (!shared) {
+                for (int qr = warp; qr < min(Q, rows); qr += JOIN_WARPS) {
+                    Sum s(d.parts, cut, w, n, qr, dim, 0, 1);
+                    const int r = cut.rg * Q + qr;
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (dim < DP)
+                            store_out<T>(a, cut.r0 + r / a.group, cut.h * a.group + r % a.group, dim + v * 128, s.o[v],
+                                         s.top, s.topw, s.sum);
+                }
+                continue;
+            }
+            if (group * JOIN_ROWS >= rows) continue;
+            const int qr = group * JOIN_ROWS + ri, r = cut.rg * Q + qr;
+            Sum s(d.parts, cut, w, n, qr, dim, rw, ROW_WARPS);
+            __syncthreads();  // the row before is read
+            if (lane == 0) {
+                stat[ri][rw][0] = s.top;
+                stat[ri][rw][1] = s.sum;
+                stat[ri][rw][2] = s.topw;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) sums[ri][rw][v][lane] = s.o[v];
+            __syncthreads();
+            if (rw == 0 && qr < rows) {
+#pragma unroll
+                for (int i = 1; i < ROW_WARPS; ++i) {
+                    float4 y[V];
+#pragma unroll
+                    for (int v = 0; v < V; ++v) y[v] = sums[ri][i][v][lane];
+                    s.add(stat[ri][i][0], stat[ri][i][1], stat[ri][i][2], y);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (dim < DP)
+                        store_out<T>(a, cut.r0 + r / a.group, cut.h * a.group + r % a.group, dim + v * 128, s.o[v], s.top,
+                                     s.topw, s.sum);
+            }
         }
     }
 }
@@ -770,6 +815,9 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 }
             }
     __syncthreads();
+    if (tid == 0)  // this CTA's share of the list: its workers', and of those that there are not
+        for (int i = 0; i < DEC_WARPS; ++i)
+            d.cuts[i < wpc ? blockIdx.x * wpc + i : gridDim.x * wpc + blockIdx.x * (DEC_WARPS - wpc) + i - wpc].last = -1;
     for (int w0 = 0; w0 < wpc;) {
         const int64_t at = seg_at[w0];
         int w1 = w0 + 1;
@@ -843,8 +891,9 @@ bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
     if (!launch_early(kv_decode_kernel<T, DP, NT>, dim3((unsigned)grid), dim3(DEC_WARPS * 32), C::SMEM, s, h->map_k,
                       h->map_v, d))
         return BSP_ERR_CUDA;
-    return launch_early(kv_join_kernel<T, DP, NT>, dim3((unsigned)h->num_sms * 4), dim3(JOIN_WARPS * 32), 0, s, d,
-                        grid * DEC_WARPS)
+    const int ones = h->num_sms * 4, groups = C::Q / JOIN_ROWS, many = std::max(1, h->num_sms * 2 / groups) * groups;
+    return launch_early(kv_join_kernel<T, DP, NT>, dim3((unsigned)(ones + many)), dim3(JOIN_WARPS * 32), 0, s, d,
+                        grid * DEC_WARPS, ones)
                ? BSP_OK
                : BSP_ERR_CUDA;
 }
@@ -856,9 +905,9 @@ bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream
     // request.  Requests with more rows are the prompt kernel's, whose row
     // tiles have 128 rows and whose dims end at 128; a step that has some is
     // taken for one of prompts and single tokens, and the block for a single
-    // token's rows.
+    // token's rows.  Steps of few rows in all stay here, in several blocks.
     const int64_t most = max_new * a.group;
-    const bool prompts = most > 24 && a.c.dim <= 128 && a.s.batch > 0;
+    const bool prompts = most > 24 && a.c.dim <= 128 && a.s.batch > 0 && a.s.rows * a.heads > 1024;
     const int64_t block = prompts ? std::min<int64_t>(a.group, 24) : most;
     const int few = block <= 8 ? 8 : block <= 16 ? 16 : 24;
     if (prompts) {
@@ -903,7 +952,8 @@ bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s)
     const size_t part = c.dim <= 64 ? std::max(floats(DecCfg<64, 1>{}), floats(DecCfg<64, 3>{}))
                         : c.dim <= 128 ? std::max(floats(DecCfg<128, 1>{}), floats(DecCfg<128, 3>{}))
                                        : floats(DecCfg<256, 2>{});
-    if (cudaMalloc(&h->parts, (size_t)h->num_sms * DEC_WARPS * 2 * part * sizeof(float)) != cudaSuccess ||
+    h->part_floats = (size_t)h->num_sms * DEC_WARPS * 2 * part;
+    if (cudaMalloc(&h->parts, h->part_floats * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&h->cuts, workers * sizeof(KvCut)) != cudaSuccess)
         return BSP_ERR_OOM;
     if (cudaMemsetAsync(h->cuts, 0, workers * sizeof(KvCut), s) != cudaSuccess) return BSP_ERR_CUDA;

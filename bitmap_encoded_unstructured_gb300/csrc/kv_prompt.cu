@@ -61,13 +61,36 @@ struct Cfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
+constexpr int MOST_SPLITS = 16;
+
 struct PromptArgs {
     AttnArgs a;
     int* err;
     uint32_t spin_cap;
     int32_t few;
-    int64_t items;  // CTAs of one KV head
+    int32_t splits;  // CTAs that share the cached rows of a row tile pair
+    int64_t items;   // row tile pairs of one KV head
+    float* parts;    // splits > 1: of CTA i and row r, O, m, l, mw at (i ROWS + r) (DP + 4)
 };
+
+// The item a CTA (or its part) works on: request b, its first query row.
+struct Item {
+    int b;
+    int64_t row0;
+};
+
+// Request b's items start at F(b) = q_start[b] * group / ROWS + b: it has at
+// most n * group / ROWS + 1, so F leaves room for them without a scan.
+__device__ __forceinline__ Item item_of(const AttnArgs& a, int64_t item)
+{
+    int b = 0, hi = a.s.batch;
+    while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if ((int64_t)a.s.q_start[mid] * a.group / ROWS + mid <= item) b = mid;
+        else hi = mid;
+    }
+    return {b, (item - ((int64_t)a.s.q_start[b] * a.group / ROWS + b)) * ROWS};
+}
 
 // kind::f16 instruction descriptor: D fp32, A and B fp16, M = 128.
 __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major)
@@ -228,29 +251,23 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // the item: long rows first (later rows of a causal prompt see more),
-    // the heads of one row tile side by side
-    const int h = (int)(blockIdx.x % H);
-    const int64_t item = d.items - 1 - (int64_t)(blockIdx.x / H);
-    int b = 0;
-    {  // request b's items start at F(b) = q_start[b] * group / ROWS + b
-        int hi = a.s.batch;
-        while (hi - b > 1) {
-            const int mid = (b + hi) >> 1;
-            if ((int64_t)a.s.q_start[mid] * a.group / ROWS + mid <= item) b = mid;
-            else hi = mid;
-        }
-    }
+    // the heads of one row tile pair side by side
+    const int piece = (int)(blockIdx.x % d.splits), h = (int)(blockIdx.x / d.splits % H);
+    const Item it = item_of(a, d.items - 1 - (int64_t)(blockIdx.x / d.splits / H));
+    const int b = it.b;
+    const int64_t row0 = it.row0;
     const Request rq = request_of(a.s, sh, b);
     const int64_t rows = (int64_t)rq.n * a.group;
-    const int64_t row0 = (item - ((int64_t)a.s.q_start[b] * a.group / ROWS + b)) * ROWS;
     if (row0 < 0 || row0 >= rows || rows <= d.few) return;
     const int n_rows = (int)min((int64_t)ROWS, rows - row0);
     const bool two = n_rows > 128;
     const int first = rq.len - rq.n;                                 // position of the request's first query
     const int pos0 = first + (int)(row0 / a.group), pos1 = first + (int)((row0 + n_rows - 1) / a.group);
     const int seen = a.window ? max(0, pos0 - a.window + 1) : 0;    // first cached row that a query sees
-    const int t0 = seen & ~(TOK - 1);
-    const int tiles = pos1 >= t0 ? (pos1 + 1 - t0 + TOK - 1) / TOK : 0;
+    const int all_tiles = pos1 >= 0 ? (pos1 + 1 - (seen & ~(TOK - 1)) + TOK - 1) / TOK : 0;
+    const int first_tile = (int)((int64_t)all_tiles * piece / d.splits);
+    const int tiles = (int)((int64_t)all_tiles * (piece + 1) / d.splits) - first_tile;
+    const int t0 = (seen & ~(TOK - 1)) + first_tile * TOK;
     const uint32_t cap = d.spin_cap;
 
     uint64_t* c_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -674,8 +691,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         // ---------------- the rows out
         if (my_tiles && !failed && !wait(o_done + t, 0, cap)) failed = true;
         tc_after();
-        const float f = l > 0.f ? ex2(mw - m) / (l * LIFT) : 0.f;
+        const bool parts = d.splits > 1;
+        const float f = parts ? 1.f / LIFT : l > 0.f ? ex2(mw - m) / (l * LIFT) : 0.f;
         T* out = (T*)a.out + q_tok * a.o_row + (int64_t)head * a.o_head;
+        float* part = d.parts + ((int64_t)blockIdx.x * ROWS + 128 * t + tr) * (DP + 4);
         if (!failed && (t == 0 || two)) {
             for (int cb = 0; cb < dim; cb += 32) {
                 uint32_t x[32];
@@ -684,24 +703,86 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     tmem_ld32(o_at + cb, x);
                     tmem_wait_ld(x, 32);
                 }
+                float o[32];
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    alignas(16) T y[8];
+                for (int i = 0; i < 32; ++i) o[i] = l > 0.f ? __uint_as_float(x[i]) * f : 0.f;
+                if (!mine) continue;
+                if (parts) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] = from_float<T>(l > 0.f ? __uint_as_float(x[i + e]) * f : 0.f);
-                    if (mine && cb + i < dim)
-                        *reinterpret_cast<uint4*>(out + cb + i) = *reinterpret_cast<const uint4*>(y);
+                    for (int i = 0; i < 32; i += 4)
+                        *reinterpret_cast<float4*>(part + cb + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        alignas(16) T y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = from_float<T>(o[i + e]);
+                        if (cb + i < dim) *reinterpret_cast<uint4*>(out + cb + i) = *reinterpret_cast<const uint4*>(y);
+                    }
                 }
             }
-            if (mine && a.lse)
+            if (mine && parts)
+                *reinterpret_cast<float4*>(part + DP) = make_float4(m, l, mw, 0.f);
+            else if (mine && a.lse)
                 a.lse[q_tok * a.heads + head] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
     }
-
     tc_before();
     __syncwarp();
     if (lane == 0) bspx::mbar_arrive(read);
     if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
+}
+
+// The parts of each row of split items joined, a warp a row.
+constexpr int JOIN_THREADS = 256;
+
+template <class T, int DP>
+__global__ void __launch_bounds__(JOIN_THREADS) kv_prompt_join_kernel(const PromptArgs d)
+{
+    wait_prior_grids();
+    const AttnArgs& a = d.a;
+    const int lane = threadIdx.x & 31, H = a.c.heads;
+    const int64_t cta = blockIdx.x / (ROWS / 32);        // of the prompt kernel, before its splits
+    const int h = (int)(cta % H);
+    const Item it = item_of(a, d.items - 1 - cta / H);
+    const Request rq = request_of(a.s, a.c.page_shift, it.b);
+    const int64_t rows = (int64_t)rq.n * a.group;
+    if (it.row0 < 0 || it.row0 >= rows || rows <= d.few) return;
+    for (int i = threadIdx.x / 32; i < 32; i += JOIN_THREADS / 32) {
+        const int tr = (int)(blockIdx.x % (ROWS / 32)) * 32 + i;
+        const int64_t r = it.row0 + tr;
+        if (r >= rows) return;
+        const float* part = d.parts + (cta * d.splits * ROWS + tr) * (DP + 4);
+        const int64_t stride = (int64_t)ROWS * (DP + 4);
+        float m = NONE, mw = NONE, l = 0.f;
+        for (int s = 0; s < d.splits; ++s) {
+            const float4 st = __ldcg(reinterpret_cast<const float4*>(part + s * stride + DP));
+            m = fmaxf(m, st.x);
+            mw = fmaxf(mw, st.z);
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int dim = lane * 4;
+#pragma unroll 4
+        for (int s = 0; s < d.splits; ++s) {
+            const float4 st = __ldcg(reinterpret_cast<const float4*>(part + s * stride + DP));
+            l += st.y * ex2(st.x - m);
+            if (dim < a.c.dim) {
+                const float f = ex2(st.z - mw);
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(part + s * stride + dim));
+                o.x += y.x * f;
+                o.y += y.y * f;
+                o.z += y.z * f;
+                o.w += y.w * f;
+            }
+        }
+        const int64_t tok = rq.r0 + r / a.group, head = (int64_t)h * a.group + r % a.group;
+        const float f = l > 0.f ? ex2(mw - m) / l : 0.f;
+        if (dim < a.c.dim) {
+            alignas(8) T y[4] = {from_float<T>(o.x * f), from_float<T>(o.y * f), from_float<T>(o.z * f), from_float<T>(o.w * f)};
+            *reinterpret_cast<uint2*>((T*)a.out + tok * a.o_row + head * a.o_head + dim) = *reinterpret_cast<const uint2*>(y);
+        }
+        if (a.lse && lane == 0) a.lse[tok * a.heads + head] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
 }
 
 template <class T, int DP>
@@ -713,18 +794,26 @@ bsp_status_t launch(const bsp_kv* h, const PromptArgs& d, cudaStream_t s)
             return cudaFuncSetAttribute(kv_prompt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         }))
         return BSP_ERR_CUDA;
-    const int64_t ctas = d.items * h->view.heads;
+    const int64_t ctas = d.items * h->view.heads * d.splits;
     if (ctas > 0x7FFFFFFF) return BSP_ERR_INVALID_ARG;
-    return launch_early(kv_prompt_kernel<T, DP>, dim3((unsigned)ctas), dim3(THREADS), C::SMEM, s, h->map_k, h->map_v, d)
-               ? BSP_OK
-               : BSP_ERR_CUDA;
+    if (!launch_early(kv_prompt_kernel<T, DP>, dim3((unsigned)ctas), dim3(THREADS), C::SMEM, s, h->map_k, h->map_v, d))
+        return BSP_ERR_CUDA;
+    if (d.splits > 1 && !launch_early(kv_prompt_join_kernel<T, DP>, dim3((unsigned)(d.items * h->view.heads * (ROWS / 32))),
+                                      dim3(JOIN_THREADS), 0, s, d))
+        return BSP_ERR_CUDA;
+    return BSP_OK;
 }
 
 }  // namespace
 
 bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dtype_t dtype, int32_t few, cudaStream_t s)
 {
-    PromptArgs d = {a, h->err, bsp_spin_cap(), few, a.s.rows * a.group / ROWS + a.s.batch};
+    // Few row tiles leave SMs idle: then several CTAs share the cached rows of
+    // each, as many as there are SMs for and the scratch holds
+    const int64_t items = a.s.rows * a.group / ROWS + a.s.batch;
+    const int64_t room = (int64_t)(h->part_floats / ((size_t)ROWS * (a.c.dim > 64 ? 132 : 68)));
+    const int64_t ctas = std::min<int64_t>(h->num_sms, room) / std::max<int64_t>(1, items * a.c.heads);
+    const PromptArgs d = {a, h->err, bsp_spin_cap(), few, (int32_t)std::clamp<int64_t>(ctas, 1, MOST_SPLITS), items, h->parts};
     const bool wide = a.c.dim > 64;
     if (dtype == BSP_FP16) return wide ? launch<__half, 128>(h, d, s) : launch<__half, 64>(h, d, s);
     return wide ? launch<__nv_bfloat16, 128>(h, d, s) : launch<__nv_bfloat16, 64>(h, d, s);
