@@ -646,19 +646,11 @@ def _row_dtype(dtype):
         raise TypeError("rows must be float16 or bfloat16") from None
 
 
-def _raw_stream(stream, index: int):
-    """The stream's handle; None: the device's current stream (read without
-    building a Stream object, which costs as much as a launch)."""
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _int32(name, t, shape, device):
+def _int32(name, t, n, index):
+    """Address of an int32 vector of n entries on device `index`."""
     import torch
-    if t.dtype is not torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+    if t.dtype is not torch.int32 or t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -690,7 +682,7 @@ class KvStep:
         s.slots = torch.empty(tokens, dtype=torch.int64, device=dev)
         s.positions = torch.empty(tokens, **i32)
         s.free_count = torch.empty(1, **i32) if free_count is None else free_count
-        _int32("free_count", s.free_count, (1,), dev)
+        _int32("free_count", s.free_count, 1, s.free_count.get_device())
         s._out = tuple(t.data_ptr() for t in (s.seq_len, s.q_start, s.granted, s.slots, s.positions, s.free_count))
         return s
 
@@ -704,8 +696,8 @@ class KvStep:
         self.block_table = t
         stride = t.stride(0) if batch > 1 else width
         self._c = bsp_kv_step_t(batch, width, stride, t.data_ptr(),
-                                _int32("seq_len", self.seq_len, (batch,), t.device),
-                                _int32("q_start", self.q_start, (batch + 1,), t.device), int(max_new))
+                                _int32("seq_len", self.seq_len, batch, t.get_device()),
+                                _int32("q_start", self.q_start, batch + 1, t.get_device()), int(max_new))
         self._ref = C.addressof(self._c)
 
 
@@ -743,6 +735,13 @@ class KvCache:
         with torch.cuda.device(self.device):
             _check("bsp_kv_create", lib().bsp_kv_create(C.addressof(d), _stream(stream), C.byref(h)))
         self.h = h.value
+        # what the calls of every step use, looked up once: they are as short
+        # as the kernels they launch
+        L = lib()
+        self._plan, self._append, self._read = L.bsp_kv_plan, L.bsp_kv_append, L.bsp_kv_read
+        self._attention = L.bsp_kv_attention
+        self._empty, self._float32, self._int64 = torch.empty, torch.float32, torch.int64
+        self._current, self._scale = torch._C._cuda_getCurrentRawStream, self.dim ** -0.5
 
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, page: int = 64, device=None):
@@ -780,39 +779,44 @@ class KvCache:
         step = KvStep.empty(block_table.shape[0], tokens, block_table.device) if out is None else out
         if step.block_table is not block_table:
             step._bind(block_table, max_new)
-        c = step._c
+        c, index = step._c, self._index
         c.max_new = max_new
-        batch, dev = c.batch, step.device
-        if step.slots is None or step.slots.shape[0] != tokens:
-            raise ValueError("out does not have these tokens (KvStep.empty)")
-        seq_len, q_start, granted, slots, positions, count = step._out
-        pages = free_list.shape
-        st = lib().bsp_kv_plan(
-            self.h, _int32("ctx_len", ctx_len, (batch,), dev), _int32("new_len", new_len, (batch,), dev), batch,
-            c.block_table, c.width, c.table_stride, _int32("free_list", free_list, pages[:1], dev), pages[0],
-            _int32("free_count", free_count, (1,), dev), tokens, seq_len, q_start, granted, slots, positions, count,
-            _raw_stream(stream, self._index))
+        batch, pages = c.batch, free_list.shape[0]
+        if step.slots is None or step.slots.shape[0] != tokens or block_table.get_device() != index:
+            raise ValueError("out does not have these tokens (KvStep.empty), or is not beside the cache")
+        st = self._plan(
+            self.h, _int32("ctx_len", ctx_len, batch, index), _int32("new_len", new_len, batch, index), batch,
+            c.block_table, c.width, c.table_stride, _int32("free_list", free_list, pages, index), pages,
+            _int32("free_count", free_count, 1, index), tokens, *step._out, self._on(stream))
         if st:
             raise BspError("bsp_kv_plan", st)
         return step
 
-    def _rows(self, name, x, heads=None):
-        """(pointer, rows, heads, row stride, head stride) of rows [n][heads][dim]."""
-        shape, strides = x.shape, x.stride()
-        if (len(shape) != 3 or shape[2] != self.dim or strides[2] != 1 or (heads and shape[1] != heads)
-                or x.get_device() != self._index):
-            raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, dim contiguous")
-        return x.data_ptr(), shape[0], shape[1], strides[0], strides[1]
+    def _on(self, stream):
+        """The stream's handle; None: the device's current stream (read without
+        building a Stream object, which costs as much as a launch)."""
+        if stream is None:
+            return self._current(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _refuse(self, name):
+        raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, dim contiguous")
 
     def append(self, step, k, v, stream=None):
         """Quantise new rows ``k``, ``v`` [rows][heads][dim] (float16 or
         bfloat16, views of a QKV output allowed) into the step's pages."""
         dt = _row_dtype(k.dtype)
-        pk, rows, _, kr, kh = self._rows("k", k, self.heads)
-        pv, vrows, _, vr, vh = self._rows("v", v, self.heads)
-        if v.dtype is not k.dtype or vrows != rows:
+        shape, want = k.shape, (self.heads, self.dim)
+        if v.dtype is not k.dtype or v.shape != shape:
             raise ValueError("k and v must have the same shape and type")
-        st = lib().bsp_kv_append(self.h, step._ref, pk, pv, dt, rows, kr, kh, vr, vh, _raw_stream(stream, self._index))
+        if len(shape) != 3 or shape[1:] != want:
+            self._refuse("k")
+        kr, kh, kd = k.stride()
+        vr, vh, vd = v.stride()
+        index = self._index
+        if kd != 1 or vd != 1 or k.get_device() != index or v.get_device() != index:
+            self._refuse("k and v")
+        st = self._append(self.h, step._ref, k.data_ptr(), v.data_ptr(), dt, shape[0], kr, kh, vr, vh, self._on(stream))
         if st:
             raise BspError("bsp_kv_append", st)
 
@@ -820,7 +824,7 @@ class KvCache:
         """Cached rows of int64 ``slots``: (k, v) [n][heads][dim]; zeros for a
         slot outside the cache."""
         import torch
-        if (slots.dtype is not torch.int64 or slots.get_device() != self._index or slots.dim() != 1
+        if (slots.dtype is not self._int64 or slots.get_device() != self._index or slots.dim() != 1
                 or not slots.is_contiguous()):
             raise ValueError(f"slots must be a contiguous int64 vector on {self.device}")
         n = slots.shape[0]
@@ -828,15 +832,15 @@ class KvCache:
         dt = _row_dtype(dtype)
         if out is None:
             shape = (n, self.heads, self.dim)  # two allocations cost less than two views of one
-            k = torch.empty(shape, dtype=dtype, device=self.device)
-            v = torch.empty(shape, dtype=dtype, device=self.device)
+            k = self._empty(shape, dtype=dtype, device=self.device)
+            v = self._empty(shape, dtype=dtype, device=self.device)
         else:
             k, v = out
             for t in (k, v):
-                if t.dtype is not dtype or t.shape != (n, self.heads, self.dim) or not t.is_contiguous():
-                    raise ValueError("out must be two contiguous tensors [n][heads][dim] of the type")
-        st = lib().bsp_kv_read(self.h, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt,
-                               _raw_stream(stream, self._index))
+                if (t.dtype is not dtype or t.shape != (n, self.heads, self.dim) or not t.is_contiguous()
+                        or t.get_device() != self._index):
+                    raise ValueError("out must be two contiguous tensors [n][heads][dim] of the type beside the cache")
+        st = self._read(self.h, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), dt, self._on(stream))
         if st:
             raise BspError("bsp_kv_read", st)
         return k, v
@@ -847,20 +851,28 @@ class KvCache:
         ``window`` rows only if it is positive).  ``scale`` defaults to
         dim ** -0.5.  Returns out, or (out, lse) with float32 lse
         [rows][heads]."""
-        import torch
-        dt = _row_dtype(q.dtype)
-        pq, rows, heads, qr, qh = self._rows("q", q)
+        dt, shape, dim = _row_dtype(q.dtype), q.shape, self.dim
+        if len(shape) != 3 or shape[2] != dim:
+            self._refuse("q")
+        rows, heads, _ = shape
+        qr, qh, qd = q.stride()
+        if qd != 1 or q.get_device() != self._index:
+            self._refuse("q")
         if out is None:
-            out = torch.empty((rows, heads, self.dim), dtype=q.dtype, device=self.device)
-            po, orow, oh = out.data_ptr(), heads * self.dim, self.dim
+            out = self._empty(shape, dtype=q.dtype, device=self.device)
+            orow, oh = heads * dim, dim
         else:
-            if out.dtype is not q.dtype or out.shape != q.shape:
-                raise ValueError("out must have q's shape and type")
-            po, _, _, orow, oh = self._rows("out", out)
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=self.device) if with_lse else None
-        st = lib().bsp_kv_attention(
-            self.h, step._ref, pq, dt, rows, heads, qr, qh, self.dim ** -0.5 if scale is None else scale, window, po,
-            orow, oh, lse.data_ptr() if with_lse else None, _raw_stream(stream, self._index))
+            orow, oh, od = out.stride()
+            if out.dtype is not q.dtype or out.shape != shape or od != 1 or out.get_device() != self._index:
+                raise ValueError("out must have q's shape and type, dim contiguous, beside the cache")
+        if with_lse:
+            lse = self._empty((rows, heads), dtype=self._float32, device=self.device)
+            pl = lse.data_ptr()
+        else:
+            lse = pl = None
+        st = self._attention(self.h, step._ref, q.data_ptr(), dt, rows, heads, qr, qh,
+                             self._scale if scale is None else scale, window, out.data_ptr(), orow, oh, pl,
+                             self._on(stream))
         if st:
             raise BspError("bsp_kv_attention", st)
         return (out, lse) if with_lse else out
