@@ -137,7 +137,7 @@ def test_missing_pages_leave_rows_empty(new):
     check(c, *run(c))
 
 
-@pytest.mark.parametrize("new", [1, 4, 70])
+@pytest.mark.parametrize("new", [1, 4, 70, 90])
 def test_more_rows_than_length(new):
     """Idle requests of a padded batch: rows whose position is negative see nothing."""
     import torch
@@ -149,7 +149,7 @@ def test_more_rows_than_length(new):
     assert torch.isneginf(lse[new:2 * new]).all()
 
 
-@pytest.mark.parametrize("new", [1, 4, 70])
+@pytest.mark.parametrize("new", [1, 4, 70, 120])
 def test_unseen_rows_do_not_matter(new):
     """Garbage in rows and scales that no query sees changes nothing, bit for bit."""
     import torch
@@ -175,7 +175,7 @@ def test_unseen_rows_do_not_matter(new):
     assert torch.equal(out, out2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 40, 200])
 def test_extreme_scales(new):
     """Sharp and flat rows, V scales that span many powers of two, zero scales."""
     import torch
@@ -192,7 +192,7 @@ def test_extreme_scales(new):
     assert torch.isfinite(out).all() and (out == 0).all()
 
 
-@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("new", [1, 40, 600])
 def test_queries_beyond_fp16_range(new):
     """bfloat16 queries whose values fp16 does not hold."""
     import torch
@@ -202,7 +202,7 @@ def test_queries_beyond_fp16_range(new):
         check(d, *run(d, scale=0.125 / f), scale=0.125 / f)
 
 
-@pytest.mark.parametrize("new", [1, 3, 64])
+@pytest.mark.parametrize("new", [1, 3, 64, 200])
 def test_strided_queries_and_outputs(new):
     import torch
     c = case([(100, new), (20, new)], 6, 2, 64, 16, torch.float16, 30 + new)
@@ -230,6 +230,35 @@ def test_same_answer_every_time(new):
     for _ in range(5):
         again = run(c, tensors=t)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("lens,heads,kvh,window", [
+    ([(0, 1100)], 4, 4, 0), ([(5000, 300)], 8, 1, 0), ([(3000, 140), (2, 150)], 8, 2, 100), ([(64, 1), (1000, 260)], 8, 2, 0)])
+def test_prompts_shared_by_several_blocks(lens, heads, kvh, window):
+    """Few row tiles: their cached rows are split and joined."""
+    import torch
+    c = case(lens, heads, kvh, 128, 64, torch.bfloat16, 90)
+    check(c, *run(c, window=window), window=window)
+
+
+@pytest.mark.parametrize("batch", [129, 700])
+def test_many_requests(batch):
+    """More requests than a block has threads, some without rows."""
+    import torch
+    g = np.random.default_rng(batch)
+    lens = [(int(g.integers(0, 90)), int(g.integers(0, 3))) for _ in range(batch)]
+    c = case(lens, 4, 2, 64, 16, torch.float16, 91)
+    check(c, *run(c))
+    lens[3] = (10, 150)
+    c = case(lens, 4, 2, 64, 16, torch.float16, 92)
+    check(c, *run(c))
+
+
+def test_few_streams_of_many_rows():
+    """Segments cut into more parts than one warp joins."""
+    import torch
+    c = case([(40000, 1), (12000, 2)], 16, 1, 128, 16, torch.float16, 93)
+    check(c, *run(c))
 
 
 def test_other_stream_and_graph_replay_on_new_lengths():
