@@ -593,7 +593,7 @@ typedef struct {
     const int32_t *block_table; /* device [batch][width] page numbers          */
     const int32_t *seq_len;   /* device [batch]                                */
     const int32_t *q_start;   /* device [batch + 1], q_start[0] = 0, rising    */
-    int64_t max_new;          /* bound on a request's new rows; 0: not known   */
+    int64_t max_new;          /* bound on a request's new rows, 0: not known; decides kernels, not results */
 } bsp_kv_step_t;
 
 /*
