@@ -178,15 +178,17 @@ __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int64_
         a.lse[row * a.heads + head] = sum > 0.f ? (top + __log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, ROW_WARPS = JOIN_WARPS / JOIN_ROWS;
-constexpr int MANY = 16;  // parts of a segment from which several warps share a row
+constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, ROW_WARPS = JOIN_WARPS / JOIN_ROWS, JOIN_CTAS = 2;
+constexpr int MANY = 8;  // parts of a segment from which several warps share a row
 
 // The parts of a row of one cut segment: the first worker's, one of each
-// further CTA's, and the last worker's.  Lane i adds up dims 4 i .. (and
-// 128 + 4 i ..) of every step-th part from `from` on.
+// further CTA's, and the last worker's; every step-th from `from` on.  L lanes
+// share a row (RPW rows a warp, each of a segment of its own): a lane adds up
+// dims 4 i .. and DP / 2 + 4 i .., and looks after the maxima and sum of one
+// part of those whose loads are in flight together.
 template <class C, int DP>
 struct RowSum {
-    static constexpr int V = DP > 128 ? 2 : 1, AT_ONCE = 8 / V;  // parts whose loads are in flight together
+    static constexpr int L = DP / 8, RPW = 32 / L, V = 2, AT_ONCE = 4;
     float top = NONE, topw = NONE, sum = 0.f;
     float4 o[V];
 
@@ -203,111 +205,152 @@ struct RowSum {
         topw = tw;
     }
 
-    __device__ RowSum(const float* parts, const KvCut& cut, int w, int n, int qr, int dim, int from, int step)
+    // n = 0: no row
+    __device__ RowSum(const float* parts, const KvCut& cut, int w, int n, int qr, int lane, int from, int step)
     {
         constexpr int Q = C::Q;
+        constexpr uint32_t FULL = 0xFFFFFFFFu;
+        const int dim = lane % L * 4, cta = n ? w / cut.per_cta : 0, most = __reduce_max_sync(FULL, n);
+        auto part = [&](int k) {
+            const int slot = k == n - 1 ? 2 * cut.last + 1 : 2 * (k ? (cta + k) * cut.per_cta : w);
+            return parts + (int64_t)slot * C::PART;
+        };
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = from; k0 < n; k0 += AT_ONCE * step) {
-            float pm[AT_ONCE], pl[AT_ONCE], pw[AT_ONCE];
-            float4 po[AT_ONCE][V];
+        for (int k0 = from; k0 < most; k0 += AT_ONCE * step) {
+            const int mine = k0 + lane % AT_ONCE * step;
+            float m = NONE, l = 0.f, mw = NONE;
+            if (mine < n) {
+                const float* p = part(mine) + Q * DP + qr;
+                m = __ldcg(p);
+                l = __ldcg(p + Q);
+                mw = __ldcg(p + 2 * Q);
+            }
+            float4 x[AT_ONCE][V];
 #pragma unroll
             for (int i = 0; i < AT_ONCE; ++i) {
-                const int k = k0 + i * step;
-                pm[i] = pw[i] = NONE;
-                pl[i] = 0.f;
 #pragma unroll
-                for (int v = 0; v < V; ++v) po[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k < n) {
-                    const int64_t slot = k == n - 1 ? 2 * (int64_t)cut.last + 1
-                                                    : 2 * (int64_t)(k ? (w / cut.per_cta + k) * cut.per_cta : w);
-                    const float* p = parts + slot * C::PART;
-                    pm[i] = __ldcg(p + Q * DP + qr);
-                    pl[i] = __ldcg(p + Q * DP + Q + qr);
-                    pw[i] = __ldcg(p + Q * DP + 2 * Q + qr);
+                for (int v = 0; v < V; ++v) x[i][v] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + i * step < n) {
+                    const float* p = part(k0 + i * step) + qr * DP + dim;
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (dim < DP) po[i][v] = __ldcg(reinterpret_cast<const float4*>(p + qr * DP + dim + v * 128));
+                    for (int v = 0; v < V; ++v) x[i][v] = __ldcg(reinterpret_cast<const float4*>(p + v * (DP / 2)));
                 }
             }
+            float t = fmaxf(top, m), tw = fmaxf(topw, mw);
 #pragma unroll
-            for (int i = 0; i < AT_ONCE; ++i) add(pm[i], pl[i], pw[i], po[i]);
+            for (int i = 1; i < AT_ONCE; i <<= 1) {
+                t = fmaxf(t, __shfl_xor_sync(FULL, t, i));
+                tw = fmaxf(tw, __shfl_xor_sync(FULL, tw, i));
+            }
+            l *= ex2(m - t);
+#pragma unroll
+            for (int i = 1; i < AT_ONCE; i <<= 1) l += __shfl_xor_sync(FULL, l, i);
+            sum = sum * ex2(top - t) + l;
+            const float f = ex2(topw - tw), g = ex2(mw - tw);
+            top = t;
+            topw = tw;
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = make_float4(o[v].x * f, o[v].y * f, o[v].z * f, o[v].w * f);
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const float gi = __shfl_sync(FULL, g, i, L);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    o[v].x += x[i][v].x * gi;
+                    o[v].y += x[i][v].y * gi;
+                    o[v].z += x[i][v].z * gi;
+                    o[v].w += x[i][v].w * gi;
+                }
+            }
         }
     }
 };
 
-// Joins the parts of the segments that were cut, in order.  The first `ones`
-// CTAs take a segment each and a warp for a row; the others take JOIN_ROWS
-// rows of segments of many parts, ROW_WARPS warps for a row, added up in
-// shared memory.
+// Joins the parts of the segments that were cut, in order.  A CTA looks at 32
+// entries of the list (or 32 of every lists * 32) with team - 1 others and
+// takes rows of their segments: L lanes a row, or for segments of many parts
+// ROW_WARPS warps that add up in shared memory.
 template <class T, int DP, int NT>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_kernel(const DecodeArgs d, int workers, int ones)
+__global__ void __launch_bounds__(JOIN_WARPS * 32, JOIN_CTAS) kv_join_kernel(const DecodeArgs d, int workers)
 {
     using C = DecCfg<DP, NT>;
     using Sum = RowSum<C, DP>;
-    constexpr int Q = C::Q, V = Sum::V, GROUPS = Q / JOIN_ROWS;
+    constexpr int Q = C::Q, V = Sum::V, L = Sum::L, RPW = Sum::RPW;
+    constexpr uint32_t FULL = 0xFFFFFFFFu;
     const AttnArgs& a = d.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, dim = lane * 4;
-    const bool shared = (int)blockIdx.x >= ones;
-    const int x = shared ? ((int)blockIdx.x - ones) / GROUPS : (int)blockIdx.x;      // this CTA's entries of the
-    const int step = shared ? ((int)gridDim.x - ones) / GROUPS : ones;               // list: x, x + step, ...
-    const int group = ((int)blockIdx.x - ones) % GROUPS, ri = warp / ROW_WARPS, rw = warp % ROW_WARPS;
-    __shared__ float stat[JOIN_ROWS][ROW_WARPS][3];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / L;
+    const int ri = warp / ROW_WARPS, rw = warp % ROW_WARPS;
+    const int lists = min((workers + 31) / 32, (int)gridDim.x), team = (int)gridDim.x / lists;
+    const int member = (int)blockIdx.x / lists;
+    __shared__ float stat[JOIN_ROWS][ROW_WARPS][RPW][3];
     __shared__ float4 sums[JOIN_ROWS][ROW_WARPS][V][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     wait_prior_grids();
-    for (int w0 = x; w0 < workers; w0 += 32 * step) {  // 32 entries at a time
-        const int wl = w0 + lane * step;
-        KvCut c;
-        c.last = -1;
-        c.per_cta = 1;
-        if (wl < workers) {
-            c.last = d.cuts[wl].last;
-            c.per_cta = d.cuts[wl].per_cta;
+    if (member >= team) return;
+    auto out = [&](const Sum& s, const KvCut& cut, int qr) {
+        const int r = cut.rg * Q + qr, of = r / a.group;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            store_out<T>(a, cut.r0 + of, cut.h * a.group + r - of * a.group, lane % L * 4 + v * (DP / 2), s.o[v], s.top,
+                         s.topw, s.sum);
+    };
+    for (int w0 = (int)blockIdx.x % lists * 32; w0 < workers; w0 += lists * 32) {
+        KvCut mine = {-1, 1, 0, 0, 0, 0, {0, 0}};
+        if (w0 + lane < workers) mine = d.cuts[w0 + lane];
+        int n_mine = 0, rows_mine = 0;  // parts and rows of this lane's segment
+        if (mine.last >= 0) {
+            n_mine = (mine.last - 1) / mine.per_cta - (w0 + lane) / mine.per_cta + 2;
+            rows_mine = min(Q, mine.n * a.group - mine.rg * Q);
         }
-        const int nl = c.last < 0 ? 0 : (c.last - 1) / c.per_cta - wl / c.per_cta + 2;
-        uint32_t todo = __ballot_sync(0xFFFFFFFFu, shared ? nl > MANY : nl > 0 && nl <= MANY);
-        for (; todo; todo &= todo - 1) {
-            const int e = __ffs(todo) - 1, w = w0 + e * step, n = __shfl_sync(0xFFFFFFFFu, nl, e);
-            const KvCut cut = d.cuts[w];
-            const int rows = cut.n * a.group - cut.rg * Q;  // of the segment
-            if (!shared) {
-                for (int qr = warp; qr < min(Q, rows); qr += JOIN_WARPS) {
-                    Sum s(d.parts, cut, w, n, qr, dim, 0, 1);
-                    const int r = cut.rg * Q + qr;
+        auto cut_of = [&](int e) {
+            return KvCut{__shfl_sync(FULL, mine.last, e), __shfl_sync(FULL, mine.per_cta, e),
+                         __shfl_sync(FULL, mine.r0, e),   __shfl_sync(FULL, mine.n, e),
+                         __shfl_sync(FULL, mine.h, e),    __shfl_sync(FULL, mine.rg, e), {0, 0}};
+        };
+        // segments of few parts: their rows in order, each to the next L lanes
+        int upto = n_mine <= MANY ? rows_mine : 0;
+        const int few = upto;
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (dim < DP)
-                            store_out<T>(a, cut.r0 + r / a.group, cut.h * a.group + r % a.group, dim + v * 128, s.o[v],
-                                         s.top, s.topw, s.sum);
+        for (int i = 1; i < 32; i <<= 1) {
+            const int y = __shfl_up_sync(FULL, upto, i);
+            if (lane >= i) upto += y;
+        }
+        const int all = __shfl_sync(FULL, upto, 31);
+        for (int i0 = (member * JOIN_WARPS + warp) * RPW; i0 < all; i0 += team * JOIN_WARPS * RPW) {
+            const int i = i0 + sub;
+            int e = 0;  // the first lane whose `upto` is beyond i
+#pragma unroll
+            for (int y = 16; y; y >>= 1)
+                if (__shfl_sync(FULL, upto, e + y - 1) <= i) e += y;
+            const int qr = i - __shfl_sync(FULL, upto - few, e), n = __shfl_sync(FULL, n_mine, e);
+            const KvCut cut = cut_of(e);
+            const Sum s(d.parts, cut, w0 + e, i < all ? n : 0, qr, lane, 0, 1);
+            if (i < all) out(s, cut, qr);
+        }
+        for (uint32_t todo = __ballot_sync(FULL, n_mine > MANY); todo; todo &= todo - 1) {
+            const int e = __ffs(todo) - 1, n = __shfl_sync(FULL, n_mine, e), rows = __shfl_sync(FULL, rows_mine, e);
+            const KvCut cut = cut_of(e);
+            for (int q0 = member * JOIN_ROWS * RPW; q0 < rows; q0 += team * JOIN_ROWS * RPW) {
+                const int qr = q0 + ri * RPW + sub;
+                Sum s(d.parts, cut, w0 + e, qr < rows ? n : 0, qr, lane, rw, ROW_WARPS);
+                __syncthreads();  // the rows before are read
+                if (lane % L == 0) {
+                    stat[ri][rw][sub][0] = s.top;
+                    stat[ri][rw][sub][1] = s.sum;
+                    stat[ri][rw][sub][2] = s.topw;
                 }
-                continue;
-            }
-            if (group * JOIN_ROWS >= rows) continue;
-            const int qr = group * JOIN_ROWS + ri, r = cut.rg * Q + qr;
-            Sum s(d.parts, cut, w, n, qr, dim, rw, ROW_WARPS);
-            __syncthreads();  // the row before is read
-            if (lane == 0) {
-                stat[ri][rw][0] = s.top;
-                stat[ri][rw][1] = s.sum;
-                stat[ri][rw][2] = s.topw;
-            }
 #pragma unroll
-            for (int v = 0; v < V; ++v) sums[ri][rw][v][lane] = s.o[v];
-            __syncthreads();
-            if (rw == 0 && qr < rows) {
+                for (int v = 0; v < V; ++v) sums[ri][rw][v][lane] = s.o[v];
+                __syncthreads();
+                if (rw == 0 && qr < rows) {
 #pragma unroll
-                for (int i = 1; i < ROW_WARPS; ++i) {
-                    float4 y[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) y[v] = sums[ri][i][v][lane];
-                    s.add(stat[ri][i][0], stat[ri][i][1], stat[ri][i][2], y);
+                    for (int i = 1; i < ROW_WARPS; ++i) {
+                        const float4 y[V] = {sums[ri][i][0][lane], sums[ri][i][1][lane]};
+                        s.add(stat[ri][i][sub][0], stat[ri][i][sub][1], stat[ri][i][sub][2], y);
+                    }
+                    out(s, cut, qr);
                 }
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (dim < DP)
-                        store_out<T>(a, cut.r0 + r / a.group, cut.h * a.group + r % a.group, dim + v * 128, s.o[v], s.top,
-                                     s.topw, s.sum);
             }
         }
     }
@@ -891,9 +934,8 @@ bsp_status_t launch_decode(const bsp_kv* h, const DecodeArgs& d, cudaStream_t s)
     if (!launch_early(kv_decode_kernel<T, DP, NT>, dim3((unsigned)grid), dim3(DEC_WARPS * 32), C::SMEM, s, h->map_k,
                       h->map_v, d))
         return BSP_ERR_CUDA;
-    const int ones = h->num_sms * 4, groups = C::Q / JOIN_ROWS, many = std::max(1, h->num_sms * 2 / groups) * groups;
-    return launch_early(kv_join_kernel<T, DP, NT>, dim3((unsigned)(ones + many)), dim3(JOIN_WARPS * 32), 0, s, d,
-                        grid * DEC_WARPS, ones)
+    return launch_early(kv_join_kernel<T, DP, NT>, dim3((unsigned)(h->num_sms * JOIN_CTAS)), dim3(JOIN_WARPS * 32), 0, s,
+                        d, grid * DEC_WARPS)
                ? BSP_OK
                : BSP_ERR_CUDA;
 }
