@@ -69,7 +69,8 @@ __device__ __forceinline__ int holder(const int* P, int n, int x)
 // takes its share of the requests, granted pages, returned pages and rows:
 // no CTA waits for another, and one launch does it all.  Granted pages that
 // are being returned in the same step are read from the returning request's
-// block table row, which nobody writes, not from the stack.
+// block table row, which nobody writes, not from the stack.  Bound by the
+// launch and the chain of sums: 5.6 us for 64 requests, 6.7 us for 1024.
 __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_kernel(const PlanArgs a)
 {
     wait_prior_grids();
@@ -245,7 +246,10 @@ __device__ __forceinline__ uint2 codes_of(const uint4& raw, float scale, float i
 // WARPS warps (1 or 4) per unit: a page that receives rows, a head, K or V.
 // Two passes over the unit's rows, its largest value and its codes; the first
 // CACHED vectors of a thread stay in registers between them.  1 << lane_shift
-// threads share a row, one 16-byte vector each.
+// threads share a row, one 16-byte vector each.  2 bytes in and 1 out a value,
+// bound by issue slots (66%: the codes' products, tie checks and permutes):
+// 15879 bfloat16 rows of 8 heads of 128 take 28.5 us, 3.4 TB/s; single rows
+// are bound by the latency of request search, scale, rows and codes (4 us).
 template <class T, int WARPS>
 __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendArgs a, const int lane_shift)
 {
@@ -370,7 +374,8 @@ constexpr int READ_AT_ONCE = 4;  // units of a thread in flight
 
 // A thread takes units of 8 values, so that a warp's loads and stores are
 // whole lines; K and V by blockIdx.y.  CTA x takes
-// pieces x, x + gridDim.x, ... of `rows` rows each.
+// pieces x, x + gridDim.x, ... of `rows` rows each.  Bound by memory: 15879
+// rows of 8 heads of 128, 98 MB, take 18.9 us (5.2 TB/s), 30011 rows 33.6 us.
 template <class T>
 __global__ void __launch_bounds__(256) kv_read_kernel(const ReadArgs a)
 {

@@ -23,6 +23,12 @@
 // Tensor memory: S0, S1 (128 fp32 columns each; W takes the lower half of
 // its own S), O0, O1.  Products of one thread run in order, so the next S
 // may be asked for right after the product that reads W.
+//
+// Bound by issue slots and each row tile's chain S -> P -> W -> S: a prompt of
+// 8101 rows, 64 heads over 8 KV heads of 128, takes 846 us (1075 TFLOP at 1271
+// TFLOP/s, 0.65 of the library's bf16 product).  Two threads a row (16
+// softmax warps of 96 registers) were slower, 1070 us: a barrier a tile joins
+// the halves, and half the registers spill.
 #include "bsp_kv.cuh"
 
 #include <algorithm>
@@ -733,7 +739,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
 }
 
-// The parts of each row of split items joined, a warp a row.
+// The parts of each row of split items joined, a warp a row: O and l weighed by
+// 2 to the part's maximum less the row's.  Bound by latency (a few loads in
+// a row); it runs only where few row tiles left SMs idle.
 constexpr int JOIN_THREADS = 256;
 
 template <class T, int DP>
