@@ -668,10 +668,12 @@ class KvStep:
 
     @classmethod
     def empty(cls, batch: int, tokens: int, device=None, free_count=None):
-        """Buffers for ``KvCache.plan(..., out=step)``: a server keeps one step
+        """Buffers for ``KvCache.plan(..., out=step)``: a server keeps a step
         and plans into it again and again.  ``free_count``: the tensor that
         receives the new count; the one that the plan reads updates it in
-        place."""
+        place.  No other array may be read and written by one plan: lengths
+        that come from a step's ``seq_len`` are copied first, or two steps
+        take turns."""
         import torch
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         s = cls.__new__(cls)

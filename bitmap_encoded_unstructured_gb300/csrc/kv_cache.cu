@@ -429,6 +429,19 @@ void free_kv(bsp_kv* h)
     delete h;
 }
 
+// Do bytes [p, p + n) meet one of `rows` pieces of `len` bytes, `stride` apart
+// from q on?
+bool meet(const void* p, int64_t n, const void* q, int64_t len, int64_t rows = 1, int64_t stride = 0)
+{
+    if (n <= 0 || len <= 0 || rows <= 0) return false;
+    const int64_t lo = (int64_t)((uintptr_t)p - (uintptr_t)q), hi = lo + n;
+    if (rows == 1 || stride <= 0) return lo < len && hi > 0;
+    if (hi <= 0 || lo >= (rows - 1) * stride + len) return false;
+    // the row that p lies in or behind, and the next one
+    const int64_t b = std::max<int64_t>(lo, 0) / stride;
+    return lo < b * stride + len || (b + 1 < rows && hi > (b + 1) * stride);
+}
+
 bool good_strides(int64_t row, int64_t head, int32_t dim, int64_t rows, int32_t heads)
 {
     return (row % 8) == 0 && (head % 8) == 0 && (rows < 2 || row >= 0) && (heads < 2 || head >= dim);
@@ -534,6 +547,26 @@ bsp_status_t bsp_kv_plan(bsp_kv_t h, const int32_t* ctx_len, const int32_t* new_
     if (batch && (!ctx_len || !new_len || !block_table || !seq_len || !granted)) return BSP_ERR_INVALID_ARG;
     if ((free_capacity && !free_list) || (tokens && (!slots || !positions))) return BSP_ERR_INVALID_ARG;
     if (batch && (width < 1 || table_stride < width)) return BSP_ERR_SHAPE;
+    // every CTA reads the lengths and the stack while others write their
+    // shares: what is written shares memory with nothing else of the call (but
+    // the count, which the last CTA writes)
+    struct Piece {
+        const void* at;
+        int64_t bytes;
+    };
+    const Piece of[] = {{seq_len, 4 * (int64_t)batch},      {q_start, 4 * ((int64_t)batch + 1)},
+                        {granted, 4 * (int64_t)batch},      {slots, 8 * tokens},
+                        {positions, 4 * tokens},            {free_list, 4 * (int64_t)free_capacity},
+                        {free_count_out, 4},                {free_count, 4},
+                        {ctx_len, 4 * (int64_t)batch},      {new_len, 4 * (int64_t)batch}};
+    constexpr int WRITTEN = 7, ALL = 10;
+    for (int i = 0; i < ALL; ++i) {
+        if (meet(of[i].at, of[i].bytes, block_table, 4 * (int64_t)width, batch, 4 * table_stride))
+            return BSP_ERR_INVALID_ARG;
+        for (int j = i + 1; i < WRITTEN && j < ALL; ++j)
+            if (meet(of[i].at, of[i].bytes, of[j].at, of[j].bytes) && !(i == 6 && j == 7 && of[i].at == of[j].at))
+                return BSP_ERR_INVALID_ARG;
+    }
     DeviceGuard g(h->device);
     if (!g.ok) return BSP_ERR_CUDA;
     static bsp_attr_once attr_once;

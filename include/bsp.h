@@ -632,6 +632,10 @@ bsp_status_t bsp_kv_check(bsp_kv_t h, bsp_stream_t stream);
  * Outputs: seq_len [batch] (0 for an ended request), q_start [batch + 1],
  * granted [batch], slots [tokens] (page * page_size + row, int64) and
  * positions [tokens] of the granted rows, -1 beyond them.
+ * An array that is written (the outputs, block_table, free_list) shares
+ * memory with no other array of the call, but for free_count_out and
+ * free_count: BSP_ERR_INVALID_ARG.  So a step's seq_len is not at once the
+ * next plan's ctx_len and seq_len: plan into two steps in turn, or copy it.
  */
 bsp_status_t bsp_kv_plan(bsp_kv_t h, const int32_t *ctx_len, const int32_t *new_len, int32_t batch,
                          int32_t *block_table, int32_t width, int64_t table_stride, int32_t *free_list,
