@@ -162,19 +162,20 @@ struct Split {
     }
 };
 
-// Four dims of one query row, joined: out = O 2^(mw - m) / l.
+// Four dims of one query row, joined: out = O 2^(mw - m) / l.  A sum of 0 is a
+// row that sees nothing; a NaN query's sum is NaN, and so is its row.
 template <class T>
 __device__ __forceinline__ void store_out(const AttnArgs& a, int64_t row, int64_t head, int dim, float4 o, float top,
                                           float topw, float sum)
 {
-    const float f = sum > 0.f ? ex2(topw - top) / sum : 0.f;
+    const float f = sum != 0.f ? ex2(topw - top) / sum : 0.f;
     if (dim < a.c.dim) {
         alignas(8) T y[4] = {from_float<T>(o.x * f), from_float<T>(o.y * f), from_float<T>(o.z * f),
                              from_float<T>(o.w * f)};
         *reinterpret_cast<uint2*>((T*)a.out + row * a.o_row + head * a.o_head + dim) = *reinterpret_cast<const uint2*>(y);
     }
     if (a.lse && dim == 0)
-        a.lse[row * a.heads + head] = sum > 0.f ? (top + __log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        a.lse[row * a.heads + head] = sum != 0.f ? (top + __log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
 constexpr int JOIN_WARPS = 8, JOIN_ROWS = 2, ROW_WARPS = JOIN_WARPS / JOIN_ROWS, JOIN_CTAS = 2;

@@ -694,11 +694,11 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             __syncwarp();
             if (lane == 0) bspx::mbar_arrive(p_full + t);
         }
-        // ---------------- the rows out
+        // ---------------- the rows out (l = 0: the row sees nothing; NaN: so is its query)
         if (my_tiles && !failed && !wait(o_done + t, 0, cap)) failed = true;
         tc_after();
         const bool parts = d.splits > 1;
-        const float f = parts ? 1.f / LIFT : l > 0.f ? ex2(mw - m) / (l * LIFT) : 0.f;
+        const float f = parts ? 1.f / LIFT : l != 0.f ? ex2(mw - m) / (l * LIFT) : 0.f;
         T* out = (T*)a.out + q_tok * a.o_row + (int64_t)head * a.o_head;
         float* part = d.parts + ((int64_t)blockIdx.x * ROWS + 128 * t + tr) * (DP + 4);
         if (!failed && (t == 0 || two)) {
@@ -711,7 +711,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 }
                 float o[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = l > 0.f ? __uint_as_float(x[i]) * f : 0.f;
+                for (int i = 0; i < 32; ++i) o[i] = l != 0.f ? __uint_as_float(x[i]) * f : 0.f;
                 if (!mine) continue;
                 if (parts) {
 #pragma unroll
@@ -730,7 +730,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             if (mine && parts)
                 *reinterpret_cast<float4*>(part + DP) = make_float4(m, l, mw, 0.f);
             else if (mine && a.lse)
-                a.lse[q_tok * a.heads + head] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+                a.lse[q_tok * a.heads + head] = l != 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
     }
     tc_before();
@@ -784,12 +784,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) kv_prompt_join_kernel(const Prom
             }
         }
         const int64_t tok = rq.r0 + r / a.group, head = (int64_t)h * a.group + r % a.group;
-        const float f = l > 0.f ? ex2(mw - m) / l : 0.f;
+        const float f = l != 0.f ? ex2(mw - m) / l : 0.f;
         if (dim < a.c.dim) {
             alignas(8) T y[4] = {from_float<T>(o.x * f), from_float<T>(o.y * f), from_float<T>(o.z * f), from_float<T>(o.w * f)};
             *reinterpret_cast<uint2*>((T*)a.out + tok * a.o_row + head * a.o_head + dim) = *reinterpret_cast<const uint2*>(y);
         }
-        if (a.lse && lane == 0) a.lse[tok * a.heads + head] = l > 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (a.lse && lane == 0) a.lse[tok * a.heads + head] = l != 0.f ? (m + __log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
 }
 

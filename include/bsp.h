@@ -681,7 +681,7 @@ bsp_status_t bsp_kv_read(bsp_kv_t h, const int64_t *slots, int64_t n, void *k, v
  *   out    device [rows][heads][dim], q's dtype and rules.
  *   lse    device fp32 [rows][heads] contiguous, log sum_j p_j, or NULL.
  * A row that sees nothing, and rows from q_start[batch] on, get out = 0 and
- * lse = -inf.  Logits, maxima and sums are fp32; a probability (relative to
+ * lse = -inf; a NaN in a query that sees something gives NaN.  Logits, maxima and sums are fp32; a probability (relative to
  * the largest seen) times its V scale is rounded to fp16 for the product.
  */
 bsp_status_t bsp_kv_attention(bsp_kv_t h, const bsp_kv_step_t *step, const void *q, bsp_dtype_t dtype,
