@@ -43,6 +43,7 @@ struct bsp_kv {
     // rows of a page by 64 or 128 dims, swizzled by their width (kv_decode)
     CUtensorMap map_k, map_v;
     int* ticket;  // arrivals of a plan whose count is updated in place; zero between calls
+    int* ready;   // 1 while the prompt kernel of an attention call runs, 0 between calls
     int* err;     // as bsp_handle::err
     // few queries: parts of segments cut between warps, two slots a warp, and
     // the cut segments by the warp that begins them (last = -1: none)
@@ -188,8 +189,9 @@ void attention_free(bsp_kv* h);
 }  // namespace bspkv
 
 // Attention of the requests with more than `few` query rows per KV head
-// (kv_prompt.cu); dim <= 128.
-bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dtype_t dtype, int32_t few,
+// (kv_prompt.cu); dim <= 128.  `beside`: the kernel launched next may start
+// while this one runs, see bsp_kv::ready; otherwise it starts behind it.
+bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dtype_t dtype, int32_t few, bool* beside,
                                cudaStream_t s);
 
 bsp_status_t bsp_run_kv_attention(const bsp_kv* h, const KvStepView& st, int64_t max_new, const void* q,

@@ -84,7 +84,8 @@ struct DecodeArgs {
     int* err;
     uint32_t spin_cap;
     int32_t most_rows;  // requests with more query rows than this (per KV head) are not this kernel's
-    bool beside;        // runs beside the prompt kernel, which waited for what came before
+    int* ready;         // set by the prompt kernel of this call (null: there is none)
+    bool beside;        // runs beside the prompt kernel
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, JOIN_CTAS) kv_join_kernel(con
     __shared__ float4 sums[JOIN_ROWS][ROW_WARPS][V][32];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     wait_prior_grids();
+    if (d.ready && blockIdx.x == 0 && threadIdx.x == 0) *d.ready = 0;
     if (member >= team) return;
     auto out = [&](const Sum& s, const KvCut& cut, int qr) {
         const int r = cut.rg * Q + qr, of = r / a.group;
@@ -359,6 +361,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32, JOIN_CTAS) kv_join_kernel(con
     }
 }
 
+__device__ __forceinline__ bool is_ready(const int* ready)
+{
+    int r;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(r) : "l"(ready) : "memory");
+    return r != 0;
+}
+
 // Bound by memory at 8 queries: 64 ragged streams of 8 KV heads, 391 MB of
 // codes, take 72 us (5.4 TB/s; 6.1 TB/s while warps work, the rest is the
 // start and uneven ends).  At 24 queries by the latency of two warps a
@@ -383,8 +392,11 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     if (lane < C::STAGES) bspx::mbar_init(full + lane, 1);
     bspx::fence_mbar_init();
     // launched before the kernel ahead of it is done; beside the prompt kernel
-    // it only has to end after it
-    if (!d.beside) wait_prior_grids();
+    // it only has to end after it, but it has to see what the kernels before
+    // both wrote: through `ready`, or (not set yet) by waiting all the same
+    if (d.beside && is_ready(d.ready)) asm volatile("fence.proxy.async.global;" ::: "memory");  // codes come by TMA
+    else wait_prior_grids();
+    __syncwarp();
 
     // the shared run: each thread sums some requests; pre[i] is what comes
     // before thread i's
@@ -959,11 +971,14 @@ bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream
     const bool prompts = most > 24 && a.c.dim <= 128 && a.s.batch > 0 && a.s.rows * a.heads > 1024;
     const int64_t block = prompts ? std::min<int64_t>(a.group, 24) : most;
     const int few = block <= 8 ? 8 : block <= 16 ? 16 : 24;
+    bool beside = false;
     if (prompts) {
-        const bsp_status_t st = bsp_run_kv_prompt(h, a, std::is_same<T, __half>::value ? BSP_FP16 : BSP_BF16, few, s);
+        const bsp_status_t st =
+            bsp_run_kv_prompt(h, a, std::is_same<T, __half>::value ? BSP_FP16 : BSP_BF16, few, &beside, s);
         if (st != BSP_OK) return st;
     }
-    const DecodeArgs d = {a, h->parts, h->cuts, h->err, bsp_spin_cap(), prompts ? few : INT32_MAX, prompts};
+    const DecodeArgs d = {a, h->parts, h->cuts, h->err, bsp_spin_cap(), prompts ? few : INT32_MAX,
+                          prompts ? h->ready : nullptr, beside};
     if (a.c.dim <= 64)
         return few == 8 ? launch_decode<T, 64, 1>(h, d, s) : few == 16 ? launch_decode<T, 64, 2>(h, d, s)
                                                                        : launch_decode<T, 64, 3>(h, d, s);

@@ -71,7 +71,7 @@ constexpr int MOST_SPLITS = 16;
 
 struct PromptArgs {
     AttnArgs a;
-    int* err;
+    int *err, *ready;
     uint32_t spin_cap;
     int32_t few;
     int32_t splits;  // CTAs that share the cached rows of a row tile pair
@@ -253,8 +253,13 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
 
     wait_prior_grids();
     // what comes next (the kernel of the other requests) may fill the SMs
-    // that this one leaves idle
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // that this one leaves idle.  Its launch orders no memory: what the
+    // kernels before this one wrote it sees through `ready`, released here
+    // after they are known to be done
+    if (threadIdx.x == 0) {
+        if (blockIdx.x == 0) asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(d.ready) : "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
 
     // the item: long rows first (later rows of a causal prompt see more),
     // the heads of one row tile pair side by side
@@ -814,14 +819,17 @@ bsp_status_t launch(const bsp_kv* h, const PromptArgs& d, cudaStream_t s)
 
 }  // namespace
 
-bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dtype_t dtype, int32_t few, cudaStream_t s)
+bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dtype_t dtype, int32_t few, bool* beside,
+                               cudaStream_t s)
 {
     // Few row tiles leave SMs idle: then several CTAs share the cached rows of
     // each, as many as there are SMs for and the scratch holds
     const int64_t items = a.s.rows * a.group / ROWS + a.s.batch;
     const int64_t room = (int64_t)(h->part_floats / ((size_t)ROWS * (a.c.dim > 64 ? 132 : 68)));
     const int64_t ctas = std::min<int64_t>(h->num_sms, room) / std::max<int64_t>(1, items * a.c.heads);
-    const PromptArgs d = {a, h->err, bsp_spin_cap(), few, (int32_t)std::clamp<int64_t>(ctas, 1, MOST_SPLITS), items, h->parts};
+    const PromptArgs d = {a, h->err, h->ready, bsp_spin_cap(), few, (int32_t)std::clamp<int64_t>(ctas, 1, MOST_SPLITS),
+                          items, h->parts};
+    *beside = d.splits == 1;  // else the joining kernel is in between
     const bool wide = a.c.dim > 64;
     if (dtype == BSP_FP16) return wide ? launch<__half, 128>(h, d, s) : launch<__half, 64>(h, d, s);
     return wide ? launch<__nv_bfloat16, 128>(h, d, s) : launch<__nv_bfloat16, 64>(h, d, s);

@@ -41,3 +41,54 @@ def test_two_steps_take_turns():
         cache.plan(ctx, dev(new.astype(np.int32)), table, free, count, tokens=64, out=step)
     assert e.value.status == 1
     cache.close()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads,kvh", [(32, 8), (8, 2)])  # prompt and decode kernel side by side; one behind the other
+def test_attention_sees_the_append_before_it(heads, kvh, dtype):
+    """A chunk of a prompt and single tokens, step after step, into pages that
+    hold earlier rows and whose scales grow: the same bits whether or not the
+    host waits between the calls."""
+    import torch
+    dtype, page, dim, steps, chunk, streams = getattr(torch, dtype), 64, 64, 40, 130, 16
+    batch = streams + 1
+    counts = [kv.pages_of(chunk * steps, page)] + [kv.pages_of(200 + steps, page)] * streams
+    pages = sum(counts)
+    table = torch.full((batch, max(counts)), -1, dtype=torch.int32)
+    at = 0
+    for b, n in enumerate(counts):
+        table[b, :n] = torch.arange(at, at + n)
+        at += n
+    table = table.cuda()
+    g = torch.Generator(device="cuda").manual_seed(6)
+    new = torch.tensor([chunk] + [1] * streams)
+    start = torch.cat([torch.zeros(1, dtype=torch.long), new.cumsum(0)]).int().cuda()
+    first = torch.tensor([0] + [200 - 7 * b for b in range(streams)])
+    rows = int(new.sum())
+    x = [[torch.randn(rows, h, dim, device="cuda", generator=g).mul_(1.15 ** i if j else 1.0).to(dtype)
+          for j, h in enumerate((heads, kvh, kvh))] for i in range(steps)]
+    seq = [(first + new * (i + 1)).int().cuda() for i in range(steps)]
+
+    def go(wait):
+        cache = bsp.KvCache.empty(pages, kvh, dim, page)
+        cache.k_scale.fill_(0.01)
+        cache.v_scale.fill_(0.01)
+        got = []
+        torch.cuda.synchronize()
+        for (q, k, v), s in zip(x, seq):
+            step = bsp.KvStep(table, s, start, max_new=chunk)
+            cache.append(step, k, v)
+            if wait:
+                torch.cuda.synchronize()
+            got.append(cache.attention(step, q, with_lse=True))
+            if wait:
+                torch.cuda.synchronize()
+        cache.check()
+        got.append((cache.k_scale, cache.v_scale))
+        cache.close()
+        return got
+
+    want = go(True)
+    for _ in range(4):
+        for (a, b), (c, d) in zip(want, go(False)):
+            assert torch.equal(a, c) and torch.equal(b, d)
