@@ -86,6 +86,7 @@ struct DecodeArgs {
     int32_t most_rows;  // requests with more query rows than this (per KV head) are not this kernel's
     int* ready;         // set by the prompt kernel of this call (null: there is none)
     bool beside;        // runs beside the prompt kernel
+    bool stall;         // test only: each warp skips the copies of its first sub-tile
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -436,13 +437,13 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     int filled = 0;
     uint32_t stage = 0, phase = 0, next = 0;  // ring: stage being read, stage of the next load
     int ahead = 0, loading = 0;               // entries looked at for loading; loads in flight
-    bool failed = false;
+    bool failed = false, stall = d.stall;
     auto load = [&]() {
         while (ahead < min(N, filled) && loading < C::STAGES) {
             const Entry& e = run[ahead % RUN];
             ++ahead;
             if (e.tok < 0) continue;
-            if (lane == 0) {
+            if (lane == 0 && !stall) {
                 uint8_t* st = ring + next * C::STAGE;
                 const int p0 = e.p0, p1 = sh == 4 ? e.p1 : -1;
                 const uint32_t rows = sh == 4 ? 16 * ((p0 >= 0) + (p1 >= 0)) : p0 >= 0 ? SUB : 0;
@@ -461,6 +462,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     }
                 }
             }
+            stall = false;
             ++loading;
             if (++next == C::STAGES) next = 0;
         }
@@ -611,8 +613,24 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             }
         }
 
-        if (!bspx::mbar_wait_bounded(full + stage, phase, failed ? 1u : d.spin_cap)) failed = true;
-        failed = __any_sync(FULL, failed);
+        failed = __any_sync(FULL, !bspx::mbar_wait_bounded(full + stage, phase, d.spin_cap));
+        if (failed) {
+            // nothing more is loaded, and no copy may land in the ring (which
+            // the CTA goes on to use) or after the CTA is gone; the rows of
+            // this segment and of the warp's later ones are not written
+            bool none = d.stall && k <= OVER;  // the first sub-tile's copies were skipped
+            for (; loading; --loading) {
+                if (!none) bspx::mbar_wait_bounded(full + stage, phase);
+                none = false;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            __syncwarp();
+            open = false;
+            break;
+        }
         const uint8_t* kt = ring + stage * C::STAGE;
         const uint8_t* vt = kt + C::HALF;
         const int p0 = e.p0, p1 = e.p1;
@@ -978,7 +996,7 @@ bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream
         if (st != BSP_OK) return st;
     }
     const DecodeArgs d = {a, h->parts, h->cuts, h->err, bsp_spin_cap(), prompts ? few : INT32_MAX,
-                          prompts ? h->ready : nullptr, beside};
+                          prompts ? h->ready : nullptr, beside, bsp_test_stall() != 0};
     if (a.c.dim <= 64)
         return few == 8 ? launch_decode<T, 64, 1>(h, d, s) : few == 16 ? launch_decode<T, 64, 2>(h, d, s)
                                                                        : launch_decode<T, 64, 3>(h, d, s);
