@@ -77,6 +77,7 @@ struct PromptArgs {
     int32_t splits;  // CTAs that share the cached rows of a row tile pair
     int64_t items;   // row tile pairs of one KV head
     float* parts;    // splits > 1: of CTA i and row r, O, m, l, mw at (i ROWS + r) (DP + 4)
+    bool stall;      // test only: the copies of the first tile are skipped
 };
 
 // The item a CTA (or its part) works on: request b, its first query row.
@@ -352,12 +353,13 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             }
             const bool mine = p >= 0 && (box == 16 || (lane & 1) == 0);
             const uint32_t bytes = __popc(__ballot_sync(FULL, mine)) * box * DP;
-            if (lane == 0) {
+            const bool skip = d.stall && n == 0;
+            if (lane == 0 && !skip) {
                 if (bytes) bspx::mbar_arrive_expect_tx(c_full + slot, bytes);
                 else bspx::mbar_arrive(c_full + slot);
             }
             __syncwarp();
-            if (mine)
+            if (mine && !skip)
                 tma_load_4d(smem + C::OFF_C + slot * C::CT + 16 * lane * DP, map, 0,
                             (t0 + j * TOK + 16 * lane) & ((1 << sh) - 1), h, p, c_full + slot);
             ++n;
@@ -399,8 +401,9 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             ks1 = ks2;
             vs1 = vs2;
         }
-        for (int i = std::max(0, n - NC); i < n; ++i)  // no copy may land after the CTA is gone
-            bspx::mbar_wait_bounded(c_full + i % NC, (i / NC) & 1, cap);
+        // no copy may land after the CTA is gone (the full cap, whatever `cap` is)
+        for (int i = std::max(d.stall ? 1 : 0, n - NC); i < n; ++i)
+            bspx::mbar_wait_bounded(c_full + i % NC, (i / NC) & 1);
         if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
         return;
     }
@@ -479,11 +482,14 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             }
         }
         // no product in flight (after a wait ran out) and nobody reading when
-        // the tensor memory is given back
+        // the tensor memory is given back: with the full cap, and for readers
+        // that may be in two waits of their own before they say so
         __syncwarp();
         commit(drain);
-        if (!wait(drain, 0, cap)) failed = true;
-        if (!wait(read, 0, cap)) failed = true;
+        if (!wait(drain, 0, bspx::kSpinCap)) failed = true;
+        bool done = false;
+        for (int i = 0; i < 4 && !done; ++i) done = wait(read, 0, bspx::kSpinCap);
+        if (!done) failed = true;
         if (failed && lane == 0) atomicExch(d.err, (int)BSP_ERR_TIMEOUT);
         tc_after();
         __syncwarp();
@@ -828,7 +834,7 @@ bsp_status_t bsp_run_kv_prompt(const bsp_kv* h, const bspkv::AttnArgs& a, bsp_dt
     const int64_t room = (int64_t)(h->part_floats / ((size_t)ROWS * (a.c.dim > 64 ? 132 : 68)));
     const int64_t ctas = std::min<int64_t>(h->num_sms, room) / std::max<int64_t>(1, items * a.c.heads);
     const PromptArgs d = {a, h->err, h->ready, bsp_spin_cap(), few, (int32_t)std::clamp<int64_t>(ctas, 1, MOST_SPLITS),
-                          items, h->parts};
+                          items, h->parts, bsp_test_stall() != 0};
     *beside = d.splits == 1;  // else the joining kernel is in between
     const bool wide = a.c.dim > 64;
     if (dtype == BSP_FP16) return wide ? launch<__half, 128>(h, d, s) : launch<__half, 64>(h, d, s);

@@ -43,3 +43,12 @@ def time_out(lens, heads, kvh, dim, page, dtype):
     ([(700, 3), (60, 20)], 4, 2, 256, 16)])
 def test_few_queries(lens, heads, kvh, dim, page, dtype):
     time_out(lens, heads, kvh, dim, page, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("lens,heads,kvh,dim,page", [
+    ([(0, 40), (0, 100)], 16, 4, 64, 16),                # one or two row tiles, one tile of codes
+    ([(0, 900)], 8, 2, 128, 64),                         # cached rows split, and joined
+    ([(300, 200), (64, 1), (0, 90)], 64, 8, 128, 32)])   # beside single tokens
+def test_prompts(lens, heads, kvh, dim, page, dtype):
+    time_out(lens, heads, kvh, dim, page, dtype)
