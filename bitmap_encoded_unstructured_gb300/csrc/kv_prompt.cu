@@ -253,14 +253,10 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     const int H = a.c.heads;
 
     wait_prior_grids();
-    // what comes next (the kernel of the other requests) may fill the SMs
-    // that this one leaves idle.  Its launch orders no memory: what the
-    // kernels before this one wrote it sees through `ready`, released here
-    // after they are known to be done
-    if (threadIdx.x == 0) {
-        if (blockIdx.x == 0) asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(d.ready) : "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    }
+    // for the kernel that may start beside this one (below): the kernels before
+    // this one are done
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(d.ready) : "memory");
 
     // the item: long rows first (later rows of a causal prompt see more),
     // the heads of one row tile pair side by side
@@ -329,6 +325,13 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     tc_after();
     const uint32_t tmem = *tmem_slot;
     bool failed = false;
+    // What comes next (the kernel of the other requests) may fill the SMs that
+    // this one leaves idle.  Its launch orders no memory: what was written
+    // before this kernel it sees through `ready`.  Not before the tensor memory
+    // is ours: the kernels behind start early in their turn, and a product
+    // kernel that took some of it here first, waiting for this grid to end,
+    // would never let this CTA have it.
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp < 4) fewer_registers<REG_CONTROL>();
     if (warp == 0) {

@@ -92,3 +92,49 @@ def test_attention_sees_the_append_before_it(heads, kvh, dtype):
     for _ in range(4):
         for (a, b), (c, d) in zip(want, go(False)):
             assert torch.equal(a, c) and torch.equal(b, d)
+
+
+def test_products_behind_prompts():
+    """The product kernel, which takes tensor memory before it waits for the
+    kernels ahead of it, close behind prompts of many and of few blocks."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(9)
+    page, kvh, heads, dim, pages = 32, 8, 32, 128, 300
+    cache = bsp.KvCache.empty(pages, kvh, dim, page)
+    cache.k.copy_(torch.randint(-127, 128, cache.k.shape, device="cuda", generator=g))
+    cache.v.copy_(torch.randint(-127, 128, cache.v.shape, device="cuda", generator=g))
+    cache.k_scale.fill_(0.01)
+    cache.v_scale.fill_(0.01)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    steps = []
+    for lens in ([(0, 500)] + [(70, 1)] * 12, [(1000, 130), (64, 1)], [(300, 90)] * 6):
+        n = [kv.pages_of(a + b, page) for a, b in lens]
+        table = torch.zeros((len(lens), max(n)), **i32)
+        for b in range(len(lens)):
+            table[b, :n[b]] = torch.randperm(pages, device="cuda", generator=g)[:n[b]]
+        new = [b for _, b in lens]
+        start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), **i32)
+        step = bsp.KvStep(table, torch.tensor([a + b for a, b in lens], **i32), start, max(new))
+        steps.append((step, torch.randn(sum(new), heads, dim, device="cuda", generator=g).half()))
+    w = torch.randn(1024, heads * dim, device="cuda", generator=g)
+    w = torch.where(w.abs() < 0.7, 0, w).half()
+    m = bsp.BitmapMatrix(w)
+    m.set_deterministic(True)
+
+    def go(wait):
+        got = []
+        for i in range(60):
+            y = cache.attention(*steps[i % 3])
+            if wait:
+                torch.cuda.synchronize()
+            got += [y, m.spmm(y[:8].reshape(8, -1))]
+            if wait:
+                torch.cuda.synchronize()
+        cache.check()
+        m.check()
+        return got
+
+    for a, b in zip(go(True), go(False)):
+        assert torch.equal(a, b)
+    m.close()
+    cache.close()
