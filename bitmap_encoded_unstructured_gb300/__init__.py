@@ -678,13 +678,13 @@ class KvStep:
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         s = cls.__new__(cls)
         i32 = dict(dtype=torch.int32, device=dev)
-        s.block_table = None
+        s.block_table = s._index = None  # until a plan
         s.seq_len, s.granted = torch.empty(batch, **i32), torch.empty(batch, **i32)
         s.q_start = torch.empty(batch + 1, **i32)
         s.slots = torch.empty(tokens, dtype=torch.int64, device=dev)
         s.positions = torch.empty(tokens, **i32)
         s.free_count = torch.empty(1, **i32) if free_count is None else free_count
-        _int32("free_count", s.free_count, 1, s.free_count.get_device())
+        _int32("free_count", s.free_count, 1, s.seq_len.get_device())
         s._out = tuple(t.data_ptr() for t in (s.seq_len, s.q_start, s.granted, s.slots, s.positions, s.free_count))
         return s
 
@@ -694,7 +694,7 @@ class KvStep:
         if t.dtype is not torch.int32 or not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
             raise ValueError("block_table must be an int32 CUDA tensor [batch][width], rows contiguous")
         batch, width = t.shape
-        self.device = t.device
+        self.device, self._index = t.device, t.get_device()
         self.block_table = t
         stride = t.stride(0) if batch > 1 else width
         self._c = bsp_kv_step_t(batch, width, stride, t.data_ptr(),
@@ -801,6 +801,9 @@ class KvCache:
             return self._current(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
+    def _refuse_step(self):
+        raise ValueError(f"the step is not planned, or not on {self.device}")
+
     def _refuse(self, name):
         raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, dim contiguous")
 
@@ -818,6 +821,8 @@ class KvCache:
         index = self._index
         if kd != 1 or vd != 1 or k.get_device() != index or v.get_device() != index:
             self._refuse("k and v")
+        if step._index != index:
+            self._refuse_step()
         st = self._append(self.h, step._ref, k.data_ptr(), v.data_ptr(), dt, shape[0], kr, kh, vr, vh, self._on(stream))
         if st:
             raise BspError("bsp_kv_append", st)
@@ -860,6 +865,8 @@ class KvCache:
         qr, qh, qd = q.stride()
         if qd != 1 or q.get_device() != self._index:
             self._refuse("q")
+        if step._index != self._index:
+            self._refuse_step()
         if out is None:
             out = self._empty(shape, dtype=q.dtype, device=self.device)
             orow, oh = heads * dim, dim
