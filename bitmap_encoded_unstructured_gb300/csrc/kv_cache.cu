@@ -442,9 +442,10 @@ bool meet(const void* p, int64_t n, const void* q, int64_t len, int64_t rows = 1
     return lo < b * stride + len || (b + 1 < rows && hi > (b + 1) * stride);
 }
 
+// A stride that is never used (one row, one head) may be anything.
 bool good_strides(int64_t row, int64_t head, int32_t dim, int64_t rows, int32_t heads)
 {
-    return (row % 8) == 0 && (head % 8) == 0 && (rows < 2 || row >= 0) && (heads < 2 || head >= dim);
+    return (rows < 2 || (row >= 0 && row % 8 == 0)) && (heads < 2 || (head >= dim && head % 8 == 0));
 }
 
 }  // namespace
@@ -481,9 +482,9 @@ bsp_status_t bsp_kv_create(const bsp_kv_desc_t* d, bsp_stream_t stream, bsp_kv_t
     if ((1 << shift) != d->page || d->pages < 1 || d->pages > INT32_MAX || d->heads < 1 || d->heads > 32767 ||
         d->dim < 16 || d->dim > 256 || d->dim % 16)
         return BSP_ERR_SHAPE;
-    if (d->row_stride < d->dim || d->row_stride % 16 || d->head_stride < 0 || d->head_stride % 16 ||
-        d->page_stride < 0 || d->page_stride % 16 || (d->heads > 1 && d->head_stride < d->dim) ||
-        (d->pages > 1 && (d->page_stride < d->dim || d->scale_stride < d->heads)))
+    if (d->row_stride < d->dim || d->row_stride % 16 ||
+        (d->heads > 1 && (d->head_stride < d->dim || d->head_stride % 16)) ||
+        (d->pages > 1 && (d->page_stride < d->dim || d->page_stride % 16 || d->scale_stride < d->heads)))
         return BSP_ERR_SHAPE;
     if (!aligned(d->k, 16) || !aligned(d->v, 16) || !aligned(d->k_scale, 4) || !aligned(d->v_scale, 4))
         return BSP_ERR_ALIGN;

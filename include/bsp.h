@@ -581,8 +581,8 @@ typedef struct {
     int32_t page;             /* rows of a page: 16, 32, 64, 128 or 256        */
     int32_t dim;              /* values of a row: a multiple of 16, 16 .. 256  */
     int64_t page_stride;      /* codes between pages, heads and rows of k (and */
-    int64_t head_stride;      /*   of v), multiples of 16; row_stride >= dim   */
-    int64_t row_stride;
+    int64_t head_stride;      /*   of v), multiples of 16; row_stride >= dim;  */
+    int64_t row_stride;       /*   any with one page, or one head              */
     int64_t scale_stride;     /* scales between pages (heads are contiguous)   */
 } bsp_kv_desc_t;
 
@@ -646,7 +646,8 @@ bsp_status_t bsp_kv_plan(bsp_kv_t h, const int32_t *ctx_len, const int32_t *new_
 /*
  * Store the step's new K and V rows, quantised, in their pages.
  *   k, v   device [rows][heads][dim], dtype BSP_FP16 or BSP_BF16, dim
- *          contiguous; strides in elements, multiples of 8; 16-B aligned.
+ *          contiguous; strides in elements, multiples of 8 (any with one
+ *          row, or one head); 16-B aligned.
  *          Rows from q_start[batch] on are ignored.
  * For each page and head that receives rows (K and V apart), with top the
  * largest finite |x| among them:
