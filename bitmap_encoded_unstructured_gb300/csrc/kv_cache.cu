@@ -448,6 +448,14 @@ bool good_strides(int64_t row, int64_t head, int32_t dim, int64_t rows, int32_t 
     return (rows < 2 || (row >= 0 && row % 8 == 0)) && (heads < 2 || (head >= dim && head % 8 == 0));
 }
 
+// Rows and heads of an output each have memory of their own.
+bool apart(int64_t row, int64_t head, int32_t dim, int64_t rows, int32_t heads)
+{
+    if (rows < 2) return true;
+    if (row < dim) return false;
+    return heads < 2 || row >= (heads - 1) * head + dim || head >= (rows - 1) * row + dim;
+}
+
 }  // namespace
 
 namespace bspkv {
@@ -655,7 +663,7 @@ bsp_status_t bsp_kv_attention(bsp_kv_t h, const bsp_kv_step_t* step, const void*
     if (!rows) return BSP_OK;
     if (!q || !out) return BSP_ERR_INVALID_ARG;
     if (!good_strides(q_row, q_head, h->view.dim, rows, heads) ||
-        !good_strides(o_row, o_head, h->view.dim, rows, heads))
+        !good_strides(o_row, o_head, h->view.dim, rows, heads) || !apart(o_row, o_head, h->view.dim, rows, heads))
         return BSP_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4))) return BSP_ERR_ALIGN;
     DeviceGuard g(h->device);

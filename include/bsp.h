@@ -679,7 +679,8 @@ bsp_status_t bsp_kv_read(bsp_kv_t h, const int64_t *slots, int64_t n, void *k, v
  *   q      device [rows][heads][dim], BSP_FP16 or BSP_BF16, dim contiguous,
  *          strides in elements, multiples of 8; 16-B aligned.
  *   heads  a multiple of the cache's heads.
- *   out    device [rows][heads][dim], q's dtype and rules.
+ *   out    device [rows][heads][dim], q's dtype and rules; its rows and heads
+ *          do not overlap (BSP_ERR_SHAPE), nor does it with q.
  *   lse    device fp32 [rows][heads] contiguous, log sum_j p_j, or NULL.
  * A row that sees nothing, and rows from q_start[batch] on, get out = 0 and
  * lse = -inf; a NaN in a query that sees something gives NaN.  Logits, maxima and sums are fp32; a probability (relative to
