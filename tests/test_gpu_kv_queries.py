@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+from oracle import kv_cache as kv
 from test_gpu_kv_attention import case, check, run
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,30 @@ def test_nan_queries_that_see_nothing(new):
     out, lse = run(c)
     assert (out[:new] == 0).all() and torch.isneginf(lse[:new]).all()
     assert torch.isfinite(out[new:]).all()
+
+
+@pytest.mark.parametrize("down", [8, 16, 18])
+@pytest.mark.parametrize("new", [1, 6, 300])
+def test_bfloat16_queries_of_wide_range(new, down):
+    """One value of each query is 2^down times the others and meets codes of 0,
+    so the logits are the small values' alone.  Scaled by their row's power of
+    two, bfloat16 values are exact in fp16 down to 2^-17 of it; below, each is
+    off by at most 2^-25 of it, so a logit by scale 2^-25 sum |k| more."""
+    import torch
+    heads, dim, page = 4, 64, 16
+    c = case([(200, new), (17, new)], heads, 2, dim, page, torch.bfloat16, 90 + down)
+    c["q"] *= 2.0 ** -down
+    c["q"][:, :, 5] = 1.0                                   # the row's power of two is 1 (or 2^-down |q|)
+    c["q"].clamp_(-1, 1)
+    c["k"][:, :, :, 5] = 0
+    scale = dim ** -0.5 * 2.0 ** down
+    out, lse = run(c, scale=scale)
+    q = c["q"].float().cpu().numpy()
+    ref, rl, weight, spread, seen = kv.attention(q, c["k"], c["v"], c["ks"], c["vs"], c["table"], c["seq"], c["start"],
+                                                 page, scale)
+    k = np.abs(c["k"].astype(np.float64)).sum(-1).max(2) * c["ks"]     # largest sum |k| of a page and head
+    d = dim * 2.0 ** -23 * spread[..., None] + 2.0 ** -20 + scale * 2.0 ** -25 * k.max()
+    vmax = 127 * c["vs"].max()
+    bound = 2.0 ** -8 * np.abs(ref) + (2 * d + 2.0 ** -11) * weight + seen[..., None] * 2.0 ** -24 * vmax + 1e-7
+    assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= d[..., 0] + 2.0 ** -20 * (1 + np.abs(rl))).all()
