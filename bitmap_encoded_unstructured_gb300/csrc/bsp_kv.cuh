@@ -160,6 +160,16 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// What p is multiplied by for its weight: 2^(m - mw) (lifted) times the V scale.
+// Rows that are not seen, or far below the maximum, have p = 0 and any scale:
+// the product stays finite for them, so that the weight is 0.  (A NaN stays one.)
+__device__ __forceinline__ float weight_of(float lift, float v_scale)
+{
+    float y;
+    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(y) : "f"(lift * v_scale));
+    return y;
+}
+
 __device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 
 // Two fp16 from bytes of w (already offset by 128) picked by sel.

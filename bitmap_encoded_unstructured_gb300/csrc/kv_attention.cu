@@ -750,7 +750,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     for (int y = 0; y < 4; ++y) {
                         p[y] = ex2(fmaf(sc[i][nt][y], kf[i][nt][y & 1], -m[nt][y & 1]));
                         l[nt][y & 1] += p[y];
-                        p[y] *= lift[nt][y & 1] * vscale[i];
+                        p[y] *= weight_of(lift[nt][y & 1], vscale[i]);
                     }
                     wf[i][nt][0] = movmatrix(h2bits(__floats2half2_rn(p[0], p[1])));
                     wf[i][nt][1] = movmatrix(h2bits(__floats2half2_rn(p[2], p[3])));

@@ -650,7 +650,7 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 uint32_t y[16];
 #pragma unroll
                 for (int g = 0; g < GROUPS; ++g) {
-                    const float v = mt[GROUPS + g] * lift;
+                    const float v = weight_of(lift, mt[GROUPS + g]);
                     const uint64_t kk = pair(kf[g], kf[g]), vv = pair(v, v);
 #pragma unroll
                     for (int i = 16 * g; i < 16 * g + 16; i += 2) {

@@ -74,3 +74,31 @@ def test_bfloat16_queries_of_wide_range(new, down):
     bound = 2.0 ** -8 * np.abs(ref) + (2 * d + 2.0 ** -11) * weight + seen[..., None] * 2.0 ** -24 * vmax + 1e-7
     assert (np.abs(out.double().cpu().numpy() - ref) <= bound).all()
     assert (np.abs(lse.double().cpu().numpy() - rl) <= d[..., 0] + 2.0 ** -20 * (1 + np.abs(rl))).all()
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("heads,kvh,dim", [(2, 2, 64), (8, 2, 128), (6, 2, 256)])
+@pytest.mark.parametrize("new", [1, 4, 40, 700])
+def test_v_scales_of_zero_beside_large_ones(heads, kvh, dim, new, dtype):
+    """Rows that have seen V scales of 0 only, where a page that they do not see
+    (or whose weights vanish) has a large one."""
+    import torch
+    page = 16
+    c = case([(3 * page - 1, new), (300, new)], heads, kvh, dim, page, getattr(torch, dtype), 60 + dim)
+    for b in range(2):
+        zero = c["table"][b][:kv.pages_of(int(c["seq"][b]), page) // 2 + 1]
+        c["vs"][:] = 8.0
+        c["vs"][zero[zero >= 0]] = 0
+        check(c, *run(c), what="unseen")
+        check(c, *run(c, window=20), window=20, what="window")
+    # weights that vanish: the second request's rows see logits thousands
+    # apart; its largest are where V is 0
+    d = dict(c, k=c["k"].copy(), ks=c["ks"].copy(), q=torch.ones_like(c["q"]))
+    d["vs"] = np.full_like(c["vs"], 100.0)
+    d["ks"][:] = 1.0
+    for j, p in enumerate(d["table"][1][:kv.pages_of(int(d["seq"][1]), page)]):
+        d["k"][p] = 100 if j % 3 == 0 else -100
+        d["vs"][p] = 0 if j % 3 == 0 else 100.0
+    out, lse = run(d, scale=1.0)
+    n = int(d["start"][1])
+    assert (out[n:] == 0).all() and torch.isfinite(lse[n:]).all()
