@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
         top = most(top);
     }
     const float now = fmaxf(old, __fdiv_rn(top, 127.f));
-    if (kept && now != old) {
+    if (kept && (now != old || now == 0.f)) {  // (a scale of 0 leaves no codes)
         const float ratio = now > 0.f ? __fdiv_rn(old, now) : 0.f;
         for (int i = tid; i < kept * (a.c.dim / 16); i += THREADS) {
             int4* at = reinterpret_cast<int4*>(codes + (i / (a.c.dim / 16)) * a.c.row_stride + (i % (a.c.dim / 16)) * 16);
