@@ -151,6 +151,7 @@ struct AttnArgs {
 // range whatever the V scales are.
 constexpr float NONE = -1e30f;           // running maximum before any row is seen
 constexpr float LAZY = 8.f;              // a maximum may lag by 2^8 before sums are rescaled
+constexpr float DEEP = 120.f;            // mw is not held further below m: 2^(m - mw) stays finite
 constexpr float LIFT = 64.f;             // weights are held 2^6 up, away from fp16's subnormals
 
 __device__ __forceinline__ float ex2(float x)

@@ -726,7 +726,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                             tw = fmaxf(tw, __shfl_xor_sync(FULL, tw, x));
                         }
                         t = fmaxf(t, m[nt][y]);
-                        tw = fmaxf(tw, mw[nt][y]);
+                        tw = fmaxf(fmaxf(tw, mw[nt][y]), t - DEEP);
                         l[nt][y] *= ex2(m[nt][y] - t);
                         const float back = ex2(mw[nt][y] - tw);
 #pragma unroll
@@ -736,7 +736,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                         }
                         m[nt][y] = t;
                         mw[nt][y] = tw;
-                        lift[nt][y] = ex2(fminf(t - tw, 120.f)) * LIFT;
+                        lift[nt][y] = ex2(t - tw) * LIFT;
                     }
             }
             // weights, as the B operand of the second product

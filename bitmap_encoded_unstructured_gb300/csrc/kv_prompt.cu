@@ -684,11 +684,12 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     top = fmaxf(top, big);
                     topw = fmaxf(topw, big + mt[2 * GROUPS + g]);
                 }
+                topw = fmaxf(topw, top - DEEP);
                 const float fade = ex2(m - top), back = ex2(mw - topw);
                 l *= fade;
                 m = top;
                 mw = topw;
-                lift = ex2(fminf(m - mw, 120.f)) * LIFT;
+                lift = ex2(m - mw) * LIFT;
                 if (j) {  // the product of the tile before is done: this S was asked for after it
                     for (int cb = 0; cb < DP; cb += 16) {
                         uint32_t o[16];

@@ -102,3 +102,23 @@ def test_v_scales_of_zero_beside_large_ones(heads, kvh, dim, new, dtype):
     out, lse = run(d, scale=1.0)
     n = int(d["start"][1])
     assert (out[n:] == 0).all() and torch.isfinite(lse[n:]).all()
+
+
+@pytest.mark.parametrize("power", [-110, -122, -126])
+@pytest.mark.parametrize("lens,heads,kvh,dim", [([(300, 1), (40, 1)], 8, 2, 64), ([(500, 5)], 4, 1, 128),
+                                                ([(70, 30)], 4, 2, 256), ([(0, 700), (64, 1)], 8, 2, 128)])
+def test_v_scales_near_the_smallest_number(lens, heads, kvh, dim, power):
+    """Outputs scale with V down to the smallest bfloat16 numbers: the same
+    calls with V scales of 1 and of 2^power, where a weight keeps at least 2^-9
+    of itself in fp16 (rows of equal logits) and an output is rounded to 2^-8."""
+    import torch
+    c = case(lens, heads, kvh, dim, 16, torch.bfloat16, 95)
+    c["ks"][:] = 0
+    c["v"] = np.abs(c["v"])
+    c["vs"][:] = 1
+    want, wl = run(c)
+    c["vs"][:] = 2.0 ** power
+    out, lse = run(c)
+    assert torch.equal(lse, wl)
+    off = (out.double() * 2.0 ** -power - want.double()).abs()
+    assert (off <= 2.0 ** -7 * want.double()).all()
