@@ -712,7 +712,9 @@ class KvCache:
     ``plan`` grants pages and lays out a step from request lengths, ``append``
     stores its new rows, ``attention`` attends over them and what was cached
     before, ``read`` returns rows by slot.  All are asynchronous on the
-    stream and can be captured in a CUDA graph."""
+    stream and can be captured in a CUDA graph.  The calls on one cache go to
+    one stream, or are ordered by events: attention keeps its parts in scratch
+    of the cache's (16 to 41 MB by ``dim``)."""
 
     def __init__(self, k, v, k_scale, v_scale, stream=None):
         import torch
@@ -775,9 +777,10 @@ class KvCache:
         rows cached, ``new_len`` rows asked for (negative: the request has
         ended and gives its pages back).  Granted pages come off ``free_list``
         (``free_count`` entries live) into ``block_table``, first come, first
-        served; ``tokens`` is the row capacity of the step.  The step also
-        carries ``granted``, ``slots``, ``positions`` and the new
-        ``free_count``."""
+        served; ``tokens`` is the row capacity of the step.  ``max_new`` bounds
+        a request's new rows: with it (1 for single tokens) attention does not
+        launch the prompt kernel in vain.  The step also carries ``granted``,
+        ``slots``, ``positions`` and the new ``free_count``."""
         step = KvStep.empty(block_table.shape[0], tokens, block_table.device) if out is None else out
         if step.block_table is not block_table:
             step._bind(block_table, max_new)

@@ -40,8 +40,13 @@ using namespace bspkv;
 // product may be permuted freely as long as both sides agree.
 constexpr int DEC_WARPS = 4;
 constexpr int SUB = 32;                  // rows of a sub-tile
-constexpr int OVER = 2;                  // sub-tiles a segment's start and end are worth
-constexpr int LEAST = 3;                 // a warp's run is at least this long (more than OVER)
+// OVER: sub-tiles a segment's start and end are worth.  LEAST: a warp's run is
+// at least this long (more than OVER).  Cold, 64 ragged streams of 64 over 8
+// heads | 256 streams of 100 .. 900 rows | one of 517: 2 and 3 take 135 | 78 |
+// 20.5 us, 0 and 1 141 | 82 | 18.4, 3 and 4 131 | 78 | 20.5, 4 and 5 137 | 80 |
+// 22.5, 2 and 10 131 | 78 | 26.6.
+constexpr int OVER = 2;
+constexpr int LEAST = 3;
 constexpr int RUN = 32, FILL = 16;       // entries of the run that a warp looks ahead, and fills at a time later
 
 template <int DP, int NT>
@@ -572,7 +577,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                     for (int y = 0; y < 16; ++y) top = fmaxf(top, fabsf(x[j][y]));
                 }
                 // bfloat16 rows are brought into fp16's range by a power of
-                // two (exact but for values 2^-24 below the row's largest)
+                // two: exact down to 2^-17 of it, below that off by at most
+                // 2^-25 of it
                 float unit = 1.f;
                 if constexpr (!std::is_same<T, __half>::value) {
                     top = fmaxf(top, __shfl_xor_sync(FULL, top, 1));
@@ -982,9 +988,22 @@ bsp_status_t run(const bsp_kv* h, const AttnArgs& a, int64_t max_new, cudaStream
 {
     // Query blocks of 8, 16 or 24 rows: the smallest that holds the largest
     // request.  Requests with more rows are the prompt kernel's, whose row
-    // tiles have 128 rows and whose dims end at 128; a step that has some is
-    // taken for one of prompts and single tokens, and the block for a single
-    // token's rows.  Steps of few rows in all stay here, in several blocks.
+    // tiles have 128 rows and whose dims end at 128.
+    //
+    // Steps of few rows in all stay here, in several blocks, each of which
+    // reads the codes again.  One request, 64 over 8 heads of 128, here |
+    // prompt kernel, cold: 16 rows (1024 rows x heads) 20.5 | 44 us with nothing
+    // cached, 27 | 44 with 500, 39 | 48 with 4000, 184 | 87 with 60000; 64 rows
+    // 25 | 38, 31 | 40, 64 | 46, 582 | 159.  The host does not know the lengths
+    // in the device's arrays: 1024 costs short requests of up to 4096 at most
+    // 24 us, and long ones of up to 1024 twice their time.
+    //
+    // A step with prompts is taken for one of prompts and single tokens, and
+    // the block for a single token's rows.  A chunk of 513 beside 16 single
+    // tokens in groups of 8: 48 us with blocks of 8, 58 with 24; beside 64 single
+    // heads' tokens 497 and 685.  Drafts of more rows then go to the prompt
+    // kernel: 16 of 5 tokens in groups of 4 56 and 62 us, but 3 of them over
+    // 60k .. 120k rows 1293 and 177.
     const int64_t most = max_new * a.group;
     const bool prompts = most > 24 && a.c.dim <= 128 && a.s.batch > 0 && a.s.rows * a.heads > 1024;
     const int64_t block = prompts ? std::min<int64_t>(a.group, 24) : most;

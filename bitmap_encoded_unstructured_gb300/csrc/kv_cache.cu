@@ -246,10 +246,12 @@ __device__ __forceinline__ uint2 codes_of(const uint4& raw, float scale, float i
 // WARPS warps (1 or 4) per unit: a page that receives rows, a head, K or V.
 // Two passes over the unit's rows, its largest value and its codes; the first
 // CACHED vectors of a thread stay in registers between them.  1 << lane_shift
-// threads share a row, one 16-byte vector each.  2 bytes in and 1 out a value,
-// bound by issue slots (66%: the codes' products, tie checks and permutes):
-// 15879 bfloat16 rows of 8 heads of 128 take 28.5 us, 3.4 TB/s; single rows
-// are bound by the latency of request search, scale, rows and codes (4 us).
+// threads share a row, one 16-byte vector each.  2 bytes in and 1 out a value:
+// 15879 bfloat16 rows of 8 heads of 128 take 28.5 us, 3.4 TB/s, 0.50 of the copy
+// rate.  Bound by instructions: the largest stall is the wait for them (the
+// codes' products, tie checks and divisions stand at each of nine stores), and
+// 66% of the issue slots are taken.  Single rows are bound by the latency of
+// request search, scale, rows and codes (4 us).
 template <class T, int WARPS>
 __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendArgs a, const int lane_shift)
 {

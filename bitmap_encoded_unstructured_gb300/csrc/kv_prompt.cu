@@ -24,9 +24,10 @@
 // its own S), O0, O1.  Products of one thread run in order, so the next S
 // may be asked for right after the product that reads W.
 //
-// Bound by issue slots and each row tile's chain S -> P -> W -> S: a prompt of
-// 8101 rows, 64 heads over 8 KV heads of 128, takes 846 us (1075 TFLOP at 1271
-// TFLOP/s, 0.65 of the library's bf16 product).  Two threads a row (16
+// Bound by each row tile's chain S -> P -> W -> S (issue slots are 55% busy, the
+// tensor pipe 56%): a prompt of 8101 rows, 64 heads over 8 KV heads of 128,
+// takes 845 us (1.075 TFLOP at 1273 TFLOP/s, 0.65 of the library's bf16
+// product).  Two threads a row (16
 // softmax warps of 96 registers) were slower, 1070 us: a barrier a tile joins
 // the halves, and half the registers spill.
 #include "bsp_kv.cuh"
@@ -551,7 +552,8 @@ kv_prompt_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         const int64_t q_tok = rq.r0 + r / a.group;
         const int head = h * a.group + (int)(r % a.group);
         // the warp's 32 query rows to shared memory, DP / 8 lanes to a row;
-        // bfloat16 rows are brought into fp16's range by a power of two
+        // bfloat16 rows are brought into fp16's range by a power of two (exact
+        // down to 2^-17 of it, below that off by at most 2^-25 of it)
         float unit = 1.f;
         {
             constexpr int LANES = DP / 8, STEP = 32 / LANES;

@@ -554,19 +554,21 @@ bsp_status_t bsp_union_check(bsp_union_t h, bsp_stream_t stream);
  * The caller owns the cache (from its own allocator) and describes it once:
  *   k, v               int8 codes [pages][heads][page][dim], dim contiguous
  *   k_scale, v_scale   fp32 [pages][heads], one for each page and KV head
- * and a cached value is code * scale (scales are not negative).  A request's rows fill the pages its
- * block table row names, `page` rows to a page, in order.
+ * and a cached value is code * scale (scales are finite and not negative).  A
+ * request's rows fill the pages its block table row names, `page` rows to a
+ * page, in order.
  *
  * A step brings new rows of several requests ("ragged"): request b has
  * new rows q_start[b] .. q_start[b + 1] - 1 and, with them, seq_len[b] rows
  * in all; the i-th of its n new rows has position seq_len[b] - n + i.  All
  * of it is device memory, so that a step can be captured in a graph and
- * replayed on other lengths.  A call takes at most 2^30 rows.  Page numbers outside 0 .. pages - 1 (-1 by
- * convention) mean "no page": append drops rows that fall there, attention
- * does not see them.
+ * replayed on other lengths.  A call takes at most 2^30 rows.  Page numbers
+ * outside 0 .. pages - 1 (-1 by convention) mean "no page": append drops rows
+ * that fall there, attention does not see them.
  *
  * Calls are asynchronous on `stream`, allocate nothing and synchronise
- * nothing.  Calls on one handle must be serialised on one stream.
+ * nothing.  Calls on one handle must be serialised on one stream: its scratch
+ * holds the parts of one attention call.
  * ------------------------------------------------------------------------ */
 typedef struct bsp_kv *bsp_kv_t;
 
@@ -599,7 +601,8 @@ typedef struct {
 /*
  * A handle over a caller-owned cache.  Copies the description (the arrays
  * must outlive the handle) and allocates the scratch of its calls on the
- * current device; synchronises `stream`.  BSP_ERR_SHAPE for sizes or strides
+ * current device, about 16 MB for dim up to 64, 31 MB up to 128, 41 MB above;
+ * synchronises `stream`.  BSP_ERR_SHAPE for sizes or strides
  * outside the ranges above, BSP_ERR_ALIGN for codes not 16-B aligned.
  */
 bsp_status_t bsp_kv_create(const bsp_kv_desc_t *desc, bsp_stream_t stream, bsp_kv_t *out);
@@ -616,7 +619,10 @@ bsp_status_t bsp_kv_check(bsp_kv_t h, bsp_stream_t stream);
  *             negative: the request has ended and gives its pages back.
  *   block_table [batch][width] the first ceil(ctx_len / page) entries name
  *             the request's pages; entries of granted pages are written,
- *             others are left as they are.
+ *             others are left as they are.  They go back to the free list as
+ *             they stand: a request that ends has no -1 among them, and a
+ *             caller that lowers ctx_len (rejected drafts) returns the pages
+ *             beyond the new ceil(ctx_len / page) itself.
  *   free_list [free_capacity] a stack of page numbers, of which *free_count
  *             (device) are live.  Pages given back go on top of it in order
  *             of request and page, first; then granted pages come off the
@@ -683,8 +689,11 @@ bsp_status_t bsp_kv_read(bsp_kv_t h, const int64_t *slots, int64_t n, void *k, v
  *          do not overlap (BSP_ERR_SHAPE), nor does it with q.
  *   lse    device fp32 [rows][heads] contiguous, log sum_j p_j, or NULL.
  * A row that sees nothing, and rows from q_start[batch] on, get out = 0 and
- * lse = -inf; a NaN in a query that sees something gives NaN.  Logits, maxima and sums are fp32; a probability (relative to
- * the largest seen) times its V scale is rounded to fp16 for the product.
+ * lse = -inf; a NaN in a query that sees something gives NaN.  Logits, maxima
+ * and sums are fp32; a probability (relative to the largest seen) times its V
+ * scale is rounded to fp16 for the product.  A bfloat16 query is taken in
+ * fp16 times the power of two of its row's largest value: exact down to
+ * 2^-17 of that power, off by at most 2^-25 of it below.
  */
 bsp_status_t bsp_kv_attention(bsp_kv_t h, const bsp_kv_step_t *step, const void *q, bsp_dtype_t dtype,
                               int64_t rows, int32_t heads, int64_t q_row_stride, int64_t q_head_stride,
