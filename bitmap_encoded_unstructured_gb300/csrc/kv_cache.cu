@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
         top = most(top);
     }
     const float now = fmaxf(old, __fdiv_rn(top, 127.f));
-    if (kept && (now != old || now == 0.f)) {  // (a scale of 0 leaves no codes)
+    if (kept && now != old) {
         const float ratio = now > 0.f ? __fdiv_rn(old, now) : 0.f;
         for (int i = tid; i < kept * (a.c.dim / 16); i += THREADS) {
             int4* at = reinterpret_cast<int4*>(codes + (i / (a.c.dim / 16)) * a.c.row_stride + (i % (a.c.dim / 16)) * 16);
@@ -334,6 +334,10 @@ __global__ void __launch_bounds__(APPEND_THREADS) kv_append_kernel(const AppendA
             *at = w;
         }
     }
+    if (kept && now == 0.f)  // no codes under a scale of 0 (apart: in the loop above it costs 7 registers)
+        for (int i = tid; i < kept * (a.c.dim / 16); i += THREADS)
+            *reinterpret_cast<int4*>(codes + (i / (a.c.dim / 16)) * a.c.row_stride + (i % (a.c.dim / 16)) * 16) =
+                make_int4(0, 0, 0, 0);
     // no reciprocal of a scale below 2^-126: NaN makes every code a quotient
     const float inv = now < 1.2e-38f ? __int_as_float(0x7FC00000) : __fdiv_rn(1.f, now);
     auto store = [&](int row, const uint4& v) {
