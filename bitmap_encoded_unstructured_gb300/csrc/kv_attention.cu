@@ -377,7 +377,7 @@ __device__ __forceinline__ bool is_ready(const int* ready)
 // Bound by memory at 8 queries: 64 ragged streams of 8 KV heads, 391 MB of
 // codes, take 72 us (5.4 TB/s; 6.1 TB/s while warps work, the rest is the
 // start and uneven ends).  At 24 queries by the latency of two warps a
-// scheduler (250 registers hold the sums): 595 MB in 140 us, 4.2 TB/s.
+// scheduler (253 registers hold the sums): 595 MB in 142 us, 4.2 TB/s.
 template <class T, int DP, int NT>
 __global__ void __launch_bounds__(DEC_WARPS * 32, DecCfg<DP, NT>::CTAS)
 kv_decode_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const DecodeArgs d)
