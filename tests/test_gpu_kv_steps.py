@@ -138,3 +138,53 @@ def test_products_behind_prompts():
         assert torch.equal(a, b)
     m.close()
     cache.close()
+
+
+@pytest.mark.parametrize("heads,kvh", [(32, 8), (8, 2)])
+def test_graph_of_a_mixed_step(heads, kvh):
+    """Prompt and decode kernel side by side (or behind a joining kernel),
+    captured once and replayed on other rows, lengths and pages."""
+    import torch
+    page, dim, pages, width = 32, 64, 400, 24
+    g = torch.Generator(device="cuda").manual_seed(12)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 150, 151, 152, 160, 161], **i32)
+    rows = 170                                              # 9 rows to spare
+    table, seq = torch.zeros((5, width), **i32), torch.zeros(5, **i32)
+    q, k, v = (torch.zeros((rows, h, dim), dtype=torch.bfloat16, device="cuda") for h in (heads, kvh, kvh))
+    cache, plain = (bsp.KvCache.empty(pages, kvh, dim, page) for _ in range(2))
+    step = bsp.KvStep(table, seq, start, 150)
+    out = torch.empty_like(q)
+
+    def go(c):
+        c.append(step, k, v)
+        return c.attention(step, q, out=out)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        seq.copy_(start[1:] - start[:-1])
+        table.copy_(torch.arange(5 * width, **i32).view(5, width))
+        go(cache)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        go(cache)
+    for i in range(12):
+        table.copy_(torch.randperm(pages, device="cuda", generator=g)[:5 * width].view(5, width))
+        n = start[1:] - start[:-1]
+        seq.copy_(n + torch.randint(0, width * page - 150, (5,), device="cuda", generator=g).int())
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+        for a, b in zip((plain.k, plain.v, plain.k_scale, plain.v_scale), (cache.k, cache.v, cache.k_scale, cache.v_scale)):
+            a.copy_(b)
+        graph.replay()
+        got = out.clone()
+        out.fill_(7)
+        torch.cuda.synchronize()
+        go(plain)
+        assert torch.equal(got, out)
+        assert torch.equal(cache.k, plain.k) and torch.equal(cache.v_scale, plain.v_scale)
+    cache.check()
+    cache.close()
+    plain.close()
