@@ -8,8 +8,9 @@ memory and streams.
 Two layers:
 
 * ``bsp_*`` functions with the C names, taking raw pointers / ints;
-* ``BitmapMatrix``, ``UnionMatrix`` (weights) and ``KvCache`` (the paged
-  8-bit KV cache and its attention), handle owners with tensor-level methods.
+* ``BitmapMatrix``, ``UnionMatrix``, ``Int4Matrix`` (weights), ``KvCache``
+  (the paged 8-bit KV cache and its attention) and ``Rotary`` (rotary
+  positions), handle owners with tensor-level methods.
 
 The library is loaded on first use; if it is missing or fails to load, the
 call raises ``RuntimeError`` (there is no fallback of any kind).
@@ -88,6 +89,19 @@ SIGNATURES = {
     "bsp_kv_read": (C.c_int, [_P, _P, _I64, _P, _P, C.c_int, _P]),
     "bsp_kv_attention": (C.c_int, [_P, _P, _P, C.c_int, _I64, C.c_int32, _I64, _I64, C.c_float, C.c_int32, _P, _I64,
                                    _I64, _P, _P]),
+    "bsp_q4_encode": (C.c_int, [_P, C.c_int, _I64, _I64, C.c_int32, C.c_int, _P, C.POINTER(_P)]),
+    "bsp_q4_import": (C.c_int, [_P, _P, _P, C.c_int, _I64, _I64, C.c_int32, _P, C.POINTER(_P)]),
+    "bsp_q4_export": (C.c_int, [_P, _P, _P, _P, _P]),
+    "bsp_q4_decode": (C.c_int, [_P, _P, _P]),
+    "bsp_q4_info": (C.c_int, [_P, _P]),
+    "bsp_q4_storage_bytes": (C.c_int, [_P, C.POINTER(C.c_uint64)]),
+    "bsp_q4_check": (C.c_int, [_P, _P]),
+    "bsp_q4_destroy": (C.c_int, [_P]),
+    "bsp_q4_mm": (C.c_int, [_P, _P, _I64, _I64, _P, _I64, _P]),
+    "bsp_q4_gated": (C.c_int, [_P, _P, _P, _I64, _I64, C.c_int, _P, _I64, _P]),
+    "bsp_rope_create": (C.c_int, [_P, _P, C.POINTER(_P)]),
+    "bsp_rope_destroy": (C.c_int, [_P]),
+    "bsp_rope_apply": (C.c_int, [_P, _P, _P, C.c_int, _I64, _P, _I64, C.c_int, _P]),
 }
 
 # Entry points of the test build only (include/bsp_testing.h).
@@ -127,6 +141,21 @@ class bsp_kv_step_t(C.Structure):
     _fields_ = [("batch", C.c_int32), ("width", C.c_int32), ("table_stride", C.c_int64),
                 ("block_table", C.c_void_p), ("seq_len", C.c_void_p), ("q_start", C.c_void_p),
                 ("max_new", C.c_int64)]
+
+
+class bsp_q4_info_t(C.Structure):
+    _fields_ = [("M", C.c_int64), ("K", C.c_int64), ("dtype", C.c_int32), ("group", C.c_int32), ("zeros", C.c_int32),
+                ("device", C.c_int32), ("groups", C.c_int64)]
+
+
+class bsp_rope_desc_t(C.Structure):
+    _fields_ = [("dim", C.c_int32), ("rot", C.c_int32), ("axes", C.c_int32), ("interleaved", C.c_int32),
+                ("freq", C.c_void_p), ("axis", C.c_void_p), ("scale", C.c_float)]
+
+
+class bsp_rope_rows_t(C.Structure):
+    _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("heads", C.c_int32), ("in_row", C.c_int64),
+                ("in_head", C.c_int64), ("out_row", C.c_int64), ("out_head", C.c_int64)]
 
 
 class BspError(RuntimeError):
@@ -888,3 +917,290 @@ class KvCache:
         if st:
             raise BspError("bsp_kv_attention", st)
         return (out, lse) if with_lse else out
+
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}  # bsp_act_t
+
+
+class Int4Matrix:
+    """A weight W (M x K) held as 4-bit codes with a scale for each ``group``
+    (32, 64 or 128) columns of a row, and zero points if wanted:
+    W = scale * (code - zero), zero = 8 without zero points.
+
+    ``Int4Matrix(W)`` quantises a float16 or bfloat16 CUDA tensor to the
+    nearest; ``from_arrays`` takes codes quantised elsewhere.  The type of the
+    scales is that of activations and outputs.  ``mm(X)`` takes X [N][K] (any
+    N, rows may be strided) and returns Y [N][M]; ``gated`` computes
+    act(W X) * (W_up X) in one kernel.  A matrix is immutable: calls on it may
+    run at the same time, on any streams of its device."""
+
+    def __init__(self, W, group: int = 128, zeros: bool = False, stream=None):
+        import torch
+        if not W.is_cuda or W.dim() != 2:
+            raise ValueError("W must be a 2-D CUDA tensor")
+        dt = _row_dtype(W.dtype)
+        W = W.contiguous()
+        h = C.c_void_p()
+        with torch.cuda.device(W.device):
+            _check("bsp_q4_encode", lib().bsp_q4_encode(W.data_ptr(), dt, W.shape[0], W.shape[1], int(group),
+                                                        int(bool(zeros)), _stream(stream), C.byref(h)))
+        self._own(h.value, W.device, W.dtype)
+
+    @classmethod
+    def from_arrays(cls, codes, scales, zeros=None, group: int = 128, device=None, stream=None):
+        """From uint8 ``codes`` [M][K / 2] (column 2 i in the low half of byte
+        i), ``scales`` [M][ceil(K / group)] (float16 or bfloat16) and
+        optionally uint8 ``zeros`` of the same shape (0 to 15): tensors on the
+        GPU or the CPU, copied.  ``device``: where the matrix lives (the codes' GPU, or the current one)."""
+        import torch
+        if codes.dtype is not torch.uint8 or codes.dim() != 2:
+            raise TypeError("codes must be a uint8 tensor [M][K / 2]")
+        dt = _row_dtype(scales.dtype)
+        M, K = codes.shape[0], 2 * codes.shape[1]
+        shape = (M, -(-K // int(group)) if group > 0 else 0)
+        if scales.shape != shape or (zeros is not None and (zeros.shape != shape or zeros.dtype is not torch.uint8)):
+            raise ValueError("scales (and uint8 zeros) must be [M][ceil(K / group)]")
+        if device is None:
+            device = codes.device if codes.is_cuda else torch.device("cuda", torch.cuda.current_device())
+        device = torch.device(device)
+        if any(t is not None and t.is_cuda and t.device != device for t in (codes, scales, zeros)):
+            raise ValueError(f"codes, scales and zeros must be on {device} or the CPU")
+        kept = [None if t is None else t.contiguous() for t in (codes, scales, zeros)]
+        at = [None if t is None else t.data_ptr() for t in kept]
+        h = C.c_void_p()
+        with torch.cuda.device(device):
+            _check("bsp_q4_import", lib().bsp_q4_import(*at, dt, M, K, int(group), _stream(stream), C.byref(h)))
+        obj = cls.__new__(cls)
+        obj._own(h.value, device, scales.dtype)
+        return obj
+
+    def _own(self, h, device, dtype):
+        import torch
+        self.h, self.device, self.torch_dtype = h, torch.device(device), dtype
+        info = self.info()
+        self.M, self.K, self.group, self.has_zeros = info["M"], info["K"], info["group"], bool(info["zeros"])
+        self._index = info["device"]
+        L = lib()
+        self._mm, self._gated = L.bsp_q4_mm, L.bsp_q4_gated
+        self._empty, self._current = torch.empty, torch._C._cuda_getCurrentRawStream
+
+    def close(self):
+        if getattr(self, "h", None):
+            _check("bsp_q4_destroy", lib().bsp_q4_destroy(self.h))
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def info(self) -> dict:
+        o = bsp_q4_info_t()
+        _check("bsp_q4_info", lib().bsp_q4_info(self.h, C.byref(o)))
+        return {f: getattr(o, f) for f, _ in bsp_q4_info_t._fields_}
+
+    def storage_bytes(self) -> int:
+        v = C.c_uint64()
+        _check("bsp_q4_storage_bytes", lib().bsp_q4_storage_bytes(self.h, C.byref(v)))
+        return v.value
+
+    def arrays(self, stream=None):
+        """Copies of (codes, scales, zeros) in ``from_arrays``' form; zeros is
+        None without zero points."""
+        import torch
+        groups = -(-self.K // self.group)
+        codes = torch.empty((self.M, self.K // 2), dtype=torch.uint8, device=self.device)
+        scales = torch.empty((self.M, groups), dtype=self.torch_dtype, device=self.device)
+        zeros = torch.empty((self.M, groups), dtype=torch.uint8, device=self.device) if self.has_zeros else None
+        _check("bsp_q4_export", lib().bsp_q4_export(self.h, codes.data_ptr(), scales.data_ptr(),
+                                                    zeros.data_ptr() if self.has_zeros else None, self._on(stream)))
+        return codes, scales, zeros
+
+    def decode(self, out=None, stream=None):
+        """W as a dense tensor [M][K]: scale * (code - zero), rounded once."""
+        W = self._empty((self.M, self.K), dtype=self.torch_dtype, device=self.device) if out is None else out
+        if W.dtype is not self.torch_dtype or W.shape != (self.M, self.K) or not W.is_contiguous() \
+                or W.get_device() != self._index:
+            raise ValueError("out must be a contiguous tensor [M][K] of the scales' type beside the matrix")
+        _check("bsp_q4_decode", lib().bsp_q4_decode(self.h, W.data_ptr(), self._on(stream)))
+        return W
+
+    def check(self, stream=None):
+        """Synchronise and raise if a kernel on this matrix gave up a wait."""
+        _check("bsp_q4_check", lib().bsp_q4_check(self.h, self._on(stream)))
+
+    def _on(self, stream):
+        if stream is None:
+            return self._current(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def _rows(self, X, out):
+        """N, the rows' strides and the output of a product with X."""
+        shape = X.shape
+        if len(shape) != 2 or shape[1] != self.K or X.dtype is not self.torch_dtype or X.get_device() != self._index:
+            raise ValueError(f"X must be {self.torch_dtype} [N][{self.K}] on {self.device}")
+        N = shape[0]
+        xs, one = X.stride()
+        if one != 1:
+            raise ValueError("X must have contiguous rows")
+        if out is None:
+            return N, xs, self._empty((N, self.M), dtype=self.torch_dtype, device=self.device), self.M
+        ys, one = out.stride()
+        if (out.dtype is not self.torch_dtype or out.shape != (N, self.M) or (one != 1 and self.M > 1)
+                or out.get_device() != self._index):
+            raise ValueError("out must be [N][M] of X's type beside the matrix, rows contiguous")
+        return N, xs, out, ys
+
+    def mm(self, X, out=None, stream=None):
+        """Y = W X: X [N][K], Y [N][M]."""
+        N, xs, Y, ys = self._rows(X, out)
+        st = self._mm(self.h, X.data_ptr(), xs, N, Y.data_ptr(), ys, self._on(stream))
+        if st:
+            raise BspError("bsp_q4_mm", st)
+        return Y
+
+    def gated(self, up, X, activation: str = "silu", out=None, stream=None):
+        """Y = act(W X) * (W_up X), the first half of a gated feed-forward
+        block whose gate is this matrix; ``activation`` a key of
+        ``ACTIVATIONS``."""
+        N, xs, Y, ys = self._rows(X, out)
+        try:
+            act = ACTIVATIONS[activation]
+        except KeyError:
+            raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}") from None
+        st = self._gated(self.h, up.h, X.data_ptr(), xs, N, act, Y.data_ptr(), ys, self._on(stream))
+        if st:
+            raise BspError("bsp_q4_gated", st)
+        return Y
+
+
+class Rotary:
+    """Rotary positions for heads of ``dim`` values, of which the first
+    ``rot`` (all by default) turn, in pairs (i, i + rot / 2) or, if
+    ``interleaved``, (2 i, 2 i + 1).  Pair i turns by positions[axis[i]] *
+    freqs[i] radians; cosines and sines are multiplied by ``scale``.
+
+    ``freqs`` defaults to base ** (-2 i / rot).  ``sections`` gives each axis
+    (time, height, width) its number of pairs, in runs, or in turns if
+    ``cyclic`` (an axis whose pairs are used up drops out of the turns); ``axis`` names each
+    pair's axis instead.  ``own_freqs``: the frequencies start over on each axis."""
+
+    def __init__(self, dim: int, rot: int = None, base: float = 10000.0, sections=None, cyclic: bool = False,
+                 own_freqs: bool = False, interleaved: bool = False, freqs=None, axis=None, scale: float = 1.0,
+                 device=None, stream=None):
+        import torch
+        rot = dim if rot is None else rot
+        half = rot // 2
+        if axis is not None and sections is not None:
+            raise ValueError("axis or sections, not both")
+        if sections is not None:
+            axis = self._axes_of(list(sections), cyclic)
+        axis = [0] * half if axis is None else [int(a) for a in axis]
+        if len(axis) != half or any(not 0 <= a < 8 for a in axis):
+            raise ValueError(f"every one of the {half} pairs needs an axis, 0 to 7")
+        if freqs is None:
+            if own_freqs:
+                seen, count = [0] * 8, [axis.count(a) for a in range(8)]
+                freqs = []
+                for a in axis:
+                    freqs.append(float(base) ** (-seen[a] / count[a]))
+                    seen[a] += 1
+            else:
+                freqs = [float(base) ** (-i / half) for i in range(half)]
+        else:
+            freqs = [float(f) for f in freqs]
+        if len(freqs) != half:
+            raise ValueError(f"{half} pairs need as many frequencies")
+        self.dim, self.rot, self.axes, self.interleaved = int(dim), int(rot), max(axis, default=0) + 1, bool(interleaved)
+        if sections is not None:
+            self.axes = len(list(sections))
+        self.freqs, self.axis, self.scale = freqs, axis, float(scale)
+        f, a = (C.c_double * max(1, half))(*freqs), (C.c_uint8 * max(1, half))(*axis)
+        d = bsp_rope_desc_t(self.dim, self.rot, self.axes, int(self.interleaved), C.addressof(f), C.addressof(a),
+                            self.scale)
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        h = C.c_void_p()
+        with torch.cuda.device(dev):
+            self._index = torch.cuda.current_device()
+            _check("bsp_rope_create", lib().bsp_rope_create(C.addressof(d), _stream(stream), C.byref(h)))
+        self.h, self.device = h.value, torch.device("cuda", self._index)
+        self._apply, self._current = lib().bsp_rope_apply, torch._C._cuda_getCurrentRawStream
+        self._empty, self._int32 = torch.empty, torch.int32
+
+    @staticmethod
+    def _axes_of(sections, cyclic):
+        if not cyclic:
+            return [a for a, n in enumerate(sections) for _ in range(n)]
+        left, got = list(sections), []
+        while any(n > 0 for n in left):
+            for a in range(len(left)):
+                if left[a] > 0:
+                    got.append(a)
+                    left[a] -= 1
+        return got
+
+    def close(self):
+        if getattr(self, "h", None):
+            _check("bsp_rope_destroy", lib().bsp_rope_destroy(self.h))
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _of(self, name, x, out, rows, dtype):
+        """(the C description of x and its output, the output)"""
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != rows or shape[2] != self.dim or x.dtype is not dtype \
+                or x.get_device() != self._index:
+            raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, q and k of one type")
+        xr, xh, xd = x.stride()
+        if out is None:
+            out = self._empty(shape, dtype=dtype, device=self.device)
+            orow, oh, od = shape[1] * self.dim, self.dim, 1
+        else:
+            if out.shape != shape or out.dtype is not dtype or out.get_device() != self._index:
+                raise ValueError(f"the output of {name} must have its shape and type, beside it")
+            orow, oh, od = out.stride()
+        if xd != 1 or od != 1:
+            raise ValueError(f"{name} and its output must have contiguous values")
+        return bsp_rope_rows_t(x.data_ptr(), out.data_ptr(), shape[1], xr, xh, orow, oh), out
+
+    def apply(self, q, k, positions, out=None, inverse: bool = False, stream=None):
+        """Turn rows ``q`` [rows][heads][dim] and ``k`` [rows][kv heads][dim]
+        (``k`` may be None; views of a QKV output allowed) by int32
+        ``positions``: [rows] with one axis, else [axes][rows].  ``out``: (q
+        out, k out); ``out=(q, k)`` works in place, None allocates.  A row with a
+        negative position on any axis (``KvStep.positions`` behind the last
+        row) is not written.  ``inverse`` turns back.  Returns (q out, k out),
+        or q out alone without k."""
+        dtype, rows = q.dtype, q.shape[0]
+        dt = _row_dtype(dtype)
+        if positions.dtype is not self._int32 or positions.get_device() != self._index:
+            raise ValueError(f"positions must be int32 on {self.device}")
+        if positions.dim() == 1 and self.axes == 1:
+            ok, stride = positions.shape[0] == rows, positions.stride(0) if rows > 1 else 1
+            apart = rows
+        else:
+            ok = positions.shape == (self.axes, rows)
+            apart, stride = positions.stride() if ok else (0, 0)
+            stride = stride if rows > 1 else 1
+        if not ok or stride != 1:
+            raise ValueError(f"positions must be [axes][rows] = [{self.axes}][{rows}], rows contiguous")
+        out_q, out_k = (None, None) if out is None else out
+        cq, out_q = self._of("q", q, out_q, rows, dtype)
+        if k is not None:
+            ck, out_k = self._of("k", k, out_k, rows, dtype)
+        st = self._apply(self.h, C.addressof(cq), C.addressof(ck) if k is not None else None, dt, rows,
+                         positions.data_ptr(), apart, int(inverse), self._on(stream))
+        if st:
+            raise BspError("bsp_rope_apply", st)
+        return out_q if k is None else (out_q, out_k)
+
+    def _on(self, stream):
+        if stream is None:
+            return self._current(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream

@@ -1,0 +1,107 @@
+// Internal declarations of the 4-bit weights (q4_weights.cu, q4_narrow.cu,
+// q4_wide.cu): the handle, its layout and the products' arguments.
+#pragma once
+
+#include "bsp_internal.cuh"
+#include "bsp_ptx.cuh"
+
+#include <cuda_bf16.h>
+
+#define BSP_Q4_MAGIC 0xB5B14B17u
+
+// Layout.  W is padded to 128-row strips and 128-column blocks and cut into
+// tiles of 16 rows x 64 columns, stored row tile by row tile, in order of
+// the columns: 512 bytes, 16 for each lane of a warp.  Lane (g, t) = (lane /
+// 4, lane % 4) holds rows g and g + 8 of the tile, columns 32 h + 8 t .. + 7
+// for h = 0, 1; its 32-bit word 2 h + j has columns k = 32 h + 8 t + 4 j and
+// the three after it, one code a nibble:
+//   nibble  0     1      2      3        4      5       6      7
+//           g,k   g+8,k  g,k+2  g+8,k+2  g,k+1  g+8,k+1 g,k+3  g+8,k+3
+// so that a mask leaves two neighbouring columns of one row in the two
+// halves of a register: the A operand of mma.m16n8k16 with its columns
+// renumbered (as the B operand's are), and eight columns of a row in 16
+// bytes for a shared-memory tile.
+//   scales  [row tile][group][g] pairs (row g, row g + 8) of the dtype
+//   zeros   [row tile][group][g] bytes, row g in the low half, g + 8 above
+// with group = columns / G.  Rows past M have scales of 0.
+struct Q4View {
+    const uint4* codes;
+    const uint32_t* scales;
+    const uint8_t* zeros;  // null: 8 throughout
+};
+
+struct bsp_q4 {
+    uint32_t magic;
+    int device, num_sms;
+    bsp_dtype_t dtype;  // of the scales, and of X and Y: BSP_FP16 or BSP_BF16
+    int64_t M, K;
+    int32_t group;      // 32, 64 or 128
+    int64_t row_tiles, k_tiles;  // padded: multiples of 8 and of 2
+    uint4* codes;
+    uint32_t* scales;
+    uint8_t* zeros;
+    int* err;  // as bsp_handle::err
+    int64_t groups() const { return k_tiles * 64 / group; }  // of the padded grid
+};
+
+namespace bspq4 {
+
+inline bool valid(const bsp_q4* h) { return h != nullptr && h->magic == BSP_Q4_MAGIC; }
+
+// Everything a product reads and writes.  Two weights: the gated form.
+struct Problem {
+    Q4View w, up;
+    bool gated;
+    int act;  // bsp_act_t
+    bsp_dtype_t dtype;
+    int64_t M, K, row_tiles, k_tiles;
+    int32_t group;
+    const void* x;
+    int64_t x_stride, N;
+    void* y;
+    int64_t y_stride;
+    int device, num_sms;
+    int* err;
+};
+
+template <class T>
+__device__ __forceinline__ float to_float(T x);
+template <>
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <>
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <class T>
+__device__ __forceinline__ T from_float(float x);
+template <>
+__device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+
+// The low (lo) or high half of a pair of the dtype as fp32.
+template <class T>
+__device__ __forceinline__ float half_of(uint32_t pair, int high)
+{
+    const uint16_t bits = (uint16_t)(high ? pair >> 16 : pair);
+    return to_float(*reinterpret_cast<const T*>(&bits));
+}
+
+__device__ __forceinline__ float activate(float g, int act)
+{
+    switch (act) {
+    case BSP_ACT_SILU: return g / (1.f + __expf(-g));
+    case BSP_ACT_GELU: return 0.5f * g * erfcf(-0.70710678118654752f * g);
+    // 0.5 (1 + tanh(y)) = 1 / (1 + exp(-2 y))
+    case BSP_ACT_GELU_TANH: return g / (1.f + __expf(-1.59576912160573071f * (g + 0.044715f * g * g * g)));
+    default: return g != g ? g : fmaxf(g, 0.f);  // relu; a NaN stays one
+    }
+}
+
+__device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+}  // namespace bspq4
+
+// N <= NARROW columns (q4_narrow.cu), and any N (q4_wide.cu).
+bsp_status_t bsp_run_q4_narrow(const bspq4::Problem& p, cudaStream_t s);
+bsp_status_t bsp_run_q4_wide(const bspq4::Problem& p, cudaStream_t s);

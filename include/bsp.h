@@ -700,6 +700,167 @@ bsp_status_t bsp_kv_attention(bsp_kv_t h, const bsp_kv_step_t *step, const void 
                               float scale, int32_t window, void *out, int64_t out_row_stride,
                               int64_t out_head_stride, float *lse, bsp_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * 4-bit weights with group scales (weights that are quantised but not
+ * pruned), their products, and the gated feed-forward form over two of them.
+ *
+ *   W[m][k] = scale[m][k / group] * (code[m][k] - zero[m][k / group])
+ *
+ * codes and zero points in 0 .. 15; without zero points they are 8
+ * throughout.  A handle owns its arrays (laid out for the kernels) and is
+ * immutable; nothing is shared between calls, so calls on one handle may run
+ * at the same time, on any streams of its device.
+ * ------------------------------------------------------------------------ */
+typedef struct bsp_q4 *bsp_q4_t;
+
+typedef enum {
+    BSP_ACT_SILU = 0,     /* g / (1 + exp(-g))                              */
+    BSP_ACT_GELU = 1,     /* g (1 + erf(g / sqrt 2)) / 2                    */
+    BSP_ACT_GELU_TANH = 2,/* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+    BSP_ACT_RELU = 3      /* max(g, 0)                                      */
+} bsp_act_t;
+
+typedef struct {
+    int64_t M, K;
+    int32_t dtype;        /* bsp_dtype_t of the scales, X and Y             */
+    int32_t group;        /* columns of a group                             */
+    int32_t zeros;        /* 1: the handle has zero points                  */
+    int32_t device;
+    int64_t groups;       /* ceil(K / group)                                */
+} bsp_q4_info_t;
+
+/*
+ * Quantise a dense weight, on the device, to the nearest.
+ *   W      device, row-major [M][K], BSP_FP16 or BSP_BF16; 16-byte aligned.
+ *   M, K   M >= 1, K a multiple of 8 (the last group may be short); at most
+ *          2^31 - 1 each and 2^24 blocks of 128 x 128.
+ *   group  32, 64 or 128.
+ *   zeros  0: scale = max |w| / 7 of the group, code = round(w / scale)
+ *             within -8 .. 7, plus 8;
+ *          1: lo = min(w, 0), hi = max(w, 0) of the group, scale =
+ *             hi / 15 - lo / 15, zero = round(-lo / scale) within 0 .. 15, code
+ *             = round(w / scale) + zero within 0 .. 15.
+ * In fp32, to nearest even, the scale rounded to the dtype before it
+ * divides; NaN and infinities count as 0 for the scale; NaN becomes 0, and
+ * everything does under a scale of 0.  Synchronises `stream`; W may be freed
+ * on return.
+ */
+bsp_status_t bsp_q4_encode(const void *W, bsp_dtype_t dtype, int64_t M, int64_t K, int32_t group, int zeros,
+                           bsp_stream_t stream, bsp_q4_t *out);
+
+/*
+ * A handle from codes quantised elsewhere (copied; device or host memory,
+ * any that cudaMemcpyAsync with cudaMemcpyDefault accepts):
+ *   codes  u8 [M][K / 2], column 2 i in the low half of byte i;
+ *   scales [M][ceil(K / group)] of the dtype (BSP_FP16 or BSP_BF16);
+ *   zeros  u8 [M][ceil(K / group)], 0 .. 15 (BSP_ERR_INVALID_ARG otherwise),
+ *          or NULL.
+ * Sizes as for bsp_q4_encode.  Synchronises `stream`.
+ */
+bsp_status_t bsp_q4_import(const uint8_t *codes, const void *scales, const uint8_t *zeros, bsp_dtype_t dtype,
+                           int64_t M, int64_t K, int32_t group, bsp_stream_t stream, bsp_q4_t *out);
+
+/* Copies of the arrays in bsp_q4_import's form into device memory (any may
+ * be NULL; zeros of a handle without them are written as 8), ordered on
+ * `stream`.  codes 4-byte, scales 2-byte aligned. */
+bsp_status_t bsp_q4_export(bsp_q4_t h, uint8_t *codes, void *scales, uint8_t *zeros, bsp_stream_t stream);
+
+/* W back as dense device [M][K] of the dtype, 16-B aligned: scale * (code -
+ * zero) in fp32, rounded once. */
+bsp_status_t bsp_q4_decode(bsp_q4_t h, void *W_out, bsp_stream_t stream);
+
+/* Shape and form of a handle. */
+bsp_status_t bsp_q4_info(bsp_q4_t h, bsp_q4_info_t *out);
+
+/* ceil(M K / 2) + 2 M groups (+ ceil(M groups / 2) with zero points): what
+ * the weight takes without the padding of the handle's layout. */
+bsp_status_t bsp_q4_storage_bytes(bsp_q4_t h, uint64_t *bytes);
+
+/* Synchronise stream and report (then clear) a device-side wait that gave up. */
+bsp_status_t bsp_q4_check(bsp_q4_t h, bsp_stream_t stream);
+
+/* Free a handle (synchronises the device first). */
+bsp_status_t bsp_q4_destroy(bsp_q4_t h);
+
+/*
+ * Y = W * X in the layout of bsp_spmm: X device [N][K], Y device [N][M], of
+ * the handle's dtype, contiguous rows x_stride and y_stride elements apart
+ * (any with N < 2; x_stride >= K a multiple of 8, y_stride >= M), both 16-B
+ * aligned.  N = 0 does nothing.  X and Y share no memory
+ * (BSP_ERR_INVALID_ARG; two slices of one tensor's rows do not).  Sums are
+ * fp32 and the scales are applied to the sums of whole groups: weights are
+ * not rounded, and Y is rounded once.  The same call gives the same bits.
+ * Asynchronous, allocates nothing.
+ */
+bsp_status_t bsp_q4_mm(bsp_q4_t h, const void *X, int64_t x_stride, int64_t N, void *Y, int64_t y_stride,
+                       bsp_stream_t stream);
+
+/*
+ * Y = act(W_gate X) * (W_up X), the first half of a gated feed-forward
+ * block, in one kernel: both products, the activation and their product in
+ * fp32, rounded once.  The weights have the same M, K, group, dtype and
+ * device (BSP_ERR_SHAPE, BSP_ERR_DTYPE, BSP_ERR_INVALID_ARG); either may
+ * have zero points, and they may be the same handle.  The rest as for
+ * bsp_q4_mm; a wait that gives up is reported by the gate's handle.
+ */
+bsp_status_t bsp_q4_gated(bsp_q4_t gate, bsp_q4_t up, const void *X, int64_t x_stride, int64_t N, bsp_act_t act,
+                          void *Y, int64_t y_stride, bsp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions, on one or several axes: query and key rows turned by
+ * their positions between the QKV projection and the cache.  Pair i of a
+ * head's first `rot` values becomes
+ *   a' = s (a cos p - b sin p),  b' = s (b cos p + a sin p),
+ *   p = positions[axis[i]][row] * freq[i]
+ * and the values from `rot` on are kept.
+ * ------------------------------------------------------------------------ */
+typedef struct bsp_rope *bsp_rope_t;
+
+typedef struct {
+    int32_t dim;          /* values of a head: a multiple of 8, 8 .. 1024   */
+    int32_t rot;          /* values that turn: a multiple of 8, 8 .. dim    */
+    int32_t axes;         /* 1 .. 8                                         */
+    int32_t interleaved;  /* pairs (2 i, 2 i + 1), else (i, i + rot / 2)    */
+    const double *freq;   /* host [rot / 2], radians a position, within +-65536 */
+    const uint8_t *axis;  /* host [rot / 2], 0 .. axes - 1, or NULL: all 0  */
+    float scale;          /* s, finite                                      */
+} bsp_rope_desc_t;
+
+/* A handle over a copy of the description, on the current device.
+ * Synchronises `stream`.  BSP_ERR_SHAPE for sizes outside the ranges,
+ * BSP_ERR_INVALID_ARG for frequencies, axes or a scale outside theirs. */
+bsp_status_t bsp_rope_create(const bsp_rope_desc_t *desc, bsp_stream_t stream, bsp_rope_t *out);
+
+/* Free a handle (synchronises the device first). */
+bsp_status_t bsp_rope_destroy(bsp_rope_t h);
+
+typedef struct {
+    const void *in;       /* device [rows][heads][dim], dim contiguous, 16-B aligned */
+    void *out;            /* the same shape, aligned; may be `in` with in's strides  */
+    int32_t heads;        /* 0: there is none (in and out are not looked at)         */
+    int64_t in_row, in_head, out_row, out_head; /* strides in elements, multiples of 8
+                             (any with one row, or one head); an output's rows and heads
+                             do not overlap                                          */
+} bsp_rope_rows_t;
+
+/*
+ * Turn the rows of q and k (either may have no heads, or be NULL) in one launch.
+ *   positions device int32 [axes][rows], axis_stride entries apart (any with
+ *          one axis).  A row with a negative position on any axis is not there:
+ *          its output is left as it was (bsp_kv_plan's positions are -1 behind
+ *          the step's last row).
+ *   inverse  1: by -p instead (the rotation undone, but for s twice; also its
+ *          gradient).
+ * fp32 arithmetic, rounded once; the angle is reduced exactly, whatever the
+ * position.  An output is its own input, element for element, or shares no
+ * memory with either input or the other output (BSP_ERR_INVALID_ARG; slices
+ * of the same rows do not).
+ * Asynchronous, allocates nothing; calls on one handle may run at the same time.
+ */
+bsp_status_t bsp_rope_apply(bsp_rope_t h, const bsp_rope_rows_t *q, const bsp_rope_rows_t *k, bsp_dtype_t dtype,
+                            int64_t rows, const int32_t *positions, int64_t axis_stride, int inverse,
+                            bsp_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
