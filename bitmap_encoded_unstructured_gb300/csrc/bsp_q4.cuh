@@ -1,5 +1,5 @@
 // Internal declarations of the 4-bit weights (q4_weights.cu, q4_narrow.cu,
-// q4_wide.cu): the handle, its layout and the products' arguments.
+// q4_wide.cuh): the handle, its layout and the products' arguments.
 #pragma once
 
 #include "bsp_internal.cuh"
@@ -86,6 +86,53 @@ __device__ __forceinline__ float half_of(uint32_t pair, int high)
     return to_float(*reinterpret_cast<const T*>(&bits));
 }
 
+// Pairs of the dtype from a word of codes: c - z of rows g (a[0], a[2]), and UPPER
+// times that of rows g + 8; z0 and z1 are the pairs that bias() makes.
+template <class T>
+struct Codes;
+template <>
+struct Codes<__half> {
+    static constexpr float UPPER = 16.f;
+    static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b)
+    {
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    }
+    static __device__ __forceinline__ void bias(uint32_t zeros, uint32_t& z0, uint32_t& z1)
+    {
+        z0 = (zeros & 15u) * 0x10001u | 0x64006400u;
+        z1 = (zeros & 240u) * 0x10001u | 0x64006400u;
+    }
+    static __device__ __forceinline__ void widen(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4])
+    {
+        const uint32_t v = w >> 8;
+        a[0] = less((w & 0x000F000Fu) | 0x64006400u, z0);
+        a[1] = less((w & 0x00F000F0u) | 0x64006400u, z1);
+        a[2] = less((v & 0x000F000Fu) | 0x64006400u, z0);
+        a[3] = less((v & 0x00F000F0u) | 0x64006400u, z1);
+    }
+};
+template <>
+struct Codes<__nv_bfloat16> {
+    static constexpr float UPPER = 1.f;
+    static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b)
+    {
+        const __nv_bfloat162 d =
+            __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    }
+    static __device__ __forceinline__ void bias(uint32_t zeros, uint32_t& z0, uint32_t& z1)
+    {
+        z0 = (zeros & 15u) * 0x10001u | 0x43004300u;
+        z1 = (zeros >> 4) * 0x10001u | 0x43004300u;
+    }
+    static __device__ __forceinline__ void widen(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4])
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = less(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, i & 1 ? z1 : z0);
+    }
+};
+
 __device__ __forceinline__ float activate(float g, int act)
 {
     switch (act) {
@@ -102,6 +149,8 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 
 }  // namespace bspq4
 
-// N <= NARROW columns (q4_narrow.cu), and any N (q4_wide.cu).
+// Few rows of X (q4_narrow.cu), and more (q4_wide.cuh, by type).
+constexpr int64_t BSP_Q4_NARROW_N = 16;
 bsp_status_t bsp_run_q4_narrow(const bspq4::Problem& p, cudaStream_t s);
-bsp_status_t bsp_run_q4_wide(const bspq4::Problem& p, cudaStream_t s);
+bsp_status_t bsp_run_q4_wide_f16(const bspq4::Problem& p, cudaStream_t s);
+bsp_status_t bsp_run_q4_wide_bf16(const bspq4::Problem& p, cudaStream_t s);

@@ -101,53 +101,6 @@ __device__ __forceinline__ void mma<__nv_bfloat16>(float (&c)[4], const uint32_t
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The A operand from a word of codes: c - z of rows g (a[0], a[2]), and UPPER
-// times that of rows g + 8; z0 and z1 are the pairs that bias() makes.
-template <class T>
-struct Codes;
-template <>
-struct Codes<__half> {
-    static constexpr float UPPER = 16.f;
-    static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b)
-    {
-        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&d);
-    }
-    static __device__ __forceinline__ void bias(uint32_t zeros, uint32_t& z0, uint32_t& z1)
-    {
-        z0 = (zeros & 15u) * 0x10001u | 0x64006400u;
-        z1 = (zeros & 240u) * 0x10001u | 0x64006400u;
-    }
-    static __device__ __forceinline__ void widen(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4])
-    {
-        const uint32_t v = w >> 8;
-        a[0] = less((w & 0x000F000Fu) | 0x64006400u, z0);
-        a[1] = less((w & 0x00F000F0u) | 0x64006400u, z1);
-        a[2] = less((v & 0x000F000Fu) | 0x64006400u, z0);
-        a[3] = less((v & 0x00F000F0u) | 0x64006400u, z1);
-    }
-};
-template <>
-struct Codes<__nv_bfloat16> {
-    static constexpr float UPPER = 1.f;
-    static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b)
-    {
-        const __nv_bfloat162 d =
-            __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&d);
-    }
-    static __device__ __forceinline__ void bias(uint32_t zeros, uint32_t& z0, uint32_t& z1)
-    {
-        z0 = (zeros & 15u) * 0x10001u | 0x43004300u;
-        z1 = (zeros >> 4) * 0x10001u | 0x43004300u;
-    }
-    static __device__ __forceinline__ void widen(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4])
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = less(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, i & 1 ? z1 : z0);
-    }
-};
-
 template <class T, int G, int NT, int RT, bool GATED>
 __global__ void __launch_bounds__(THREADS, 2) q4_narrow_kernel(const NarrowArgs a)
 {
