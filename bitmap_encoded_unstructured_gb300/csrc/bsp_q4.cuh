@@ -9,21 +9,22 @@
 
 #define BSP_Q4_MAGIC 0xB5B14B17u
 
-// Layout.  W is padded to 128-row strips and 128-column blocks and cut into
-// tiles of 16 rows x 64 columns, stored row tile by row tile, in order of
-// the columns: 512 bytes, 16 for each lane of a warp.  Lane (g, t) = (lane /
-// 4, lane % 4) holds rows g and g + 8 of the tile, columns 32 h + 8 t .. + 7
-// for h = 0, 1; its 32-bit word 2 h + j has columns k = 32 h + 8 t + 4 j and
-// the three after it, one code a nibble:
+// Layout.  W is padded to strips of 128 rows and blocks of 128 columns and cut
+// into tiles of 16 rows x 64 columns of 512 bytes, 16 for each lane of a
+// warp: [strip][columns / 64][row tile of the strip][lane].  Lane (g, t) =
+// (lane / 4, lane % 4) holds rows g and g + 8 of the tile, columns 32 h + 8 t
+// .. + 7 for h = 0, 1; its 32-bit word 2 h + j has columns k = 32 h + 8 t + 4 j
+// and the three after it, one code a nibble:
 //   nibble  0     1      2      3        4      5       6      7
 //           g,k   g+8,k  g,k+2  g+8,k+2  g,k+1  g+8,k+1 g,k+3  g+8,k+3
 // so that a mask leaves two neighbouring columns of one row in the two
 // halves of a register: the A operand of mma.m16n8k16 with its columns
 // renumbered (as the B operand's are), and eight columns of a row in 16
 // bytes for a shared-memory tile.
-//   scales  [row tile][group][g] pairs (row g, row g + 8) of the dtype
-//   zeros   [row tile][group][g] bytes, row g in the low half, g + 8 above
-// with group = columns / G.  Rows past M have scales of 0.
+//   scales  [strip][group][row tile][g] pairs (row g, row g + 8) of the dtype
+//   zeros   [strip][group][row tile][g] bytes, row g in the low half, g + 8 above
+// with group = columns / G.  A strip's block of 128 columns is one piece of
+// memory in each of the three.  Rows past M have scales of 0.
 struct Q4View {
     const uint4* codes;
     const uint32_t* scales;
@@ -36,7 +37,7 @@ struct bsp_q4 {
     bsp_dtype_t dtype;  // of the scales, and of X and Y: BSP_FP16 or BSP_BF16
     int64_t M, K;
     int32_t group;      // 32, 64 or 128
-    int64_t row_tiles, k_tiles;  // padded: multiples of 8 and of 2
+    int64_t strips, k_tiles;  // of the padded grid; k_tiles is even
     uint4* codes;
     uint32_t* scales;
     uint8_t* zeros;
@@ -54,7 +55,7 @@ struct Problem {
     bool gated;
     int act;  // bsp_act_t
     bsp_dtype_t dtype;
-    int64_t M, K, row_tiles, k_tiles;
+    int64_t M, K, strips, k_tiles;
     int32_t group;
     const void* x;
     int64_t x_stride, N;

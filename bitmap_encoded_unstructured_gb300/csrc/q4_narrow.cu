@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(THREADS, 2) q4_narrow_kernel(const NarrowArgs 
     uint32_t C, crank;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(C));
     crank = bspx::cluster_ctarank();
-    const int64_t tile0 = (int64_t)(blockIdx.x / C) * TILES;
+    const int64_t tile0 = (int64_t)(blockIdx.x / C) * TILES, strip = tile0 / 8;
+    const int rt0 = (int)(tile0 % 8);  // TILES divides 8: one strip
     const int n0 = blockIdx.y * COLS, n_here = min(COLS, a.N - n0);
     const uint32_t ring = bspx::smem_u32(smem) + warp * D * L::BYTES;
 
@@ -129,16 +130,17 @@ __global__ void __launch_bounds__(THREADS, 2) q4_narrow_kernel(const NarrowArgs 
     const uint8_t *meta = nullptr, *zero = nullptr;  // what this lane copies of the scales and zero points
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-        codes[r] = of(r).codes + ((tile0 + r % TILES) * a.k_tiles + k_begin) * 32 + lane;
+        codes[r] = of(r).codes + (strip * a.k_tiles + k_begin) * 256 + (rt0 + r % TILES) * 32 + lane;
+    const int64_t group0 = strip * a.groups + (int64_t)k_begin * 64 / G;
     constexpr int CHUNKS = PER * 2;  // 16-byte pieces of a row tile's scales in a stage
     if (lane < RT * CHUNKS) {
-        const int r = lane / CHUNKS;
-        meta = reinterpret_cast<const uint8_t*>(of(r).scales + (tile0 + r % TILES) * a.groups * 8) +
-               (int64_t)k_begin * 64 / G * 32 + lane % CHUNKS * 16;
+        const int r = lane / CHUNKS, c = lane % CHUNKS;
+        meta = reinterpret_cast<const uint8_t*>(of(r).scales + (group0 + c / 2) * 64 + (rt0 + r % TILES) * 8) + c % 2 * 16;
     }
-    if (lane < RT) {
-        const uint8_t* z = of(lane).zeros;
-        if (z) zero = z + ((tile0 + lane % TILES) * a.groups + (int64_t)k_begin * 64 / G) * 8;
+    if (lane < RT * PER) {
+        const int r = lane / PER;
+        const uint8_t* z = of(r).zeros;
+        if (z) zero = z + (group0 + lane % PER) * 64 + (rt0 + r % TILES) * 8;
     }
     const bool has_zeros[2] = {a.w[0].zeros != nullptr, GATED && a.w[1].zeros != nullptr};
     const char* xrow[NT];
@@ -152,14 +154,11 @@ __global__ void __launch_bounds__(THREADS, 2) q4_narrow_kernel(const NarrowArgs 
     auto copy_weights = [&](int i) {  // stage i of this warp
         const uint32_t slot = ring + (uint32_t)(i % D) * L::BYTES;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) cp16(slot + r * 512 + lane * 16, codes[r] + (int64_t)i * 32, 16);
+        for (int r = 0; r < RT; ++r) cp16(slot + r * 512 + lane * 16, codes[r] + (int64_t)i * 256, 16);
         if (G < 128 || !(i & 1)) {
-            const int at = G == 128 ? i >> 1 : i;
-            if (lane < RT * CHUNKS) cp16(slot + L::S + lane / CHUNKS * 64 + lane % CHUNKS * 16, meta + (int64_t)at * PER * 32, 16);
-            if (lane < RT && zero) {
-                if (PER == 2) cp16(slot + L::Z + lane * 16, zero + (int64_t)at * 16, 16);
-                else cp8(slot + L::Z + lane * 16, zero + (int64_t)at * 8);
-            }
+            const int64_t at = (int64_t)(G == 128 ? i >> 1 : i) * PER * 64;
+            if (lane < RT * CHUNKS) cp16(slot + L::S + lane / CHUNKS * 64 + lane % CHUNKS * 16, meta + at * 4, 16);
+            if (lane < RT * PER && zero) cp8(slot + L::Z + lane / PER * 16 + lane % PER * 8, zero + at);
         }
     };
     auto copy_x = [&](int i) {

@@ -96,13 +96,28 @@ __device__ __forceinline__ uint32_t eight(const uint8_t* codes, int64_t M, int64
 
 __device__ __forceinline__ uint32_t nibble(uint32_t w, int i) { return (w >> (4 * i)) & 15u; }
 
+// The first row and column of lane i of the layout.
+struct Place {
+    int64_t m, k;
+};
+__device__ __forceinline__ Place place_of(int64_t i, int64_t k_tiles)
+{
+    const int lane = (int)(i & 31), rt = (int)(i >> 5 & 7);
+    const int64_t tile = i >> 8;  // strip, columns / 64
+    return {tile / k_tiles * 128 + rt * 16 + (lane >> 2), tile % k_tiles * 64 + 8 * (lane & 3)};
+}
+// The first row of pair i of the scales, and its group.
+__device__ __forceinline__ Place pair_of(int64_t i, int64_t groups)
+{
+    return {(i >> 6) / groups * 128 + (i >> 3 & 7) * 16 + (i & 7), (i >> 6) % groups};
+}
+
 // A thread a lane of a tile.
 __global__ void q4_pack_kernel(const uint8_t* codes, int64_t M, int64_t K, int64_t k_tiles, int64_t n, uint4* out)
 {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
-    const int lane = (int)(i & 31), g = lane >> 2, t = lane & 3;
-    const int64_t tile = i >> 5, m = tile / k_tiles * 16 + g, k = tile % k_tiles * 64 + 8 * t;
+    const int64_t m = place_of(i, k_tiles).m, k = place_of(i, k_tiles).k;
     uint32_t w[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -133,8 +148,7 @@ __global__ void q4_unpack_kernel(const uint4* in, int64_t M, int64_t K, int64_t 
 {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
-    const int lane = (int)(i & 31), g = lane >> 2, t = lane & 3;
-    const int64_t tile = i >> 5, m = tile / k_tiles * 16 + g, k = tile % k_tiles * 64 + 8 * t;
+    const int64_t m = place_of(i, k_tiles).m, k = place_of(i, k_tiles).k;
     const uint4 w = in[i];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -146,13 +160,13 @@ __global__ void q4_unpack_kernel(const uint4* in, int64_t M, int64_t K, int64_t 
 }
 
 // Scales and zero points between the plain form [M][plain_groups] and the
-// layout [row tile][groups][8] of pairs (row g, row g + 8); a thread a pair.
+// layout [strip][groups][row tile][8] of pairs (row g, row g + 8); a thread a pair.
 __global__ void q4_pack_scales_kernel(const uint16_t* scales, const uint8_t* zeros, int64_t M, int64_t plain_groups,
                                       int64_t groups, int64_t n, uint32_t* out, uint8_t* zeros_out, int* bad)
 {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
-    const int64_t gr = i / 8 % groups, m = i / 8 / groups * 16 + i % 8;
+    const int64_t m = pair_of(i, groups).m, gr = pair_of(i, groups).k;
     uint32_t s = 0, z = 0;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -172,7 +186,7 @@ __global__ void q4_unpack_scales_kernel(const uint32_t* in, const uint8_t* zeros
 {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
-    const int64_t gr = i / 8 % groups, m = i / 8 / groups * 16 + i % 8;
+    const int64_t m = pair_of(i, groups).m, gr = pair_of(i, groups).k;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         if (m + 8 * u >= M || gr >= plain_groups) continue;
@@ -187,13 +201,12 @@ __global__ void q4_decode_kernel(Q4View v, int64_t M, int64_t K, int32_t G, int6
 {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
-    const int lane = (int)(i & 31), g = lane >> 2, t = lane & 3;
-    const int64_t tile = i >> 5, row_tile = tile / k_tiles, m = row_tile * 16 + g, k = tile % k_tiles * 64 + 8 * t;
+    const int64_t m = place_of(i, k_tiles).m, k = place_of(i, k_tiles).k;
     const uint4 w = v.codes[i];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (k + 32 * h >= K) continue;
-        const int64_t at = (row_tile * (k_tiles * 64 / G) + (k + 32 * h) / G) * 8 + g;
+        const int64_t at = (m / 128 * (k_tiles * 64 / G) + (k + 32 * h) / G) * 64 + m % 128 / 16 * 8 + m % 8;
         const uint32_t pair = v.scales[at], zero = v.zeros ? v.zeros[at] : 0x88u;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -257,9 +270,9 @@ bsp_status_t build(bsp_dtype_t dtype, int64_t M, int64_t K, int32_t group, const
     h->M = M;
     h->K = K;
     h->group = group;
-    h->row_tiles = (M + 127) / 128 * 8;
+    h->strips = (M + 127) / 128;
     h->k_tiles = (K + 127) / 128 * 2;
-    const int64_t lanes = h->row_tiles * h->k_tiles * 32, pairs = h->row_tiles * h->groups() * 8;
+    const int64_t lanes = h->strips * h->k_tiles * 256, pairs = h->strips * h->groups() * 64;
     bsp_status_t st = BSP_OK;
     int bad = 0;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
@@ -316,7 +329,7 @@ bsp_status_t run(const bsp_q4* h, const bsp_q4* up, const void* X, int64_t x_str
     p.dtype = h->dtype;
     p.M = h->M;
     p.K = h->K;
-    p.row_tiles = h->row_tiles;
+    p.strips = h->strips;
     p.k_tiles = h->k_tiles;
     p.group = h->group;
     p.x = X;
@@ -386,7 +399,7 @@ bsp_status_t bsp_q4_export(bsp_q4_t h, uint8_t* codes, void* scales, uint8_t* ze
     DeviceGuard g(h->device);
     if (!g.ok) return BSP_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    const int64_t lanes = h->row_tiles * h->k_tiles * 32, pairs = h->row_tiles * h->groups() * 8;
+    const int64_t lanes = h->strips * h->k_tiles * 256, pairs = h->strips * h->groups() * 64;
     if (codes) q4_unpack_kernel<<<blocks_for(lanes), BLOCK, 0, s>>>(h->codes, h->M, h->K, h->k_tiles, lanes, codes);
     if (scales || zeros)
         q4_unpack_scales_kernel<<<blocks_for(pairs), BLOCK, 0, s>>>(h->scales, h->zeros, h->M,
@@ -402,7 +415,7 @@ bsp_status_t bsp_q4_decode(bsp_q4_t h, void* W, bsp_stream_t stream)
     DeviceGuard g(h->device);
     if (!g.ok) return BSP_ERR_CUDA;
     cudaStream_t s = (cudaStream_t)stream;
-    const int64_t lanes = h->row_tiles * h->k_tiles * 32;
+    const int64_t lanes = h->strips * h->k_tiles * 256;
     if (h->dtype == BSP_FP16)
         q4_decode_kernel<<<blocks_for(lanes), BLOCK, 0, s>>>(view(h), h->M, h->K, h->group, h->k_tiles, lanes, (__half*)W);
     else

@@ -14,9 +14,9 @@
 // values at a time.  So no weight is rounded, whatever its scale; weights
 // multiplied out and rounded to the type would leave an error of 1.3 times
 // the output's own rounding (the gated form 1.55 times).
-// Warps: 0 loads X, 1 issues the products, DW widen, PW promote (a warp
-// reaches the tensor-memory lanes 32 (w % 4) .. + 31, so a thread has one
-// row of each strip).  Where few tiles leave SMs idle, the CTAs of a cluster
+// Warps: 0 loads X, 1 issues the products, 3 loads codes and scales, DW widen,
+// PW promote (a warp reaches the tensor-memory lanes 32 (w % 4) ..
+// + 31, so a thread has one row of each strip).  Where few tiles leave SMs idle, the CTAs of a cluster
 // share a tile's columns and add their parts in order through shared memory.
 #pragma once
 
@@ -29,38 +29,47 @@
 #include <mutex>
 #include <type_traits>
 
-namespace bspq4 {
+// (Anonymous: the test library has the same kernels, and a process may load
+// both.)
+namespace {
+
+using namespace bspq4;
 
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr int BM = 128, BK = 64;
 constexpr int A_BYTES = BM * BK * 2;  // of a strip's step
 
-// BN columns of Y and MS strips a CTA.  Registers of a thread by role, from
-// REGS of each at launch (their sum over warpgroups is the launch's).
-template <int BN, int MS>
+// BN columns of Y and MS strips a CTA, G columns of a group.  Registers of a
+// thread by role, from REGS of each at launch (their sum over warpgroups is
+// the launch's).
+template <int G, int BN, int MS>
 struct Wide {
     static constexpr int SIZE = BN * MS;
-    static constexpr int CTAS = SIZE <= 64 ? 2 : 1;       // an SM
+    static constexpr int CTAS = SIZE <= 64 && MS == 1 ? 2 : 1;  // an SM
     static constexpr int DW = SIZE == 256 ? 4 : 8, PW = SIZE <= 64 ? 4 : 8;
     static constexpr int WARPS = 4 + DW + PW, THREADS = 32 * WARPS;
-    static constexpr int REGS = SIZE == 256 ? 128 : SIZE == 128 ? 96 : 64;
-    static constexpr int R_CONTROL = SIZE == 256 ? 40 : SIZE == 128 ? 32 : SIZE == 64 ? 24 : 40;
-    static constexpr int R_WIDEN = SIZE == 256 ? 72 : SIZE == 128 ? 72 : SIZE == 64 ? 64 : 72;
-    static constexpr int R_PROMOTE = SIZE == 256 ? 200 : SIZE == 128 ? 152 : SIZE == 64 ? 104 : 72;
+    static constexpr int REGS = SIZE == 256 ? 128 : SIZE == 128 ? 96 : CTAS == 1 ? 128 : 64;
+    static constexpr int R_CONTROL = SIZE == 256 ? 40 : SIZE == 128 ? 32 : CTAS == 1 ? 128 : SIZE == 64 ? 24 : 40;
+    static constexpr int R_WIDEN = SIZE == 256 ? 72 : SIZE == 128 ? 72 : CTAS == 1 ? 128 : SIZE == 64 ? 64 : 72;
+    static constexpr int R_PROMOTE = SIZE == 256 ? 200 : SIZE == 128 ? 152 : CTAS == 1 ? 128 : SIZE == 64 ? 104 : 72;
     static_assert(4 * R_CONTROL + DW * R_WIDEN + PW * R_PROMOTE == WARPS * REGS, "shares of the launch's registers");
     static constexpr int TILES = 8 * MS / DW;             // row tiles of a widening warp and step
-    static constexpr int AHEAD = TILES == 1 ? 6 : TILES == 2 ? 4 : 2;  // steps whose codes are on their way
-    static constexpr int B_BYTES = BN * BK * 2;
-    static constexpr int SA = SIZE <= 64 ? (MS == 2 ? 2 : 3) : (MS == 2 ? 3 : 4);
-    static constexpr int SB = BN == 256 ? 4 : BN == 128 ? 5 : BN == 64 ? 5 : 6;
     static constexpr int COLS = BN / (PW / 4);            // columns of a promoting thread, of each strip
+    // rings: A and B in steps of 64 columns, codes (with zero points) and
+    // scales in blocks of 128
+    static constexpr int SA = SIZE == 256 ? (MS == 2 ? 2 : 3) : SIZE == 128 ? (MS == 2 ? 3 : 4) : BN == 64 ? 2 : 3;
+    static constexpr int SB = 4, SC = SIZE == 128 && MS == 1 ? 6 : 4, SS = 8;
+    static constexpr int B_BYTES = BN * BK * 2;
+    static constexpr int Z_BYTES = 128 / G * 64, C_BYTES = MS * (8192 + Z_BYTES), S_BYTES = MS * (128 / G * 256);
     static constexpr int OFF_B = 0, OFF_A = SB * B_BYTES;
-    static constexpr int OFF_BAR = OFF_A + SA * MS * A_BYTES;
-    static constexpr int NBAR = 2 * SA + 2 * SB + 4 + 2;
+    static constexpr int OFF_C = OFF_A + SA * MS * A_BYTES, OFF_S = OFF_C + SC * C_BYTES;
+    static constexpr int OFF_BAR = OFF_S + SS * S_BYTES;
+    static constexpr int NBAR = 2 * (SA + SB + SC + SS) + 4 + 2;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
     static constexpr uint32_t TMEM = 2 * SIZE;
-    static_assert(SMEM <= (CTAS == 2 ? 113 : 227) * 1024 && OFF_BAR >= SIZE * BM * 4, "shared memory; parts of a split");
-    static_assert(CTAS == 2 || SMEM > 114 * 1024 || TMEM * 2 <= 512, "tensor memory of the CTAs that fit an SM");
+    static_assert(SMEM <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+    static_assert(OFF_S >= SIZE * BM * 4, "the sums, over the rings");
+    static_assert(CTAS == 2 || SMEM > 114 * 1024, "one CTA may take all of the tensor memory");
 };
 
 struct WideArgs {
@@ -173,6 +182,29 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds2(uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // The whole warp waits; false if the wait ran out.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t cap)
 {
@@ -180,11 +212,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t ca
 }
 
 template <class T, int G, int BN, int MS>
-__global__ void __launch_bounds__(Wide<BN, MS>::THREADS, Wide<BN, MS>::CTAS)
+__global__ void __launch_bounds__(Wide<G, BN, MS>::THREADS, Wide<G, BN, MS>::CTAS)
 q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ WideArgs a)
 {
-    using C = Wide<BN, MS>;
-    constexpr int SA = C::SA, SB = C::SB;
+    using C = Wide<G, BN, MS>;
+    constexpr int SA = C::SA, SB = C::SB, SC = C::SC, SS = C::SS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (bspx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -197,14 +229,17 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     const int units = a.k_tiles >> 1;
     const int k_begin = 2 * (int)((int64_t)units * rank / ranks);
     const int steps = 2 * (int)((int64_t)units * (rank + 1) / ranks) - k_begin;
-    const int groups = steps * BK / G;
     const uint32_t cap = a.spin_cap;
 
     uint64_t* a_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
     uint64_t* a_empty = a_full + SA;
     uint64_t* b_full = a_empty + SA;
     uint64_t* b_empty = b_full + SB;
-    uint64_t* d_full = b_empty + SB;
+    uint64_t* c_full = b_empty + SB;
+    uint64_t* c_empty = c_full + SC;
+    uint64_t* s_full = c_empty + SC;
+    uint64_t* s_empty = s_full + SS;
+    uint64_t* d_full = s_empty + SS;
     uint64_t* d_empty = d_full + 2;
     uint64_t* drain = d_empty + 2;
     uint64_t* read = drain + 1;
@@ -226,6 +261,14 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         for (int i = 0; i < SB; ++i) {
             bspx::mbar_init(b_full + i, 1);
             bspx::mbar_init(b_empty + i, 1);
+        }
+        for (int i = 0; i < SC; ++i) {
+            bspx::mbar_init(c_full + i, 1);
+            bspx::mbar_init(c_empty + i, C::DW);
+        }
+        for (int i = 0; i < SS; ++i) {
+            bspx::mbar_init(s_full + i, 1);
+            bspx::mbar_init(s_empty + i, C::PW);
         }
         for (int i = 0; i < 2; ++i) {
             bspx::mbar_init(d_full + i, 1);
@@ -270,38 +313,49 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             const uint32_t tm = __shfl_sync(FULL, tmem, 0);
             const uint64_t a_desc = smem_desc(bspx::smem_u32(smem + C::OFF_A)), b_desc = smem_desc(bspx::smem_u32(smem + C::OFF_B));
             constexpr uint32_t ID = idesc<T>(BN);
-            constexpr int PER = G / 16;  // products of a group (and strip)
-            int sa = 0, sb = 0, gi = 0, in = 0;  // ring slots; group, and products of it so far
+            constexpr int PARTS = G == 32 ? 2 : 1;            // groups of a step
+            constexpr int STEPS = G == 128 ? 2 : 1;           // steps of a group
+            constexpr int KS = BK / 16 / PARTS;               // products of a group in a step
+            int sa = 0, sb = 0;                               // ring slots
             uint32_t pa = 0, pb = 0;
-            for (int i = 0; i < n && !failed; ++i) {
-                if (!wait(a_full + sa, pa, cap) || !wait(b_full + sb, pb, cap)) {
-                    failed = true;
-                    break;
-                }
-                const uint64_t ad = a_desc + (uint64_t)(sa * (MS * A_BYTES >> 4)), bd = b_desc + (uint64_t)(sb * (C::B_BYTES >> 4));
+            // the next group's buffer is d; its last sums have been read when
+            // phase pd of its barrier is over (a fresh barrier's phase 1 is)
+            uint32_t buf = 0, pd = 1;
+            for (int i = 0; i < n && !failed; i += STEPS) {
 #pragma unroll
-                for (int k = 0; k < BK / 16; ++k) {
-                    if (in == 0 && gi >= 2) {  // the buffer's last sums have been read
-                        if (!wait(d_empty + (gi & 1), ((gi >> 1) - 1) & 1, cap)) {
-                            failed = true;
-                            break;
+                for (int e = 0; e < STEPS; ++e) {
+                    if (!wait(a_full + sa, pa, cap) || !wait(b_full + sb, pb, cap)) {
+                        failed = true;
+                        break;
+                    }
+                    const uint64_t ad = a_desc + (uint64_t)(sa * (MS * A_BYTES >> 4)), bd = b_desc + (uint64_t)(sb * (C::B_BYTES >> 4));
+#pragma unroll
+                    for (int x = 0; x < PARTS; ++x) {
+                        if (e == 0) {
+                            if (!wait(d_empty + buf, pd, cap)) {
+                                failed = true;
+                                break;
+                            }
+                            tc_after();
                         }
-                        tc_after();
-                    }
 #pragma unroll
-                    for (int m = 0; m < MS; ++m)
-                        product(tm + (gi & 1) * C::SIZE + m * BN, ad + (uint64_t)(m * (A_BYTES >> 4) + 2 * k),
-                                bd + (uint64_t)(2 * k), ID, in ? 1u : 0u);
-                    if (++in == PER) {
-                        commit(d_full + (gi & 1));
-                        in = 0;
-                        ++gi;
+                        for (int k = 0; k < KS; ++k)
+#pragma unroll
+                            for (int m = 0; m < MS; ++m)
+                                product(tm + buf * C::SIZE + m * BN, ad + (uint64_t)(m * (A_BYTES >> 4) + 2 * (x * KS + k)),
+                                        bd + (uint64_t)(2 * (x * KS + k)), ID, e || k ? 1u : 0u);
+                        if (e == STEPS - 1) {
+                            commit(d_full + buf);
+                            buf ^= 1u;
+                            if (!buf) pd ^= 1u;
+                        }
                     }
+                    if (failed) break;
+                    commit(a_empty + sa);
+                    commit(b_empty + sb);
+                    if (++sa == SA) { sa = 0; pa ^= 1u; }
+                    if (++sb == SB) { sb = 0; pb ^= 1u; }
                 }
-                commit(a_empty + sa);
-                commit(b_empty + sb);
-                if (++sa == SA) { sa = 0; pa ^= 1u; }
-                if (++sb == SB) { sb = 0; pb ^= 1u; }
             }
             // no product in flight and nobody reading when the tensor memory is
             // given back: with the full cap, and for readers that may be in
@@ -315,6 +369,40 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             tc_after();
             __syncwarp();
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(C::TMEM) : "memory");
+        } else if (warp == 3) {
+            // ---------------- codes and zero points, and scales: they depend
+            // on no kernel before this one
+            const int64_t block = strip * units + (k_begin >> 1);  // of 128 columns
+            const int n = steps >> 1;
+            int u = 0, sc = 0, ss = 0;
+            uint32_t pc = 0, ps = 0;
+            for (; u < n; ++u) {
+                if ((u >= SC && !wait(c_empty + sc, pc ^ 1u, cap)) || (u >= SS && !wait(s_empty + ss, ps ^ 1u, cap))) {
+                    failed = true;
+                    break;
+                }
+                if (lane == 0) {
+                    uint8_t *to = smem + C::OFF_C + sc * C::C_BYTES, *to_s = smem + C::OFF_S + ss * C::S_BYTES;
+                    uint32_t bytes = 0;
+#pragma unroll
+                    for (int m = 0; m < MS; ++m) bytes += 8192 + (a.w[m].zeros ? C::Z_BYTES : 0);
+                    bspx::mbar_arrive_expect_tx(c_full + sc, bytes);
+                    bspx::mbar_arrive_expect_tx(s_full + ss, C::S_BYTES);
+#pragma unroll
+                    for (int m = 0; m < MS; ++m) {
+                        bspx::bulk_g2s(to + m * 8192, a.w[m].codes + (block + u) * 512, 8192, c_full + sc);
+                        if (a.w[m].zeros)
+                            bspx::bulk_g2s(to + MS * 8192 + m * C::Z_BYTES, a.w[m].zeros + (block + u) * C::Z_BYTES, C::Z_BYTES, c_full + sc);
+                        bspx::bulk_g2s(to_s + m * (C::S_BYTES / MS), a.w[m].scales + (block + u) * (C::S_BYTES / MS / 4),
+                                       C::S_BYTES / MS, s_full + ss);
+                    }
+                }
+                __syncwarp();
+                if (++sc == SC) { sc = 0; pc ^= 1u; }
+                if (++ss == SS) { ss = 0; ps ^= 1u; }
+            }
+            for (int k = std::max(0, u - SC); k < u; ++k) bspx::mbar_wait_bounded(c_full + k % SC, (k / SC) & 1);
+            for (int k = std::max(0, u - SS); k < u; ++k) bspx::mbar_wait_bounded(s_full + k % SS, (k / SS) & 1);
         }
         if (failed && lane == 0) atomicExch(a.err, (int)BSP_ERR_TIMEOUT);
         if (ranks > 1) {
@@ -331,70 +419,59 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         // columns first, so that the eight lanes of a store's phase reach
         // distinct banks.
         const int w = warp - 4, g = lane >> 2, t = lane & 3;
-        const uint4* codes[C::TILES];
-        const uint8_t* zeros[C::TILES];
-        uint32_t to[C::TILES];
+        constexpr int ZN = G == 32 ? 2 : 1;  // groups of a step
+        const bool odd = g & 1;
+        uint32_t from[C::TILES], zero[C::TILES], to[C::TILES];
+        bool has_zeros[C::TILES];
 #pragma unroll
         for (int x = 0; x < C::TILES; ++x) {
             const int rt = w + x * C::DW, m = rt / 8, r = rt % 8;
-            const Q4View& v = MS == 2 && m ? a.w[1] : a.w[0];
-            codes[x] = v.codes + ((strip * 8 + r) * a.k_tiles + k_begin) * 32 + lane;
-            zeros[x] = v.zeros ? v.zeros + ((strip * 8 + r) * a.groups + (int64_t)k_begin * BK / G) * 8 + g : nullptr;
-            const int h = g & 1;
-            to[x] = bspx::smem_u32(smem + C::OFF_A) + m * A_BYTES + r * 2048 + g * 128 + (((4 * h + t) ^ g) << 4);
+            has_zeros[x] = (m ? a.w[1] : a.w[0]).zeros != nullptr;
+            from[x] = bspx::smem_u32(smem + C::OFF_C) + m * 8192 + r * 512 + lane * 16;
+            zero[x] = bspx::smem_u32(smem + C::OFF_C) + MS * 8192 + m * C::Z_BYTES + r * 8 + g;
+            to[x] = bspx::smem_u32(smem + C::OFF_A) + m * A_BYTES + r * 2048 + g * 128 + (((4 * (g & 1) + t) ^ g) << 4);
         }
-        constexpr int ZN = G == 32 ? 2 : 1;
-        uint4 next[C::AHEAD][C::TILES];
-        uint32_t znext[C::AHEAD][C::TILES][ZN];
-        auto fetch = [&](int i, int slot) {
-#pragma unroll
-            for (int x = 0; x < C::TILES; ++x) {
-                asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(next[slot][x].x), "=r"(next[slot][x].y), "=r"(next[slot][x].z), "=r"(next[slot][x].w)
-                             : "l"(codes[x] + (int64_t)i * 32));
-#pragma unroll
-                for (int z = 0; z < ZN; ++z)
-                    znext[slot][x][z] = zeros[x] ? __ldg(zeros[x] + ((int64_t)i * BK / G + z) * 8) : 0x88u;
+        int sa = 0, sc = 0;
+        uint32_t pa = 0, pc = 0;
+        for (int u = 0; u < steps >> 1 && !failed; ++u) {
+            if (!wait(c_full + sc, pc, cap)) {
+                failed = true;
+                break;
             }
-        };
+            uint4 v[2][C::TILES];
+            uint32_t z[2][C::TILES][ZN];
 #pragma unroll
-        for (int j = 0; j < C::AHEAD; ++j)
-            if (j < steps) fetch(j, j);
-        int sa = 0;
-        uint32_t pa = 0;
-        for (int i0 = 0; i0 < steps && !failed; i0 += C::AHEAD) {
-#pragma unroll
-            for (int j = 0; j < C::AHEAD; ++j) {
-                const int i = i0 + j;
-                if (i >= steps) break;
-                uint4 v[C::TILES];
-                uint32_t z[C::TILES][ZN];
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int x = 0; x < C::TILES; ++x) {
-                    v[x] = next[j][x];
+                    v[e][x] = lds16(from[x] + sc * C::C_BYTES + e * 4096);
 #pragma unroll
-                    for (int y = 0; y < ZN; ++y) z[x][y] = znext[j][x][y];
+                    for (int y = 0; y < ZN; ++y)
+                        z[e][x][y] = has_zeros[x] ? lds1(zero[x] + sc * C::C_BYTES + (e * BK / G + y) * 64) : 0x88u;
                 }
-                if (i + C::AHEAD < steps) fetch(i + C::AHEAD, j);
-                if (i >= SA && !wait(a_empty + sa, pa ^ 1u, cap)) {
+            __syncwarp();
+            if (lane == 0) bspx::mbar_arrive(c_empty + sc);
+            if (++sc == SC) { sc = 0; pc ^= 1u; }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (2 * u + e >= SA && !wait(a_empty + sa, pa ^ 1u, cap)) {
                     failed = true;
                     break;
                 }
 #pragma unroll
                 for (int x = 0; x < C::TILES; ++x) {
-                    const bool odd = g & 1;
-                    const uint32_t c[2][2] = {{odd ? v[x].z : v[x].x, odd ? v[x].w : v[x].y},
-                                              {odd ? v[x].x : v[x].z, odd ? v[x].y : v[x].w}};
+                    const uint4 q4 = v[e][x];
+                    const uint32_t c[2][2] = {{odd ? q4.z : q4.x, odd ? q4.w : q4.y}, {odd ? q4.x : q4.z, odd ? q4.y : q4.w}};
                     const uint32_t at = to[x] + sa * (MS * A_BYTES);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t z0, z1, p[4], q[4];
-                        Codes<T>::bias(ZN == 2 ? (odd ? z[x][ZN - 1 - h * (ZN - 1)] : z[x][h * (ZN - 1)]) : z[x][0], z0, z1);
+                        Codes<T>::bias(ZN == 2 && (odd ? !h : h) ? z[e][x][ZN - 1] : z[e][x][0], z0, z1);
                         Codes<T>::widen(c[h][0], z0, z1, p);
                         Codes<T>::widen(c[h][1], z0, z1, q);
                         const uint32_t o = at ^ (h << 6);  // the other half: chunk ^ 4
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(o), "r"(p[0]), "r"(p[2]), "r"(q[0]), "r"(q[2]) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(o + 1024), "r"(p[1]), "r"(p[3]), "r"(q[1]), "r"(q[3]) : "memory");
+                        sts16(o, p[0], p[2], q[0], q[2]);
+                        sts16(o + 1024, p[1], p[3], q[1], q[3]);
                     }
                 }
                 bspx::fence_proxy_async_smem();
@@ -415,118 +492,114 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     {
         // ---------------- sums of groups, scaled, into registers
         const int p = warp - 4 - C::DW, quad = warp & 3, row = 32 * quad + lane, c0 = (p >> 2) * C::COLS;
-        const uint16_t* scales[MS];
-#pragma unroll
-        for (int m = 0; m < MS; ++m) {
-            const Q4View& v = m ? a.w[1] : a.w[0];
-            scales[m] = reinterpret_cast<const uint16_t*>(v.scales + ((strip * 8 + row / 16) * a.groups + (int64_t)k_begin * BK / G) * 8 + row % 8) +
-                        (row >> 3 & 1);
-        }
+        const uint32_t scales = bspx::smem_u32(smem + C::OFF_S) + (row / 16 * 8 + row % 8) * 4 + (row >> 3 & 1) * 2;
         const float upper = row & 8 ? 1.f / Codes<T>::UPPER : 1.f;
-        auto scale_of = [&](int m, int gi) {
-            const uint16_t bits = __ldg(scales[m] + (int64_t)min(gi, groups - 1) * 16);
-            return to_float(*reinterpret_cast<const T*>(&bits)) * upper;
-        };
+        constexpr int PER = 128 / G;  // groups of a block
         uint64_t sum[MS][C::COLS / 2];
 #pragma unroll
         for (int m = 0; m < MS; ++m)
 #pragma unroll
             for (int i = 0; i < C::COLS / 2; ++i) sum[m][i] = 0;
         const uint32_t at = tmem + ((uint32_t)(32 * quad) << 16) + c0;
-        float s0[MS], s1[MS];
-#pragma unroll
-        for (int m = 0; m < MS; ++m) {
-            s0[m] = groups ? scale_of(m, 0) : 0.f;
-            s1[m] = groups ? scale_of(m, 1) : 0.f;
-        }
-        for (int gi = 0; gi < groups; ++gi) {
-            float s2[MS];
-#pragma unroll
-            for (int m = 0; m < MS; ++m) s2[m] = scale_of(m, gi + 2);
-            if (!wait(d_full + (gi & 1), (gi >> 1) & 1, cap)) {
+        int ss = 0, gi = 0;
+        uint32_t ps = 0;
+        for (int u = 0; u < steps >> 1 && !failed; ++u) {
+            if (!wait(s_full + ss, ps, cap)) {
                 failed = true;
                 break;
             }
-            tc_after();
+            float s[PER][MS];
 #pragma unroll
-            for (int m = 0; m < MS; ++m) {
-                const uint64_t ss = pair(s0[m], s0[m]);
+            for (int y = 0; y < PER; ++y)
 #pragma unroll
-                for (int c = 0; c < C::COLS; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32(at + (gi & 1) * C::SIZE + m * BN + c, r);
-                    tmem_wait(r);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        sum[m][c / 2 + i] = fma2(ss, pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sum[m][c / 2 + i]);
-                }
-            }
-            tc_before();
+                for (int m = 0; m < MS; ++m)
+                    s[y][m] = half_of<T>(lds2(scales + ss * C::S_BYTES + (m * PER + y) * 256), 0) * upper;
             __syncwarp();
-            if (lane == 0) bspx::mbar_arrive(d_empty + (gi & 1));
+            if (lane == 0) bspx::mbar_arrive(s_empty + ss);
+            if (++ss == SS) { ss = 0; ps ^= 1u; }
 #pragma unroll
-            for (int m = 0; m < MS; ++m) {
-                s0[m] = s1[m];
-                s1[m] = s2[m];
+            for (int y = 0; y < PER; ++y, ++gi) {
+                if (!wait(d_full + (gi & 1), (gi >> 1) & 1, cap)) {
+                    failed = true;
+                    break;
+                }
+                tc_after();
+#pragma unroll
+                for (int m = 0; m < MS; ++m) {
+                    const uint64_t f = pair(s[y][m], s[y][m]);
+#pragma unroll
+                    for (int c = 0; c < C::COLS; c += 32) {
+                        uint32_t r[32];
+                        tmem_ld32(at + (gi & 1) * C::SIZE + m * BN + c, r);
+                        tmem_wait(r);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            sum[m][c / 2 + i] = fma2(f, pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sum[m][c / 2 + i]);
+                    }
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bspx::mbar_arrive(d_empty + (gi & 1));
             }
         }
         tc_before();
         __syncwarp();
         if (lane == 0) bspx::mbar_arrive(read);
-        wait_prior_grids();  // what is written below may still be read by the kernels before this one
-        const int64_t row_y = strip * BM + row;
-        T* y = reinterpret_cast<T*>(a.y) + row_y;
-        if (ranks == 1) {
-            if (!failed && row_y < a.M) {
+        // ---------------- the sums to shared memory, [strip][column][row],
+        // over the rings: every product is done, and every promoting warp
+        // has its last scales
+        asm volatile("bar.sync 1, %0;" ::"n"(C::PW * 32) : "memory");
+        float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-                for (int i = 0; i < C::COLS / 2; ++i) {
-                    float v[2], u[2];
-                    unpair(sum[0][i], v[0], v[1]);
-                    if (MS == 2) {
-                        unpair(sum[MS - 1][i], u[0], u[1]);
-                        v[0] = activate(v[0], a.act) * u[0];
-                        v[1] = activate(v[1], a.act) * u[1];
-                    }
+        for (int m = 0; m < MS; ++m)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int64_t n = n0 + c0 + 2 * i + e;
-                        if (n < a.N) y[n * a.y_stride] = from_float<T>(v[e]);
-                    }
+            for (int i = 0; i < C::COLS / 2; ++i) {
+                float v[2];
+                unpair(sum[m][i], v[0], v[1]);
+                part[(m * BN + c0 + 2 * i) * BM + row] = v[0];
+                part[(m * BN + c0 + 2 * i + 1) * BM + row] = v[1];
+            }
+        if (ranks > 1) bspx::cluster_sync();
+        else asm volatile("bar.sync 1, %0;" ::"n"(C::PW * 32) : "memory");
+        wait_prior_grids();  // Y may still be read by the kernels before this one
+        // a warp a column: four rows a lane
+        const int first = BN * rank / ranks, last = (int)min((int64_t)(BN * (rank + 1) / ranks), a.N - n0);
+        const int64_t m0 = strip * BM + 4 * lane;
+        const bool whole = m0 + 4 <= a.M && a.y_stride % 4 == 0;
+#pragma unroll 1
+        for (int c = first + p; c < last && !failed; c += C::PW) {
+            float4 v[MS];
+#pragma unroll
+            for (int m = 0; m < MS; ++m) {
+                const uint32_t from = bspx::smem_u32(part + (m * BN + c) * BM + 4 * lane);
+                v[m] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (uint32_t k = 0; k < ranks; ++k) {
+                    float4 x;
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                                 : "r"(ranks > 1 ? bspx::mapa_shared(from, k) : from)
+                                 : "memory");
+                    v[m].x += x.x;
+                    v[m].y += x.y;
+                    v[m].z += x.z;
+                    v[m].w += x.w;
                 }
             }
-        } else {
-            // the rings are idle: every product of this CTA is done (its last
-            // sums are here).  Parts [strip][column][row].
-            float* part = reinterpret_cast<float*>(smem);
+            if (MS == 2) {
+                v[0].x = activate(v[0].x, a.act) * v[MS - 1].x;
+                v[0].y = activate(v[0].y, a.act) * v[MS - 1].y;
+                v[0].z = activate(v[0].z, a.act) * v[MS - 1].z;
+                v[0].w = activate(v[0].w, a.act) * v[MS - 1].w;
+            }
+            T* y = reinterpret_cast<T*>(a.y) + (n0 + c) * a.y_stride + m0;
+            alignas(8) const T o[4] = {from_float<T>(v[0].x), from_float<T>(v[0].y), from_float<T>(v[0].z), from_float<T>(v[0].w)};
+            if (whole) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
+            else
 #pragma unroll
-            for (int m = 0; m < MS; ++m)
-#pragma unroll
-                for (int i = 0; i < C::COLS / 2; ++i) {
-                    float v[2];
-                    unpair(sum[m][i], v[0], v[1]);
-                    part[(m * BN + c0 + 2 * i) * BM + row] = v[0];
-                    part[(m * BN + c0 + 2 * i + 1) * BM + row] = v[1];
-                }
-            bspx::cluster_sync();
-            const int first = BN * rank / ranks, last = BN * (rank + 1) / ranks;
-            if (!failed && row_y < a.M)
-                for (int c = first + (p >> 2); c < last; c += C::PW / 4) {
-                    float v[MS];
-#pragma unroll
-                    for (int m = 0; m < MS; ++m) {
-                        v[m] = 0.f;
-                        const uint32_t from = bspx::smem_u32(part + (m * BN + c) * BM + row);
-                        for (uint32_t k = 0; k < ranks; ++k) {
-                            float x;
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(bspx::mapa_shared(from, k)) : "memory");
-                            v[m] += x;
-                        }
-                    }
-                    if (MS == 2) v[0] = activate(v[0], a.act) * v[MS - 1];
-                    if (n0 + c < a.N) y[(n0 + c) * a.y_stride] = from_float<T>(v[0]);
-                }
-            bspx::cluster_sync();  // others may still read this CTA's parts
+                for (int e = 0; e < 4; ++e)
+                    if (m0 + e < a.M) y[e] = o[e];
         }
+        if (ranks > 1) bspx::cluster_sync();  // others may still read this CTA's sums
     }
     if (failed && lane == 0) atomicExch(a.err, (int)BSP_ERR_TIMEOUT);
 }
@@ -548,7 +621,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 template <class T, int G, int BN, int MS>
 bsp_status_t launch_wide(const Problem& p, int ranks, cudaStream_t s)
 {
-    using C = Wide<BN, MS>;
+    using C = Wide<G, BN, MS>;
     static bsp_attr_once attr_once;
     if (!attr_once.run(p.device, [] {
             return cudaFuncSetAttribute(q4_wide_kernel<T, G, BN, MS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -614,7 +687,7 @@ bsp_status_t wide_by_shape(const Problem& p, cudaStream_t s)
     auto go = [&](auto bn, auto ms) {
         constexpr int BN = decltype(bn)::value, MS = decltype(ms)::value;
         const int64_t tiles = strips * ((p.N + BN - 1) / BN);
-        return launch_wide<T, G, BN, MS>(p, split_of(p, tiles, Wide<BN, MS>::CTAS), s);
+        return launch_wide<T, G, BN, MS>(p, split_of(p, tiles, Wide<G, BN, MS>::CTAS), s);
     };
     using std::integral_constant;
     if (p.gated) {
@@ -639,4 +712,4 @@ bsp_status_t run_wide(const Problem& p, cudaStream_t s)
     }
 }
 
-}  // namespace bspq4
+}  // namespace

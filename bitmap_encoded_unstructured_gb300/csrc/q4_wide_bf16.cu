@@ -1,4 +1,4 @@
 // The bf16 instances of the wide 4-bit products (q4_wide.cuh).
 #include "q4_wide.cuh"
 
-bsp_status_t bsp_run_q4_wide_bf16(const bspq4::Problem& p, cudaStream_t s) { return bspq4::run_wide<__nv_bfloat16>(p, s); }
+bsp_status_t bsp_run_q4_wide_bf16(const bspq4::Problem& p, cudaStream_t s) { return run_wide<__nv_bfloat16>(p, s); }

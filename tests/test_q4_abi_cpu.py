@@ -21,12 +21,12 @@ def lib():
 
 class Q4(C.Structure):  # what the checks see of a handle
     _fields_ = [("magic", C.c_uint32), ("device", C.c_int), ("num_sms", C.c_int), ("dtype", C.c_int), ("M", C.c_int64),
-                ("K", C.c_int64), ("group", C.c_int32), ("pad", C.c_int32), ("row_tiles", C.c_int64),
+                ("K", C.c_int64), ("group", C.c_int32), ("pad", C.c_int32), ("strips", C.c_int64),
                 ("k_tiles", C.c_int64), ("at", C.c_void_p * 4)]
 
 
 def q4(**kw):
-    d = dict(magic=0xB5B14B17, device=0, num_sms=152, dtype=0, M=40, K=64, group=32, row_tiles=8, k_tiles=2)
+    d = dict(magic=0xB5B14B17, device=0, num_sms=152, dtype=0, M=40, K=64, group=32, strips=1, k_tiles=2)
     d.update(kw)
     return Q4(**d)
 
