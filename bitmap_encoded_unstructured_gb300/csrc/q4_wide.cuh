@@ -2,22 +2,27 @@
 // more than a few), and the gated form over two weights, on the
 // 5th-generation tensor cores.
 //
-// A CTA takes one strip of 128 rows of W (the gated form: the strips of both
-// weights) and BN rows of X, and walks the columns in steps of 64:
+// A pair of CTAs takes 256 rows (two strips of W; the gated form: a strip of
+// each weight) and BN rows of X, and walks the columns in blocks of 128:
 //   A  codes less zero points as fp16 or bf16, exact small integers, made
-//      by the widening warps in shared memory (K-major, swizzled by 128
-//      bytes: a lane's eight columns of a row are one 16-byte chunk)
-//   B  X by TMA, the same layout
-//   D  sums of one group of columns, in tensor memory, two buffers
+//      by each CTA's widening warps from its own strip, in shared memory
+//      (K-major, swizzled by 128 bytes: a lane's eight columns of a row are
+//      one 16-byte chunk)
+//   B  X by TMA, the same layout, half of the BN rows in each CTA
+//   D  sums of one group of columns, in tensor memory, two buffers; one
+//      product (cta_group::2) works on both CTAs' rows
 // Scales are applied to D: the promoting warps read a group's sums while
-// the next group's products run, and add s D to fp32 sums in registers, two
-// values at a time.  So no weight is rounded, whatever its scale; weights
+// the next group's products run, and add s D to fp32 sums in registers.  So no weight is rounded, whatever its scale; weights
 // multiplied out and rounded to the type would leave an error of 1.3 times
 // the output's own rounding (the gated form 1.55 times).
-// Warps: 0 loads X, 1 issues the products, 3 loads codes and scales, DW widen,
-// PW promote (a warp reaches the tensor-memory lanes 32 (w % 4) ..
-// + 31, so a thread has one row of each strip).  Where few tiles leave SMs idle, the CTAs of a cluster
-// share a tile's columns and add their parts in order through shared memory.
+//
+// Warps of a CTA: 0 loads X and 2 says when it is there, 1 issues the products
+// (in the pair's first CTA), 3 loads codes and scales, DW widen, PW promote (a warp reaches the tensor-memory lanes 32 (w % 4) .. + 31, so
+// a thread has one row).  The issuing warp sets the pace, not the tensor
+// pipe: a wait costs it about 150 cycles though it is over, a product 75.  So
+// a block has one barrier for all that its products read, from both CTAs.
+// Where few tiles leave SMs idle, the pairs of a larger cluster share a
+// tile's columns and add their parts in order through shared memory.
 #pragma once
 
 #include "bsp_q4.cuh"
@@ -36,46 +41,40 @@ namespace {
 using namespace bspq4;
 
 constexpr uint32_t FULL = 0xFFFFFFFFu;
-constexpr int BM = 128, BK = 64;
-constexpr int A_BYTES = BM * BK * 2;  // of a strip's step
+constexpr int BM = 128, BK = 128;      // rows of a strip, columns of a block
+constexpr int A_HALF = BM * 64 * 2, A_BYTES = 2 * A_HALF;  // 64 columns of a strip; a block
 
-// BN columns of Y and MS strips a CTA, G columns of a group.  Registers of a
-// thread by role, from REGS of each at launch (their sum over warpgroups is
-// the launch's).
-template <int G, int BN, int MS>
+// BN columns of Y, G columns of a group.  Registers of a thread by role, from
+// REGS of each at launch (their sum over warpgroups is the launch's).
+template <int G, int BN>
 struct Wide {
-    static constexpr int SIZE = BN * MS;
-    static constexpr int CTAS = SIZE <= 64 && MS == 1 ? 2 : 1;  // an SM
-    static constexpr int DW = SIZE == 256 ? 4 : 8, PW = SIZE <= 64 ? 4 : 8;
+    static constexpr int CTAS = BN <= 64 ? 2 : 1;         // an SM
+    static constexpr int DW = BN == 256 ? 4 : 8, PW = BN <= 64 ? 4 : 8;
     static constexpr int WARPS = 4 + DW + PW, THREADS = 32 * WARPS;
-    static constexpr int REGS = SIZE == 256 ? 128 : SIZE == 128 ? 96 : CTAS == 1 ? 128 : 64;
-    static constexpr int R_CONTROL = SIZE == 256 ? 40 : SIZE == 128 ? 32 : CTAS == 1 ? 128 : SIZE == 64 ? 24 : 40;
-    static constexpr int R_WIDEN = SIZE == 256 ? 72 : SIZE == 128 ? 72 : CTAS == 1 ? 128 : SIZE == 64 ? 64 : 72;
-    static constexpr int R_PROMOTE = SIZE == 256 ? 200 : SIZE == 128 ? 152 : CTAS == 1 ? 128 : SIZE == 64 ? 104 : 72;
-    static_assert(4 * R_CONTROL + DW * R_WIDEN + PW * R_PROMOTE == WARPS * REGS, "shares of the launch's registers");
-    static constexpr int TILES = 8 * MS / DW;             // row tiles of a widening warp and step
-    static constexpr int COLS = BN / (PW / 4);            // columns of a promoting thread, of each strip
-    // rings: A and B in steps of 64 columns, codes (with zero points) and
-    // scales in blocks of 128
-    static constexpr int SA = SIZE == 256 ? (MS == 2 ? 2 : 3) : SIZE == 128 ? (MS == 2 ? 3 : 4) : BN == 64 ? 2 : 3;
-    static constexpr int SB = 4, SC = SIZE == 128 && MS == 1 ? 6 : 4, SS = 8;
-    static constexpr int B_BYTES = BN * BK * 2;
-    static constexpr int Z_BYTES = 128 / G * 64, C_BYTES = MS * (8192 + Z_BYTES), S_BYTES = MS * (128 / G * 256);
-    static constexpr int OFF_B = 0, OFF_A = SB * B_BYTES;
-    static constexpr int OFF_C = OFF_A + SA * MS * A_BYTES, OFF_S = OFF_C + SC * C_BYTES;
+    static constexpr int REGS = BN == 256 ? 128 : BN == 128 ? 96 : 64;
+    static constexpr int R_CONTROL = 40;
+    static constexpr int R_WIDEN = BN == 256 ? 104 : BN == 128 ? 88 : BN == 64 ? 56 : 72;
+    static constexpr int R_PROMOTE = BN == 256 ? 184 : BN == 128 ? 128 : BN == 64 ? 104 : 72;
+    static constexpr int TILES = 8 / DW;                  // row tiles of a widening warp
+    static constexpr int COLS = BN / (PW / 4);            // columns of a promoting thread
+    // rings: A with B, codes (with zero points), scales
+    static constexpr int SR = BN >= 128 ? 3 : 2, SC = BN == 256 ? 3 : BN == 128 ? 6 : BN == 64 ? 3 : 4, SS = BN <= 64 && G == 32 ? 4 : 8;
+    static constexpr int B_HALF = BN / 2 * 64 * 2, B_BYTES = 2 * B_HALF;
+    static constexpr int Z_BYTES = 128 / G * 64, C_BYTES = 8192 + Z_BYTES, S_BYTES = 128 / G * 256;
+    static constexpr int OFF_B = SR * A_BYTES, OFF_C = OFF_B + SR * B_BYTES, OFF_S = OFF_C + SC * C_BYTES;
     static constexpr int OFF_BAR = OFF_S + SS * S_BYTES;
-    static constexpr int NBAR = 2 * (SA + SB + SC + SS) + 4 + 2;
+    static constexpr int NBAR = 3 * SR + 2 * (SC + SS) + 4 + 2;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
-    static constexpr uint32_t TMEM = 2 * SIZE;
+    static constexpr uint32_t TMEM = 2 * BN;
     static_assert(SMEM <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
-    static_assert(OFF_S >= SIZE * BM * 4, "the sums, over the rings");
+    static_assert(OFF_S >= BN * BM * 4, "the sums, over the rings");
     static_assert(CTAS == 2 || SMEM > 114 * 1024, "one CTA may take all of the tensor memory");
 };
 
 struct WideArgs {
     Q4View w[2];
     int act;
-    int64_t M, N, groups;
+    int64_t M, N, groups, strips;
     int32_t k_tiles, ntiles;
     void* y;
     int64_t y_stride;
@@ -84,12 +83,13 @@ struct WideArgs {
     bool stall;  // test only: the first copy of X is skipped
 };
 
-// kind::f16 instruction descriptor: D fp32, A and B fp16 (or bf16), K-major.
+// kind::f16 instruction descriptor: D fp32, A and B fp16 (or bf16), K-major,
+// the 256 rows of both CTAs.
 template <class T>
 __host__ __device__ constexpr uint32_t idesc(int n)
 {
     const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
-    return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+    return (1u << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(2 * BM >> 4) << 24);
 }
 
 // Shared-memory matrix descriptor: K-major rows of 128 B swizzled by 128 B,
@@ -108,18 +108,21 @@ __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint
         "{\n\t.reg .pred p, q;\n\t"
         "elect.sync _|q, 0xFFFFFFFF;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"(accum)
         : "memory");
 }
 
-__device__ __forceinline__ void commit(uint64_t* bar)
+// One arrival, when the products issued so far are done, on the barrier at
+// this offset in each CTA of `mask` (by cluster rank).
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t mask)
 {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
         "elect.sync _|q, 0xFFFFFFFF;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-            bspx::smem_u32(bar))
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            bspx::smem_u32(bar)),
+        "h"((uint16_t)mask)
         : "memory");
 }
 
@@ -146,20 +149,6 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));
-}
-
-__device__ __forceinline__ uint64_t pair(float a, float b)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
 }
 
 template <int REGS>
@@ -211,56 +200,68 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint32_t ca
     return __all_sync(FULL, bspx::mbar_wait_bounded(bar, parity, cap));
 }
 
-template <class T, int G, int BN, int MS>
-__global__ void __launch_bounds__(Wide<G, BN, MS>::THREADS, Wide<G, BN, MS>::CTAS)
+// An arrival on a barrier of another CTA of the cluster (or this one's), by
+// its shared-window address there.  It releases to this CTA only: what it
+// tells of (a tile in this CTA's shared memory, behind a proxy fence; sums read from its tensor
+// memory) is read by this SM's own tensor core.  A release to the cluster
+// took some 1000 cycles.
+__device__ __forceinline__ void arrive_at(uint32_t addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+template <class T, int G, int BN, bool GATED>
+__global__ void __launch_bounds__(Wide<G, BN>::THREADS, Wide<G, BN>::CTAS)
 q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ WideArgs a)
 {
-    using C = Wide<G, BN, MS>;
-    constexpr int SA = C::SA, SB = C::SB, SC = C::SC, SS = C::SS;
+    using C = Wide<G, BN>;
+    static_assert(4 * C::R_CONTROL + C::DW * C::R_WIDEN + C::PW * C::R_PROMOTE <= C::WARPS * C::REGS, "shares of the launch's registers");
+    constexpr int SR = C::SR, SC = C::SC, SS = C::SS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (bspx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t ranks;
     asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
-    const uint32_t rank = bspx::cluster_ctarank();
+    const uint32_t rank = bspx::cluster_ctarank(), half = rank & 1u, lead = rank & ~1u;
+    const uint32_t shares = ranks >> 1, share = rank >> 1;  // pairs that share the columns
     const int64_t tile = blockIdx.x / ranks;
-    const int64_t strip = tile / a.ntiles, n0 = tile % a.ntiles * BN;
-    // this CTA's share of the columns, in blocks of 128
-    const int units = a.k_tiles >> 1;
-    const int k_begin = 2 * (int)((int64_t)units * rank / ranks);
-    const int steps = 2 * (int)((int64_t)units * (rank + 1) / ranks) - k_begin;
+    const int64_t strip = GATED ? tile / a.ntiles : tile / a.ntiles * 2 + half, n0 = tile % a.ntiles * BN;
+    // (an odd last strip is read twice, and stored once)
+    const int64_t strip_in = GATED || strip < a.strips ? strip : a.strips - 1;
+    const Q4View& w = GATED && half ? a.w[1] : a.w[0];
+    // this pair's share of the blocks of columns
+    const int blocks_all = a.k_tiles >> 1;
+    const int first = (int)((int64_t)blocks_all * share / shares);
+    int blocks = (int)((int64_t)blocks_all * (share + 1) / shares) - first;
+    const int64_t block0 = strip_in * blocks_all + first;
     const uint32_t cap = a.spin_cap;
 
-    uint64_t* a_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* a_empty = a_full + SA;
-    uint64_t* b_full = a_empty + SA;
-    uint64_t* b_empty = b_full + SB;
-    uint64_t* c_full = b_empty + SB;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // A and B of a block, in the first CTA
+    uint64_t* x_full = full + SR;                                     // this CTA's half of B
+    uint64_t* empty = x_full + SR;
+    uint64_t* c_full = empty + SR;
     uint64_t* c_empty = c_full + SC;
     uint64_t* s_full = c_empty + SC;
     uint64_t* s_empty = s_full + SS;
     uint64_t* d_full = s_empty + SS;
-    uint64_t* d_empty = d_full + 2;
+    uint64_t* d_empty = d_full + 2;                                   // in the first CTA
     uint64_t* drain = d_empty + 2;
     uint64_t* read = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(read + 1);
 
     if (warp == 1) {
         __syncwarp();
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          bspx::smem_u32(tmem_slot)),
                      "r"(C::TMEM)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < SA; ++i) {
-            bspx::mbar_init(a_full + i, C::DW);
-            bspx::mbar_init(a_empty + i, 1);
-        }
-        for (int i = 0; i < SB; ++i) {
-            bspx::mbar_init(b_full + i, 1);
-            bspx::mbar_init(b_empty + i, 1);
+        for (int i = 0; i < SR; ++i) {
+            bspx::mbar_init(full + i, 2 * C::DW + 2);
+            bspx::mbar_init(x_full + i, 1);
+            bspx::mbar_init(empty + i, 1);
         }
         for (int i = 0; i < SC; ++i) {
             bspx::mbar_init(c_full + i, 1);
@@ -272,7 +273,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         }
         for (int i = 0; i < 2; ++i) {
             bspx::mbar_init(d_full + i, 1);
-            bspx::mbar_init(d_empty + i, C::PW);
+            bspx::mbar_init(d_empty + i, 2 * C::PW);
         }
         bspx::mbar_init(drain, 1);
         bspx::mbar_init(read, C::PW);
@@ -280,9 +281,14 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     }
     tc_before();
     __syncthreads();
+    bspx::cluster_sync();
     tc_after();
     const uint32_t tmem = *tmem_slot;
-    bool failed = false;
+    // one product addresses both CTAs' tensor memory: they were given the same
+    uint32_t other;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(bspx::mapa_shared(bspx::smem_u32(tmem_slot), rank ^ 1u)) : "memory");
+    bool failed = other != tmem;
+    if (failed) blocks = 0;
     // (not before the tensor memory is this CTA's: a kernel that starts early
     // may take some, and then waits for this one)
     if (threadIdx.x == 0) launch_dependents();
@@ -290,112 +296,108 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     if (warp < 4) {
         take_registers<C::REGS, C::R_CONTROL>();
         if (warp == 0) {
-            // ---------------- X
+            // ---------------- X: this CTA's half of the rows
             wait_prior_grids();
-            int i = 0;
-            for (; i < steps; ++i) {
-                const int s = i % SB;
-                if (i >= SB && !wait(b_empty + s, (i / SB - 1) & 1, cap)) {
+            int i = 0, s = 0;
+            uint32_t ph = 0;
+            for (; i < blocks; ++i) {
+                if (i >= SR && !wait(empty + s, ph ^ 1u, cap)) {
                     failed = true;
                     break;
                 }
                 if (lane == 0 && !(a.stall && i == 0)) {
-                    bspx::mbar_arrive_expect_tx(b_full + s, (uint32_t)C::B_BYTES);
-                    tma_load_2d(bspx::smem_u32(smem + C::OFF_B + s * C::B_BYTES), &map_x, (k_begin + i) * BK, (int)n0, b_full + s);
+                    const uint32_t to = bspx::smem_u32(smem + C::OFF_B + s * C::B_BYTES);
+                    bspx::mbar_arrive_expect_tx(x_full + s, (uint32_t)C::B_BYTES);
+                    tma_load_2d(to, &map_x, (first + i) * BK, (int)(n0 + half * (BN / 2)), x_full + s);
+                    tma_load_2d(to + C::B_HALF, &map_x, (first + i) * BK + 64, (int)(n0 + half * (BN / 2)), x_full + s);
                 }
                 __syncwarp();
+                if (++s == SR) { s = 0; ph ^= 1u; }
             }
             // no copy may land after the CTA is gone (the full cap, whatever `cap` is)
-            for (int k = std::max(a.stall ? 1 : 0, i - SB); k < i; ++k) bspx::mbar_wait_bounded(b_full + k % SB, (k / SB) & 1);
+            for (int k = std::max(a.stall ? 1 : 0, i - SR); k < i; ++k) bspx::mbar_wait_bounded(x_full + k % SR, (k / SR) & 1);
+        } else if (warp == 2) {
+            // ---------------- tells the first CTA that this half of X is here
+            int s = 0;
+            uint32_t ph = 0;
+            for (int i = 0; i < blocks; ++i) {
+                if (!wait(x_full + s, ph, cap)) {
+                    failed = true;
+                    break;
+                }
+                if (lane == 0) arrive_at(bspx::mapa_shared(bspx::smem_u32(full + s), lead));
+                __syncwarp();
+                if (++s == SR) { s = 0; ph ^= 1u; }
+            }
         } else if (warp == 1) {
-            // ---------------- products
-            const int n = __shfl_sync(FULL, steps, 0);
-            const uint32_t tm = __shfl_sync(FULL, tmem, 0);
-            const uint64_t a_desc = smem_desc(bspx::smem_u32(smem + C::OFF_A)), b_desc = smem_desc(bspx::smem_u32(smem + C::OFF_B));
-            constexpr uint32_t ID = idesc<T>(BN);
-            constexpr int PARTS = G == 32 ? 2 : 1;            // groups of a step
-            constexpr int STEPS = G == 128 ? 2 : 1;           // steps of a group
-            constexpr int KS = BK / 16 / PARTS;               // products of a group in a step
-            int sa = 0, sb = 0;                               // ring slots
-            uint32_t pa = 0, pb = 0;
-            // the next group's buffer is d; its last sums have been read when
-            // phase pd of its barrier is over (a fresh barrier's phase 1 is)
-            uint32_t buf = 0, pd = 1;
-            for (int i = 0; i < n && !failed; i += STEPS) {
-#pragma unroll
-                for (int e = 0; e < STEPS; ++e) {
-                    if (!wait(a_full + sa, pa, cap) || !wait(b_full + sb, pb, cap)) {
+            if (!half) {
+                // ---------------- products
+                const int n = __shfl_sync(FULL, blocks, 0);
+                const uint32_t tm = __shfl_sync(FULL, tmem, 0), both = __shfl_sync(FULL, 3u << lead, 0);
+                const uint64_t a_desc = smem_desc(bspx::smem_u32(smem)), b_desc = smem_desc(bspx::smem_u32(smem + C::OFF_B));
+                constexpr uint32_t ID = idesc<T>(BN);
+                constexpr int PER = 128 / G, KS = G / 16;         // groups of a block, products of a group
+                int s = 0;
+                // the next group's buffer is buf; its last sums have been read when
+                // phase pd of its barrier is over (a fresh barrier's phase 1 is)
+                uint32_t ph = 0, buf = 0, pd = 1;
+                for (int i = 0; i < n && !failed; ++i) {
+                    if (!wait(full + s, ph, cap)) {
                         failed = true;
                         break;
                     }
-                    const uint64_t ad = a_desc + (uint64_t)(sa * (MS * A_BYTES >> 4)), bd = b_desc + (uint64_t)(sb * (C::B_BYTES >> 4));
+                    const uint64_t ad = a_desc + (uint64_t)(s * (A_BYTES >> 4)), bd = b_desc + (uint64_t)(s * (C::B_BYTES >> 4));
 #pragma unroll
-                    for (int x = 0; x < PARTS; ++x) {
-                        if (e == 0) {
-                            if (!wait(d_empty + buf, pd, cap)) {
-                                failed = true;
-                                break;
-                            }
-                            tc_after();
+                    for (int x = 0; x < PER; ++x) {
+                        if (!wait(d_empty + buf, pd, cap)) {
+                            failed = true;
+                            break;
                         }
+                        tc_after();
 #pragma unroll
-                        for (int k = 0; k < KS; ++k)
-#pragma unroll
-                            for (int m = 0; m < MS; ++m)
-                                product(tm + buf * C::SIZE + m * BN, ad + (uint64_t)(m * (A_BYTES >> 4) + 2 * (x * KS + k)),
-                                        bd + (uint64_t)(2 * (x * KS + k)), ID, e || k ? 1u : 0u);
-                        if (e == STEPS - 1) {
-                            commit(d_full + buf);
-                            buf ^= 1u;
-                            if (!buf) pd ^= 1u;
+                        for (int k = 0; k < KS; ++k) {
+                            const int at = x * KS + k;            // of the block's eight
+                            product(tm + buf * BN, ad + (uint64_t)((at >> 2) * (A_HALF >> 4) + (at & 3) * 2),
+                                    bd + (uint64_t)((at >> 2) * (C::B_HALF >> 4) + (at & 3) * 2), ID, k ? 1u : 0u);
                         }
+                        if (x == PER - 1) commit(empty + s, both);
+                        commit(d_full + buf, both);
+                        buf ^= 1u;
+                        if (!buf) pd ^= 1u;
                     }
-                    if (failed) break;
-                    commit(a_empty + sa);
-                    commit(b_empty + sb);
-                    if (++sa == SA) { sa = 0; pa ^= 1u; }
-                    if (++sb == SB) { sb = 0; pb ^= 1u; }
+                    if (++s == SR) { s = 0; ph ^= 1u; }
                 }
+                __syncwarp();
+                commit(drain, both);
             }
             // no product in flight and nobody reading when the tensor memory is
-            // given back: with the full cap, and for readers that may be in
-            // waits of their own before they say so
+            // given back: with the full cap, and for those that may be in waits of
+            // their own before they say so
             __syncwarp();
-            commit(drain);
-            if (!wait(drain, 0, bspx::kSpinCap)) failed = true;
-            bool done = false;
+            bool done = false, idle = false;
+            for (int k = 0; k < 4 && !idle; ++k) idle = wait(drain, 0, bspx::kSpinCap);
             for (int k = 0; k < 4 && !done; ++k) done = wait(read, 0, bspx::kSpinCap);
-            if (!done) failed = true;
+            if (!done || !idle) failed = true;
             tc_after();
             __syncwarp();
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "r"(C::TMEM) : "memory");
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM) : "memory");
         } else if (warp == 3) {
             // ---------------- codes and zero points, and scales: they depend
             // on no kernel before this one
-            const int64_t block = strip * units + (k_begin >> 1);  // of 128 columns
-            const int n = steps >> 1;
             int u = 0, sc = 0, ss = 0;
             uint32_t pc = 0, ps = 0;
-            for (; u < n; ++u) {
+            for (; u < blocks; ++u) {
                 if ((u >= SC && !wait(c_empty + sc, pc ^ 1u, cap)) || (u >= SS && !wait(s_empty + ss, ps ^ 1u, cap))) {
                     failed = true;
                     break;
                 }
                 if (lane == 0) {
-                    uint8_t *to = smem + C::OFF_C + sc * C::C_BYTES, *to_s = smem + C::OFF_S + ss * C::S_BYTES;
-                    uint32_t bytes = 0;
-#pragma unroll
-                    for (int m = 0; m < MS; ++m) bytes += 8192 + (a.w[m].zeros ? C::Z_BYTES : 0);
-                    bspx::mbar_arrive_expect_tx(c_full + sc, bytes);
+                    uint8_t* to = smem + C::OFF_C + sc * C::C_BYTES;
+                    bspx::mbar_arrive_expect_tx(c_full + sc, 8192 + (w.zeros ? C::Z_BYTES : 0));
+                    bspx::bulk_g2s(to, w.codes + (block0 + u) * 512, 8192, c_full + sc);
+                    if (w.zeros) bspx::bulk_g2s(to + 8192, w.zeros + (block0 + u) * C::Z_BYTES, C::Z_BYTES, c_full + sc);
                     bspx::mbar_arrive_expect_tx(s_full + ss, C::S_BYTES);
-#pragma unroll
-                    for (int m = 0; m < MS; ++m) {
-                        bspx::bulk_g2s(to + m * 8192, a.w[m].codes + (block + u) * 512, 8192, c_full + sc);
-                        if (a.w[m].zeros)
-                            bspx::bulk_g2s(to + MS * 8192 + m * C::Z_BYTES, a.w[m].zeros + (block + u) * C::Z_BYTES, C::Z_BYTES, c_full + sc);
-                        bspx::bulk_g2s(to_s + m * (C::S_BYTES / MS), a.w[m].scales + (block + u) * (C::S_BYTES / MS / 4),
-                                       C::S_BYTES / MS, s_full + ss);
-                    }
+                    bspx::bulk_g2s(smem + C::OFF_S + ss * C::S_BYTES, w.scales + (block0 + u) * (C::S_BYTES / 4), C::S_BYTES, s_full + ss);
                 }
                 __syncwarp();
                 if (++sc == SC) { sc = 0; pc ^= 1u; }
@@ -405,68 +407,56 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             for (int k = std::max(0, u - SS); k < u; ++k) bspx::mbar_wait_bounded(s_full + k % SS, (k / SS) & 1);
         }
         if (failed && lane == 0) atomicExch(a.err, (int)BSP_ERR_TIMEOUT);
-        if (ranks > 1) {
-            bspx::cluster_sync();
-            bspx::cluster_sync();
-        }
+        bspx::cluster_sync();
+        bspx::cluster_sync();
         return;
     }
 
     if (warp < 4 + C::DW) {
         take_registers<C::REGS, C::R_WIDEN>();
-        // ---------------- codes -> A.  Warp w takes row tiles w, w + DW, ...
-        // of the strips.  Lanes of odd rows store the upper half of their
-        // columns first, so that the eight lanes of a store's phase reach
-        // distinct banks.
-        const int w = warp - 4, g = lane >> 2, t = lane & 3;
-        constexpr int ZN = G == 32 ? 2 : 1;  // groups of a step
-        const bool odd = g & 1;
-        uint32_t from[C::TILES], zero[C::TILES], to[C::TILES];
-        bool has_zeros[C::TILES];
-#pragma unroll
-        for (int x = 0; x < C::TILES; ++x) {
-            const int rt = w + x * C::DW, m = rt / 8, r = rt % 8;
-            has_zeros[x] = (m ? a.w[1] : a.w[0]).zeros != nullptr;
-            from[x] = bspx::smem_u32(smem + C::OFF_C) + m * 8192 + r * 512 + lane * 16;
-            zero[x] = bspx::smem_u32(smem + C::OFF_C) + MS * 8192 + m * C::Z_BYTES + r * 8 + g;
-            to[x] = bspx::smem_u32(smem + C::OFF_A) + m * A_BYTES + r * 2048 + g * 128 + (((4 * (g & 1) + t) ^ g) << 4);
-        }
-        int sa = 0, sc = 0;
-        uint32_t pa = 0, pc = 0;
-        for (int u = 0; u < steps >> 1 && !failed; ++u) {
+        // ---------------- codes -> A.  Warp w takes row tiles w, w + DW of the
+        // strip.  Lanes of odd rows store the upper half of their columns
+        // first, so that the eight lanes of a store's phase reach distinct
+        // banks.
+        const int w0 = warp - 4, g = lane >> 2, t = lane & 3;
+        constexpr int ZN = G == 32 ? 4 : G == 64 ? 2 : 1;  // groups of a block
+        const bool odd = g & 1, has_zeros = w.zeros != nullptr;
+        const uint32_t from = bspx::smem_u32(smem + C::OFF_C) + w0 * 512 + lane * 16;
+        const uint32_t zero = bspx::smem_u32(smem + C::OFF_C) + 8192 + w0 * 8 + g;
+        const uint32_t to = bspx::smem_u32(smem) + w0 * 2048 + g * 128 + (((4 * (g & 1) + t) ^ g) << 4);
+        const uint32_t told = bspx::mapa_shared(bspx::smem_u32(full), lead);
+        int s = 0, sc = 0;
+        uint32_t ph = 0, pc = 0;
+        for (int u = 0; u < blocks; ++u) {
             if (!wait(c_full + sc, pc, cap)) {
                 failed = true;
                 break;
             }
-            uint4 v[2][C::TILES];
-            uint32_t z[2][C::TILES][ZN];
+            uint4 v[C::TILES][2];
+            uint32_t z[C::TILES][ZN];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int x = 0; x < C::TILES; ++x) {
 #pragma unroll
-                for (int x = 0; x < C::TILES; ++x) {
-                    v[e][x] = lds16(from[x] + sc * C::C_BYTES + e * 4096);
+                for (int e = 0; e < 2; ++e) v[x][e] = lds16(from + sc * C::C_BYTES + x * (C::DW * 512) + e * 4096);
 #pragma unroll
-                    for (int y = 0; y < ZN; ++y)
-                        z[e][x][y] = has_zeros[x] ? lds1(zero[x] + sc * C::C_BYTES + (e * BK / G + y) * 64) : 0x88u;
-                }
-            __syncwarp();
-            if (lane == 0) bspx::mbar_arrive(c_empty + sc);
-            if (++sc == SC) { sc = 0; pc ^= 1u; }
+                for (int y = 0; y < ZN; ++y)
+                    z[x][y] = has_zeros ? lds1(zero + sc * C::C_BYTES + x * (C::DW * 8) + y * 64) : 0x88u;
+            }
+            if (u >= SR && !wait(empty + s, ph ^ 1u, cap)) {
+                failed = true;
+                break;
+            }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (2 * u + e >= SA && !wait(a_empty + sa, pa ^ 1u, cap)) {
-                    failed = true;
-                    break;
-                }
+            for (int x = 0; x < C::TILES; ++x)
 #pragma unroll
-                for (int x = 0; x < C::TILES; ++x) {
-                    const uint4 q4 = v[e][x];
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 q4 = v[x][e];
                     const uint32_t c[2][2] = {{odd ? q4.z : q4.x, odd ? q4.w : q4.y}, {odd ? q4.x : q4.z, odd ? q4.y : q4.w}};
-                    const uint32_t at = to[x] + sa * (MS * A_BYTES);
+                    const uint32_t at = to + s * A_BYTES + e * A_HALF + x * (C::DW * 2048);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t z0, z1, p[4], q[4];
-                        Codes<T>::bias(ZN == 2 && (odd ? !h : h) ? z[e][x][ZN - 1] : z[e][x][0], z0, z1);
+                        Codes<T>::bias(ZN == 4 ? ((odd ? !h : h) ? z[x][(2 * e + 1) % ZN] : z[x][2 * e % ZN]) : z[x][e % ZN], z0, z1);
                         Codes<T>::widen(c[h][0], z0, z1, p);
                         Codes<T>::widen(c[h][1], z0, z1, q);
                         const uint32_t o = at ^ (h << 6);  // the other half: chunk ^ 4
@@ -474,17 +464,21 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                         sts16(o + 1024, p[1], p[3], q[1], q[3]);
                     }
                 }
-                bspx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) bspx::mbar_arrive(a_full + sa);
-                if (++sa == SA) { sa = 0; pa ^= 1u; }
+            bspx::fence_proxy_async_smem();
+            __syncwarp();
+            // the codes' slot is given back here, not where they were loaded: an
+            // arrival there went ahead of other lanes' loads (one block in some
+            // thousands held codes of a later one)
+            if (lane == 0) {
+                arrive_at(told + s * 8);
+                bspx::mbar_arrive(c_empty + sc);
             }
+            if (++s == SR) { s = 0; ph ^= 1u; }
+            if (++sc == SC) { sc = 0; pc ^= 1u; }
         }
         if (failed && lane == 0) atomicExch(a.err, (int)BSP_ERR_TIMEOUT);
-        if (ranks > 1) {
-            bspx::cluster_sync();
-            bspx::cluster_sync();
-        }
+        bspx::cluster_sync();
+        bspx::cluster_sync();
         return;
     }
 
@@ -493,113 +487,114 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         // ---------------- sums of groups, scaled, into registers
         const int p = warp - 4 - C::DW, quad = warp & 3, row = 32 * quad + lane, c0 = (p >> 2) * C::COLS;
         const uint32_t scales = bspx::smem_u32(smem + C::OFF_S) + (row / 16 * 8 + row % 8) * 4 + (row >> 3 & 1) * 2;
+        const uint32_t told = bspx::mapa_shared(bspx::smem_u32(d_empty), lead);
         const float upper = row & 8 ? 1.f / Codes<T>::UPPER : 1.f;
         constexpr int PER = 128 / G;  // groups of a block
-        uint64_t sum[MS][C::COLS / 2];
+        float sum[C::COLS];
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-            for (int i = 0; i < C::COLS / 2; ++i) sum[m][i] = 0;
+        for (int i = 0; i < C::COLS; ++i) sum[i] = 0.f;
         const uint32_t at = tmem + ((uint32_t)(32 * quad) << 16) + c0;
-        int ss = 0, gi = 0;
-        uint32_t ps = 0;
-        for (int u = 0; u < steps >> 1 && !failed; ++u) {
+        int ss = 0;
+        uint32_t ps = 0, buf = 0, pd = 0;
+        for (int u = 0; u < blocks && !failed; ++u) {
             if (!wait(s_full + ss, ps, cap)) {
                 failed = true;
                 break;
             }
-            float s[PER][MS];
+            float f[PER];
 #pragma unroll
-            for (int y = 0; y < PER; ++y)
+            for (int y = 0; y < PER; ++y) f[y] = half_of<T>(lds2(scales + ss * C::S_BYTES + y * 256), 0) * upper;
 #pragma unroll
-                for (int m = 0; m < MS; ++m)
-                    s[y][m] = half_of<T>(lds2(scales + ss * C::S_BYTES + (m * PER + y) * 256), 0) * upper;
-            __syncwarp();
-            if (lane == 0) bspx::mbar_arrive(s_empty + ss);
-            if (++ss == SS) { ss = 0; ps ^= 1u; }
-#pragma unroll
-            for (int y = 0; y < PER; ++y, ++gi) {
-                if (!wait(d_full + (gi & 1), (gi >> 1) & 1, cap)) {
+            for (int y = 0; y < PER; ++y) {
+                if (!wait(d_full + buf, pd, cap)) {
                     failed = true;
                     break;
                 }
                 tc_after();
 #pragma unroll
-                for (int m = 0; m < MS; ++m) {
-                    const uint64_t f = pair(s[y][m], s[y][m]);
+                for (int c = 0; c < C::COLS; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld32(at + buf * BN + c, r);
+                    tmem_wait(r);
 #pragma unroll
-                    for (int c = 0; c < C::COLS; c += 32) {
-                        uint32_t r[32];
-                        tmem_ld32(at + (gi & 1) * C::SIZE + m * BN + c, r);
-                        tmem_wait(r);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            sum[m][c / 2 + i] = fma2(f, pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), sum[m][c / 2 + i]);
-                    }
+                    for (int i = 0; i < 32; ++i) sum[c + i] = fmaf(f[y], __uint_as_float(r[i]), sum[c + i]);
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bspx::mbar_arrive(d_empty + (gi & 1));
+                if (lane == 0) arrive_at(told + buf * 8);
+                buf ^= 1u;
+                if (!buf) pd ^= 1u;
             }
+            if (lane == 0) bspx::mbar_arrive(s_empty + ss);  // (every lane has used its scales: see the codes)
+            if (++ss == SS) { ss = 0; ps ^= 1u; }
         }
         tc_before();
         __syncwarp();
         if (lane == 0) bspx::mbar_arrive(read);
-        // ---------------- the sums to shared memory, [strip][column][row],
-        // over the rings: every product is done, and every promoting warp
-        // has its last scales
+        // ---------------- the sums to shared memory, [column][row], over the
+        // rings: every product is done, and every promoting warp has its last
+        // scales
         asm volatile("bar.sync 1, %0;" ::"n"(C::PW * 32) : "memory");
         float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int m = 0; m < MS; ++m)
-#pragma unroll
-            for (int i = 0; i < C::COLS / 2; ++i) {
-                float v[2];
-                unpair(sum[m][i], v[0], v[1]);
-                part[(m * BN + c0 + 2 * i) * BM + row] = v[0];
-                part[(m * BN + c0 + 2 * i + 1) * BM + row] = v[1];
-            }
-        if (ranks > 1) bspx::cluster_sync();
-        else asm volatile("bar.sync 1, %0;" ::"n"(C::PW * 32) : "memory");
+        for (int i = 0; i < C::COLS; ++i) part[(c0 + i) * BM + row] = sum[i];
+        bspx::cluster_sync();
         wait_prior_grids();  // Y may still be read by the kernels before this one
-        // a warp a column: four rows a lane
-        const int first = BN * rank / ranks, last = (int)min((int64_t)(BN * (rank + 1) / ranks), a.N - n0);
+        // a warp four columns at a time (another CTA's sums take some 1000 cycles
+        // to come), four rows a lane.  Rows of one strip: its CTAs share its
+        // columns.  Gated: all CTAs do.
+        const int of = GATED ? ranks : shares, mine = GATED ? rank : share;
+        const int from_col = BN * mine / of, to_col = (int)min((int64_t)(BN * (mine + 1) / of), a.N - n0);
         const int64_t m0 = strip * BM + 4 * lane;
         const bool whole = m0 + 4 <= a.M && a.y_stride % 4 == 0;
-#pragma unroll 1
-        for (int c = first + p; c < last && !failed; c += C::PW) {
-            float4 v[MS];
+        auto total = [&](uint32_t side, int c0, float4 (&v)[4]) {  // of columns c0, c0 + PW, ...
 #pragma unroll
-            for (int m = 0; m < MS; ++m) {
-                const uint32_t from = bspx::smem_u32(part + (m * BN + c) * BM + 4 * lane);
-                v[m] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (uint32_t k = 0; k < ranks; ++k) {
-                    float4 x;
+            for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t k = 0; k < shares; ++k) {
+                const uint32_t from = bspx::mapa_shared(bspx::smem_u32(part + c0 * BM + 4 * lane), 2 * k + side);
+                float4 x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
                     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                                 : "r"(ranks > 1 ? bspx::mapa_shared(from, k) : from)
+                                 : "=f"(x[j].x), "=f"(x[j].y), "=f"(x[j].z), "=f"(x[j].w)
+                                 : "r"(from + (c0 + j * C::PW < to_col ? j * C::PW * BM * 4 : 0))
                                  : "memory");
-                    v[m].x += x.x;
-                    v[m].y += x.y;
-                    v[m].z += x.z;
-                    v[m].w += x.w;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[j].x += x[j].x;
+                    v[j].y += x[j].y;
+                    v[j].z += x[j].z;
+                    v[j].w += x[j].w;
                 }
             }
-            if (MS == 2) {
-                v[0].x = activate(v[0].x, a.act) * v[MS - 1].x;
-                v[0].y = activate(v[0].y, a.act) * v[MS - 1].y;
-                v[0].z = activate(v[0].z, a.act) * v[MS - 1].z;
-                v[0].w = activate(v[0].w, a.act) * v[MS - 1].w;
-            }
-            T* y = reinterpret_cast<T*>(a.y) + (n0 + c) * a.y_stride + m0;
-            alignas(8) const T o[4] = {from_float<T>(v[0].x), from_float<T>(v[0].y), from_float<T>(v[0].z), from_float<T>(v[0].w)};
-            if (whole) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
-            else
+        };
+#pragma unroll 1
+        for (int c = from_col + p; c < to_col && !failed; c += 4 * C::PW) {
+            float4 v[4], u[4];
+            total(GATED ? 0 : half, c, v);
+            if (GATED) total(1, c, u);
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const int n = c + j * C::PW;
+                if (n >= to_col) break;
+                float4 z = v[0];
+                if (GATED) z = make_float4(activate(z.x, a.act) * u[0].x, activate(z.y, a.act) * u[0].y, activate(z.z, a.act) * u[0].z,
+                                           activate(z.w, a.act) * u[0].w);
+                T* y = reinterpret_cast<T*>(a.y) + (n0 + n) * a.y_stride + m0;
+                alignas(8) const T o[4] = {from_float<T>(z.x), from_float<T>(z.y), from_float<T>(z.z), from_float<T>(z.w)};
+                if (whole) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
+                else
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (m0 + e < a.M) y[e] = o[e];
+                    for (int e = 0; e < 4; ++e)
+                        if (m0 + e < a.M) y[e] = o[e];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {  // the next one
+                    v[i] = v[i + 1];
+                    if (GATED) u[i] = u[i + 1];
+                }
+            }
         }
-        if (ranks > 1) bspx::cluster_sync();  // others may still read this CTA's sums
+        bspx::cluster_sync();  // others may still read this CTA's sums
     }
     if (failed && lane == 0) atomicExch(a.err, (int)BSP_ERR_TIMEOUT);
 }
@@ -618,13 +613,13 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-template <class T, int G, int BN, int MS>
-bsp_status_t launch_wide(const Problem& p, int ranks, cudaStream_t s)
+template <class T, int G, int BN, bool GATED>
+bsp_status_t launch_wide(const Problem& p, int shares, cudaStream_t s)
 {
-    using C = Wide<G, BN, MS>;
+    using C = Wide<G, BN>;
     static bsp_attr_once attr_once;
     if (!attr_once.run(p.device, [] {
-            return cudaFuncSetAttribute(q4_wide_kernel<T, G, BN, MS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+            return cudaFuncSetAttribute(q4_wide_kernel<T, G, BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         }))
         return BSP_ERR_CUDA;
     const auto encode = encode_fn();
@@ -632,7 +627,7 @@ bsp_status_t launch_wide(const Problem& p, int ranks, cudaStream_t s)
     CUtensorMap map;
     const cuuint64_t dims[2] = {(cuuint64_t)p.K, (cuuint64_t)p.N};
     const cuuint64_t strides[1] = {(cuuint64_t)p.x_stride * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)BN};
+    const cuuint32_t box[2] = {64, BN / 2};
     const cuuint32_t estr[2] = {1, 1};
     if (encode(&map, std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                const_cast<void*>(p.x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -644,7 +639,8 @@ bsp_status_t launch_wide(const Problem& p, int ranks, cudaStream_t s)
     a.act = p.act;
     a.M = p.M;
     a.N = p.N;
-    a.groups = p.k_tiles * BK / G;
+    a.groups = p.k_tiles * 64 / G;
+    a.strips = p.strips;
     a.k_tiles = (int32_t)p.k_tiles;
     a.ntiles = (int32_t)((p.N + BN - 1) / BN);
     a.y = p.y;
@@ -652,7 +648,7 @@ bsp_status_t launch_wide(const Problem& p, int ranks, cudaStream_t s)
     a.err = p.err;
     a.spin_cap = bsp_spin_cap();
     a.stall = bsp_test_stall() != 0;
-    const int64_t ctas = (p.M + BM - 1) / BM * a.ntiles * ranks;
+    const int64_t ctas = (GATED ? p.strips : (p.strips + 1) / 2) * a.ntiles * 2 * shares;
     if (ctas > INT32_MAX) return BSP_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -663,48 +659,37 @@ bsp_status_t launch_wide(const Problem& p, int ranks, cudaStream_t s)
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = ranks;
+    at[1].val.clusterDim.x = 2 * shares;
     at[1].val.clusterDim.y = 1;
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, q4_wide_kernel<T, G, BN, MS>, map, a) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
-}
-
-// CTAs of a cluster that share a tile's columns: while the tiles leave half
-// of the GPU's places idle and each keeps four blocks of 128 columns.
-inline int split_of(const Problem& p, int64_t tiles, int ctas_an_sm)
-{
-    int r = 1;
-    while (r < 8 && tiles * r * 2 <= (int64_t)p.num_sms * ctas_an_sm && p.k_tiles / 2 >= 4 * 2 * r) r *= 2;
-    return r;
+    return cudaLaunchKernelEx(&cfg, q4_wide_kernel<T, G, BN, GATED>, map, a) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
 template <class T, int G>
 bsp_status_t wide_by_shape(const Problem& p, cudaStream_t s)
 {
-    const int64_t strips = (p.M + BM - 1) / BM;
-    auto go = [&](auto bn, auto ms) {
-        constexpr int BN = decltype(bn)::value, MS = decltype(ms)::value;
-        const int64_t tiles = strips * ((p.N + BN - 1) / BN);
-        return launch_wide<T, G, BN, MS>(p, split_of(p, tiles, Wide<G, BN, MS>::CTAS), s);
+    const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2;
+    auto go = [&](auto bn) {
+        constexpr int BN = decltype(bn)::value;
+        const int64_t tiles = pairs * ((p.N + BN - 1) / BN), places = (int64_t)p.num_sms / 2 * Wide<G, BN>::CTAS;
+        // pairs that share a tile's columns: while the tiles leave half of the
+        // GPU's places idle and each keeps four blocks
+        int shares = 1;
+        while (shares < 4 && tiles * shares * 2 <= places && p.k_tiles / 2 >= 4 * 2 * shares) shares *= 2;
+        return p.gated ? launch_wide<T, G, BN, true>(p, shares, s) : launch_wide<T, G, BN, false>(p, shares, s);
     };
     using std::integral_constant;
-    if (p.gated) {
-        if (p.N <= 32) return go(integral_constant<int, 32>(), integral_constant<int, 2>());
-        if (p.N <= 64) return go(integral_constant<int, 64>(), integral_constant<int, 2>());
-        return go(integral_constant<int, 128>(), integral_constant<int, 2>());
-    }
-    if (p.N <= 32) return go(integral_constant<int, 32>(), integral_constant<int, 1>());
-    if (p.N <= 64) return go(integral_constant<int, 64>(), integral_constant<int, 1>());
-    if (p.N <= 128) return go(integral_constant<int, 128>(), integral_constant<int, 1>());
-    return go(integral_constant<int, 256>(), integral_constant<int, 1>());
+    if (p.N <= 32) return go(integral_constant<int, 32>());
+    if (p.N <= 64) return go(integral_constant<int, 64>());
+    if (p.N <= 128) return go(integral_constant<int, 128>());
+    return go(integral_constant<int, 256>());
 }
 
 template <class T>
 bsp_status_t run_wide(const Problem& p, cudaStream_t s)
 {
-    if (p.K > INT32_MAX || p.N > INT32_MAX) return BSP_ERR_SHAPE;
     switch (p.group) {
     case 32: return wide_by_shape<T, 32>(p, s);
     case 64: return wide_by_shape<T, 64>(p, s);
