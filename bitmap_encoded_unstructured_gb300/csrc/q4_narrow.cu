@@ -2,9 +2,8 @@
 // gated form over two weights, on mma.sync.
 //
 // A warp takes RT row tiles (16 rows of W each) and a share of the columns;
-// codes, scales and activations run through a ring of its own in shared
-// memory (cp.async: every lane reads back its own codes and activations, so
-// no barrier but the warp's).  Codes less zero points are small integers,
+// codes and scales run through a ring of its own in shared memory (cp.async:
+// every lane reads back its own codes, so no barrier but the warp's).  Codes less zero points are small integers,
 // exact in either type; they are multiplied as they are and the group's scale
 // is applied to its fp32 sums, so no weight is rounded:
 //   Y[n][m] += s sum_k (c - z) x
@@ -15,18 +14,19 @@
 //   (A masked nibble alone, a subnormal, needs no subtraction, but tensor
 //   cores align subnormals as if they had the smallest normal exponent: the sums
 //   lose ten bits.)
-// The 8 warps of a CTA split the columns, and C CTAs of a cluster split them
+// The warps of a CTA split the columns, and C CTAs of a cluster split them
 // further where the row tiles alone do not fill the GPU; all parts are added in
 // a fixed order.
 #include "bsp_q4.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace {
 
 using namespace bspq4;
 
-constexpr int WARPS = 8, THREADS = WARPS * 32;
+constexpr int WARPS = 4, THREADS = WARPS * 32;
 
 struct NarrowArgs {
     Q4View w[2];
@@ -39,23 +39,25 @@ struct NarrowArgs {
     int64_t y_stride;
 };
 
-template <int RT, int NT>
-struct Slot {  // of a warp and a stage of 64 columns
-    static constexpr int X = RT * 512, S = X + NT * 1024, Z = S + RT * 64, BYTES = Z + RT * 16;
-};
-
-template <int RT, int NT>
+// A warp's ring: blocks of 128 columns of RT row tiles, with the scales and
+// zero points of their groups.
+template <int G, int RT, int NT>
 struct Ring {
-    static constexpr int DEPTH = RT * NT == 2 ? 6 : 3;
-    static constexpr int BYTES = WARPS * DEPTH * Slot<RT, NT>::BYTES;
-    static_assert(BYTES >= WARPS * RT * 8 * NT * 17 * 4 + RT * 8 * NT * 16 * 4, "parts of the warps and their sum");
+    static constexpr int PER = 128 / G;  // groups of a block
+    static constexpr int S = RT * 1024, Z = S + PER * RT * 32;
+    static constexpr int BYTES = (Z + PER * RT * 8 + 15) / 16 * 16;
+    static constexpr int DEPTH = RT == 2 ? 6 : 4, ALL = WARPS * DEPTH * BYTES;
+    static constexpr int CTAS = RT == 2 ? 4 : 3;  // an SM
+    static_assert(ALL >= WARPS * RT * 8 * NT * 17 * 4 + RT * 8 * NT * 16 * 4, "parts of the warps and their sum");
+    static_assert(CTAS * (ALL + 1024) <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes)
+template <int TO, int FROM>
+__device__ __forceinline__ void cp16(uint32_t dst, const char* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src), "n"(TO), "n"(FROM) : "memory");
 }
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src)
+__device__ __forceinline__ void cp8(uint32_t dst, const char* src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -82,34 +84,30 @@ __device__ __forceinline__ uint32_t lds1(uint32_t at)
     return v;
 }
 
-template <class T>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// c += a b, or a b (FIRST).
+template <class T, bool FIRST>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <>
-__device__ __forceinline__ void mma<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    const float z0 = FIRST ? 0.f : c[0], z1 = FIRST ? 0.f : c[1], z2 = FIRST ? 0.f : c[2], z3 = FIRST ? 0.f : c[3];
+    if constexpr (std::is_same<T, __half>::value)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
 }
 
 template <class T, int G, int NT, int RT, bool GATED>
-__global__ void __launch_bounds__(THREADS, 2) q4_narrow_kernel(const NarrowArgs a)
+__global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kernel(const __grid_constant__ NarrowArgs a)
 {
-    using L = Slot<RT, NT>;
-    using R = Ring<RT, NT>;
-    constexpr int D = R::DEPTH;
+    using R = Ring<G, RT, NT>;
+    constexpr int D = R::DEPTH, PER = R::PER;
     constexpr int TILES = GATED ? RT / 2 : RT;  // row tiles of Y
     constexpr int COLS = 8 * NT;
-    constexpr int PER = 64 / G ? 64 / G : 1;    // groups of a stage (G = 128: one of two stages)
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     uint32_t C, crank;
@@ -118,143 +116,159 @@ __global__ void __launch_bounds__(THREADS, 2) q4_narrow_kernel(const NarrowArgs 
     const int64_t tile0 = (int64_t)(blockIdx.x / C) * TILES, strip = tile0 / 8;
     const int rt0 = (int)(tile0 % 8);  // TILES divides 8: one strip
     const int n0 = blockIdx.y * COLS, n_here = min(COLS, a.N - n0);
-    const uint32_t ring = bspx::smem_u32(smem) + warp * D * L::BYTES;
+    const uint32_t ring = bspx::smem_u32(smem) + warp * D * R::BYTES, ring_end = ring + D * R::BYTES;
 
-    // this warp's columns: whole blocks of 128
-    const int units = a.k_tiles >> 1, ranks = WARPS * C, rank = crank * WARPS + warp;
-    const int k_begin = 2 * (int)((int64_t)units * rank / ranks);
-    const int k_count = 2 * (int)((int64_t)units * (rank + 1) / ranks) - k_begin;
+    // this warp's blocks of 128 columns
+    const int blocks = a.k_tiles >> 1, ranks = WARPS * C, rank = crank * WARPS + warp;
+    const int first = (int)((int64_t)blocks * rank / ranks);
+    const int count = (int)((int64_t)blocks * (rank + 1) / ranks) - first;
 
-    auto of = [&](int r) { return GATED && r >= TILES ? a.w[1] : a.w[0]; };  // row tile r's weight
-    const uint4* codes[RT];
-    const uint8_t *meta = nullptr, *zero = nullptr;  // what this lane copies of the scales and zero points
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-        codes[r] = of(r).codes + (strip * a.k_tiles + k_begin) * 256 + (rt0 + r % TILES) * 32 + lane;
-    const int64_t group0 = strip * a.groups + (int64_t)k_begin * 64 / G;
-    constexpr int CHUNKS = PER * 2;  // 16-byte pieces of a row tile's scales in a stage
-    if (lane < RT * CHUNKS) {
-        const int r = lane / CHUNKS, c = lane % CHUNKS;
-        meta = reinterpret_cast<const uint8_t*>(of(r).scales + (group0 + c / 2) * 64 + (rt0 + r % TILES) * 8) + c % 2 * 16;
+    // what this lane copies of a block, at the next block to copy
+    const char *codes = nullptr, *codes_up = nullptr, *scales = nullptr, *zeros = nullptr;
+    auto codes_of = [&](const Q4View& v) {
+        return reinterpret_cast<const char*>(v.codes + (strip * a.k_tiles + 2 * first) * 256 + rt0 * 32 + lane);
+    };
+    codes = codes_of(a.w[0]);
+    if (GATED) codes_up = codes_of(a.w[1]);
+    const int64_t group0 = strip * a.groups + (int64_t)first * PER;
+    if (lane < PER * RT * 2) {  // scales [group][row tile]: 32 bytes, two lanes
+        const int p = lane / (RT * 2), r = lane / 2 % RT;
+        const Q4View& v = GATED && r >= TILES ? a.w[1] : a.w[0];
+        scales = reinterpret_cast<const char*>(v.scales + (group0 + p) * 64 + (rt0 + r % TILES) * 8) + lane % 2 * 16;
     }
-    if (lane < RT * PER) {
-        const int r = lane / PER;
-        const uint8_t* z = of(r).zeros;
-        if (z) zero = z + (group0 + lane % PER) * 64 + (rt0 + r % TILES) * 8;
+    if (lane < PER * RT) {  // zero points: 8 bytes
+        const int p = lane / RT, r = lane % RT;
+        const uint8_t* z = (GATED && r >= TILES ? a.w[1] : a.w[0]).zeros;
+        if (z) zeros = reinterpret_cast<const char*>(z + (group0 + p) * 64 + (rt0 + r % TILES) * 8);
     }
+    const bool any_zeros = a.w[0].zeros || (GATED && a.w[1].zeros);
     const bool has_zeros[2] = {a.w[0].zeros != nullptr, GATED && a.w[1].zeros != nullptr};
-    const char* xrow[NT];
-    bool live[NT];
+    // activations go from L2 to registers, a block ahead: this lane's eight
+    // columns of row 8 nt + g in each quarter of the block
+    const char* x[NT];
+    int left[NT];  // columns of the row behind this lane's first (none: the row is not there)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        live[i] = 8 * i + g < n_here;
-        xrow[i] = reinterpret_cast<const char*>(a.x) + (int64_t)(n0 + (live[i] ? 8 * i + g : 0)) * a.x_stride * 2;
+        const bool live = 8 * i + g < n_here;
+        x[i] = reinterpret_cast<const char*>(a.x) + ((int64_t)(n0 + (live ? 8 * i + g : 0)) * a.x_stride + (int64_t)first * 128 + 8 * t) * 2;
+        left[i] = live ? (int)(a.K - (int64_t)first * 128) - 8 * t : 0;
     }
-
-    auto copy_weights = [&](int i) {  // stage i of this warp
-        const uint32_t slot = ring + (uint32_t)(i % D) * L::BYTES;
-#pragma unroll
-        for (int r = 0; r < RT; ++r) cp16(slot + r * 512 + lane * 16, codes[r] + (int64_t)i * 256, 16);
-        if (G < 128 || !(i & 1)) {
-            const int64_t at = (int64_t)(G == 128 ? i >> 1 : i) * PER * 64;
-            if (lane < RT * CHUNKS) cp16(slot + L::S + lane / CHUNKS * 64 + lane % CHUNKS * 16, meta + at * 4, 16);
-            if (lane < RT * PER && zero) cp8(slot + L::Z + lane / PER * 16 + lane % PER * 8, zero + at);
-        }
+    uint4 b[NT][4];
+    auto load_x = [&](int nt, int q) {
+        b[nt][q] = make_uint4(0u, 0u, 0u, 0u);
+        if (left[nt] > 32 * q) b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q));  // (K is a multiple of 8)
     };
-    auto copy_x = [&](int i) {
-        const uint32_t slot = ring + (uint32_t)(i % D) * L::BYTES + L::X;
+
+    auto copy_weights = [&](uint32_t slot) {
+        const uint32_t to = slot + lane * 16;
+        auto tile = [&](auto r) {
+            constexpr int Q = decltype(r)::value;
+            if constexpr (Q < RT) {
+                cp16<Q * 512, Q % TILES * 512>(to, GATED && Q >= TILES ? codes_up : codes);
+                cp16<RT * 512 + Q * 512, 4096 + Q % TILES * 512>(to, GATED && Q >= TILES ? codes_up : codes);
+            }
+        };
+        tile(std::integral_constant<int, 0>());
+        tile(std::integral_constant<int, 1>());
+        tile(std::integral_constant<int, 2>());
+        tile(std::integral_constant<int, 3>());
+        if (lane < PER * RT * 2) cp16<R::S, 0>(to, scales);
+        if (any_zeros && zeros) cp8(slot + R::Z + lane * 8, zeros);
+        codes += 8192;
+        if (GATED) codes_up += 8192;
+        scales += PER * 256;
+        if (any_zeros && zeros) zeros += PER * 64;
+    };
+    // weights do not depend on the kernels before this one
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) {
+        if (i < count) copy_weights(ring + i * R::BYTES);
+        cp_commit();
+    }
+    launch_dependents();
+    wait_prior_grids();
+    if (count > 0)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t k = (int64_t)(k_begin + i) * 64 + 32 * h + 8 * t;  // K is a multiple of 8
-                if (live[nt]) cp16(slot + (2 * nt + h) * 512 + lane * 16, xrow[nt] + (k < a.K ? k * 2 : 0), k < a.K ? 16 : 0);
-            }
-    };
+            for (int q = 0; q < 4; ++q) load_x(nt, q);
 
-    // weights do not depend on the kernels before this one
-#pragma unroll
-    for (int i = 0; i < D - 1; ++i)
-        if (i < k_count) copy_weights(i);
-    launch_dependents();
-    wait_prior_grids();
-#pragma unroll
-    for (int i = 0; i < D - 1; ++i) {
-        if (i < k_count) copy_x(i);
-        cp_commit();
-    }
-
-    float out[RT][NT][4], acc[RT][NT][4];
+    float out[RT][NT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[r][nt][e] = acc[r][nt][e] = 0.f;
-    uint32_t scale[RT], z0[RT], z1[RT];
+            for (int e = 0; e < 4; ++e) out[r][nt][e] = 0.f;
 
-    auto load_scales = [&](uint32_t slot, int part) {
+    uint32_t slot = ring, to_slot = ring + (D - 1) * R::BYTES;  // to read, to fill
+    for (int i = 0; i < count; ++i) {
+        cp_wait<D - 2>();
+        __syncwarp();  // every lane's copies of this block are there, and the slot of the last one is free
+        if (i + D - 1 < count) copy_weights(to_slot);
+        cp_commit();
+        // the next block's activations take the place of this one's as they are used
+        const bool more = i + 1 < count;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            scale[r] = lds4(slot + L::S + r * 64 + part * 32 + g * 4);
-            Codes<T>::bias(has_zeros[GATED ? r / TILES : 0] ? lds1(slot + L::Z + r * 16 + part * 8 + g) : 0x88u, z0[r],
-                           z1[r]);
+        for (int nt = 0; nt < NT; ++nt) {
+            x[nt] += 256;
+            left[nt] = more ? left[nt] - 128 : 0;
         }
-    };
-    auto flush = [&]() {  // the group's sums, scaled, into out
+        to_slot += R::BYTES;
+        if (to_slot == ring_end) to_slot = ring;
+        float acc[RT][NT][4];
+        float s0[RT], s1[RT];
+        uint32_t z0[RT], z1[RT];
+        auto load_scales = [&](int p) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const float s0 = half_of<T>(scale[r], 0), s1 = half_of<T>(scale[r], 1) * (1.f / Codes<T>::UPPER);
+            for (int r = 0; r < RT; ++r) {
+                const uint32_t pair = lds4(slot + R::S + (p * RT + r) * 32 + g * 4);
+                s0[r] = half_of<T>(pair, 0);
+                s1[r] = half_of<T>(pair, 1) * (1.f / Codes<T>::UPPER);
+                Codes<T>::bias(has_zeros[GATED && r >= TILES] ? lds1(slot + R::Z + (p * RT + r) * 8 + g) : 0x88u, z0[r], z1[r]);
+            }
+        };
+        auto flush = [&]() {  // the group's sums, scaled, into out
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    out[r][nt][e] = fmaf(e < 2 ? s0 : s1, acc[r][nt][e], out[r][nt][e]);
-                    acc[r][nt][e] = 0.f;
-                }
-        }
-    };
-
-    for (int i0 = 0; i0 < k_count; i0 += 2) {
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) out[r][nt][e] = fmaf(e < 2 ? s0[r] : s1[r], acc[r][nt][e], out[r][nt][e]);
+        };
+        if (G == 128) load_scales(0);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int i = i0 + e;
-            cp_wait<D - 2>();
-            __syncwarp();  // every lane's copies of this stage are there, and its slot of the last one is free
-            if (i + D - 1 < k_count) {
-                copy_weights(i + D - 1);
-                copy_x(i + D - 1);
-            }
-            cp_commit();
-            const uint32_t slot = ring + (uint32_t)(i % D) * L::BYTES;
             uint4 w[RT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) w[r] = lds16(slot + r * 512 + lane * 16);
-            if (G == 64 || (G == 128 && e == 0)) load_scales(slot, 0);
+            for (int r = 0; r < RT; ++r) w[r] = lds16(slot + e * (RT * 512) + r * 512 + lane * 16);
+            if (G == 64) load_scales(e);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint4 x[NT];
+                if (G == 32) load_scales(2 * e + h);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    x[nt] = make_uint4(0u, 0u, 0u, 0u);
-                    if (live[nt]) x[nt] = lds16(slot + L::X + (2 * nt + h) * 512 + lane * 16);
-                }
-                if (G == 32) load_scales(slot, h);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int r = 0; r < RT; ++r) {
                         uint32_t av[4];
                         Codes<T>::widen(h ? (j ? w[r].w : w[r].z) : (j ? w[r].y : w[r].x), z0[r], z1[r], av);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma<T>(acc[r][nt], av, j ? x[nt].z : x[nt].x, j ? x[nt].w : x[nt].y);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4& q = b[nt][2 * e + h];
+                            const uint32_t b0 = j ? q.z : q.x, b1 = j ? q.w : q.y;
+                            if (j == 0 && (G == 32 || (h == 0 && (G == 64 || e == 0)))) mma<T, true>(acc[r][nt], av, b0, b1);
+                            else mma<T, false>(acc[r][nt], av, b0, b1);
+                        }
                     }
-                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) load_x(nt, 2 * e + h);
                 if (G == 32) flush();
             }
-            if (G == 64 || (G == 128 && e == 1)) flush();
+            if (G == 64) flush();
         }
+        if (G == 128) flush();
+        slot += R::BYTES;
+        if (slot == ring_end) slot = ring;
     }
 
     // ---- the warps' parts, then the cluster's, added in order
@@ -304,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 2) q4_narrow_kernel(const NarrowArgs 
 template <class T, int G, int NT, int RT, bool GATED>
 bsp_status_t launch(const Problem& p, cudaStream_t s)
 {
-    constexpr int SMEM = Ring<RT, NT>::BYTES;
+    constexpr int SMEM = Ring<G, RT, NT>::ALL;
     static bsp_attr_once attr_once;
     if (!attr_once.run(p.device, [] {
             return cudaFuncSetAttribute(q4_narrow_kernel<T, G, NT, RT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -326,10 +340,10 @@ bsp_status_t launch(const Problem& p, cudaStream_t s)
     a.y_stride = p.y_stride;
     constexpr int TILES = GATED ? RT / 2 : RT;
     const int64_t tiles = (p.M + 16 * TILES - 1) / (16 * TILES), blocks = (p.N + 8 * NT - 1) / (8 * NT);
-    // a cluster splits the columns until two CTAs an SM are there, or a warp
-    // has less than two blocks of columns
+    // a cluster splits the columns while its CTAs fit the GPU at once and a
+    // warp keeps two blocks of columns
     int c = 1;
-    while (c < 8 && tiles * blocks * c < 2 * p.num_sms && p.k_tiles / 2 >= 2 * WARPS * c * 2) c *= 2;
+    while (c < 8 && tiles * blocks * c * 2 <= (int64_t)Ring<G, RT, NT>::CTAS * p.num_sms && p.k_tiles / 2 >= 2 * WARPS * c * 2) c *= 2;
     if (tiles * c > INT32_MAX || blocks > 65535) return BSP_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * c), (unsigned)blocks);
