@@ -101,7 +101,10 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(z0), "f"(z1), "f"(z2), "f"(z3));
 }
 
-template <class T, int G, int NT, int RT, bool GATED>
+// What lanes of rows that are not there read as activations.
+__device__ const uint4 kNothing[16] = {};
+
+template <class T, int G, int NT, int RT, bool GATED, bool ZEROS>
 __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kernel(const __grid_constant__ NarrowArgs a)
 {
     using R = Ring<G, RT, NT>;
@@ -139,24 +142,28 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
     if (lane < PER * RT) {  // zero points: 8 bytes
         const int p = lane / RT, r = lane % RT;
         const uint8_t* z = (GATED && r >= TILES ? a.w[1] : a.w[0]).zeros;
-        if (z) zeros = reinterpret_cast<const char*>(z + (group0 + p) * 64 + (rt0 + r % TILES) * 8);
+        if (ZEROS && z) zeros = reinterpret_cast<const char*>(z + (group0 + p) * 64 + (rt0 + r % TILES) * 8);
     }
-    const bool any_zeros = a.w[0].zeros || (GATED && a.w[1].zeros);
     const bool has_zeros[2] = {a.w[0].zeros != nullptr, GATED && a.w[1].zeros != nullptr};
     // activations go from L2 to registers, a block ahead: this lane's eight
     // columns of row 8 nt + g in each quarter of the block
     const char* x[NT];
-    int left[NT];  // columns of the row behind this lane's first (none: the row is not there)
+    int step[NT];  // bytes between blocks; 0: the row is not there
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const bool live = 8 * i + g < n_here;
-        x[i] = reinterpret_cast<const char*>(a.x) + ((int64_t)(n0 + (live ? 8 * i + g : 0)) * a.x_stride + (int64_t)first * 128 + 8 * t) * 2;
-        left[i] = live ? (int)(a.K - (int64_t)first * 128) - 8 * t : 0;
+        step[i] = 8 * i + g < n_here ? 256 : 0;
+        x[i] = step[i] ? reinterpret_cast<const char*>(a.x) + ((int64_t)(n0 + 8 * i + g) * a.x_stride + (int64_t)first * 128 + 8 * t) * 2
+                       : reinterpret_cast<const char*>(kNothing) + t * 16;
     }
+    const int whole = (int)(a.K / 128) - first;       // blocks from here on that lie inside K
+    const int left = (int)(a.K % 128) - 8 * t;        // of the block behind them: columns from this lane's first on
     uint4 b[NT][4];
-    auto load_x = [&](int nt, int q) {
-        b[nt][q] = make_uint4(0u, 0u, 0u, 0u);
-        if (left[nt] > 32 * q) b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q));  // (K is a multiple of 8)
+    auto load_x = [&](int nt, int q, int i) {  // of block i
+        if (i < whole) b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q));
+        else {  // K, a multiple of 8, ends here
+            b[nt][q] = make_uint4(0u, 0u, 0u, 0u);
+            if (i == whole && left > 32 * q) b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q));
+        }
     };
 
     auto copy_weights = [&](uint32_t slot) {
@@ -173,11 +180,11 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
         tile(std::integral_constant<int, 2>());
         tile(std::integral_constant<int, 3>());
         if (lane < PER * RT * 2) cp16<R::S, 0>(to, scales);
-        if (any_zeros && zeros) cp8(slot + R::Z + lane * 8, zeros);
+        if (ZEROS && zeros) cp8(slot + R::Z + lane * 8, zeros);
         codes += 8192;
         if (GATED) codes_up += 8192;
         scales += PER * 256;
-        if (any_zeros && zeros) zeros += PER * 64;
+        if (ZEROS && zeros) zeros += PER * 64;
     };
     // weights do not depend on the kernels before this one
 #pragma unroll
@@ -191,7 +198,7 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) load_x(nt, q);
+            for (int q = 0; q < 4; ++q) load_x(nt, q, 0);
 
     float out[RT][NT][4];
 #pragma unroll
@@ -201,19 +208,17 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
 #pragma unroll
             for (int e = 0; e < 4; ++e) out[r][nt][e] = 0.f;
 
-    uint32_t slot = ring, to_slot = ring + (D - 1) * R::BYTES;  // to read, to fill
+    uint32_t slot = ring, to_slot = ring + (D - 1) * R::BYTES;  // to read; to fill: the one read last
     for (int i = 0; i < count; ++i) {
         cp_wait<D - 2>();
         __syncwarp();  // every lane's copies of this block are there, and the slot of the last one is free
         if (i + D - 1 < count) copy_weights(to_slot);
         cp_commit();
-        // the next block's activations take the place of this one's as they are used
-        const bool more = i + 1 < count;
+        // the next block's activations take the place of this one's as they are
+        // used (behind the last block: its own again)
+        const int next = min(i + 1, count - 1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            x[nt] += 256;
-            left[nt] = more ? left[nt] - 128 : 0;
-        }
+        for (int nt = 0; nt < NT; ++nt) x[nt] += i + 1 < count ? step[nt] : 0;
         to_slot += R::BYTES;
         if (to_slot == ring_end) to_slot = ring;
         float acc[RT][NT][4];
@@ -224,8 +229,8 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
             for (int r = 0; r < RT; ++r) {
                 const uint32_t pair = lds4(slot + R::S + (p * RT + r) * 32 + g * 4);
                 s0[r] = half_of<T>(pair, 0);
-                s1[r] = half_of<T>(pair, 1) * (1.f / Codes<T>::UPPER);
-                Codes<T>::bias(has_zeros[GATED && r >= TILES] ? lds1(slot + R::Z + (p * RT + r) * 8 + g) : 0x88u, z0[r], z1[r]);
+                s1[r] = half_of<T>(pair, 1);
+                Codes<T>::bias(ZEROS && has_zeros[GATED && r >= TILES] ? lds1(slot + R::Z + (p * RT + r) * 8 + g) : 0x88u, z0[r], z1[r]);
             }
         };
         auto flush = [&]() {  // the group's sums, scaled, into out
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
                         }
                     }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) load_x(nt, 2 * e + h);
+                for (int nt = 0; nt < NT; ++nt) load_x(nt, 2 * e + h, next);
                 if (G == 32) flush();
             }
             if (G == 64) flush();
@@ -282,7 +287,8 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                parts[((warp * RT + r) * COLS + 8 * nt + 2 * t + (e & 1)) * 17 + g + 8 * (e >> 1)] = out[r][nt][e];
+                parts[((warp * RT + r) * COLS + 8 * nt + 2 * t + (e & 1)) * 17 + g + 8 * (e >> 1)] =
+                    e < 2 ? out[r][nt][e] : out[r][nt][e] * (1.f / Codes<T>::UPPER);
     __syncthreads();
     for (int i = threadIdx.x; i < RT * COLS * 16; i += THREADS) {
         float v = 0.f;
@@ -315,13 +321,13 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
     if (C > 1) bspx::cluster_sync();  // others may still read this CTA's sums
 }
 
-template <class T, int G, int NT, int RT, bool GATED>
-bsp_status_t launch(const Problem& p, cudaStream_t s)
+template <class T, int G, int NT, int RT, bool GATED, bool ZEROS>
+bsp_status_t launch_as(const Problem& p, cudaStream_t s)
 {
     constexpr int SMEM = Ring<G, RT, NT>::ALL;
     static bsp_attr_once attr_once;
     if (!attr_once.run(p.device, [] {
-            return cudaFuncSetAttribute(q4_narrow_kernel<T, G, NT, RT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(q4_narrow_kernel<T, G, NT, RT, GATED, ZEROS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         SMEM);
         }))
         return BSP_ERR_CUDA;
@@ -359,7 +365,14 @@ bsp_status_t launch(const Problem& p, cudaStream_t s)
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, q4_narrow_kernel<T, G, NT, RT, GATED>, a) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, q4_narrow_kernel<T, G, NT, RT, GATED, ZEROS>, a) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+}
+
+template <class T, int G, int NT, int RT, bool GATED>
+bsp_status_t launch(const Problem& p, cudaStream_t s)
+{
+    return p.w.zeros || (GATED && p.up.zeros) ? launch_as<T, G, NT, RT, GATED, true>(p, s)
+                                              : launch_as<T, G, NT, RT, GATED, false>(p, s);
 }
 
 template <class T, int G>
