@@ -9,7 +9,7 @@
 //      (K-major, swizzled by 128 bytes: a lane's eight columns of a row are
 //      one 16-byte chunk)
 //   B  X by TMA, the same layout, half of the BN rows in each CTA
-//   D  sums of one group of columns, in tensor memory, two buffers; one
+//   D  sums of one group of columns, in tensor memory, two to eight buffers; one
 //      product (cta_group::2) works on both CTAs' rows
 // Scales are applied to D: the promoting warps read a group's sums while
 // the next group's products run, and add s D to fp32 sums in registers.  So no weight is rounded, whatever its scale; weights
@@ -48,27 +48,30 @@ constexpr int A_HALF = BM * 64 * 2, A_BYTES = 2 * A_HALF;  // 64 columns of a st
 // REGS of each at launch (their sum over warpgroups is the launch's).
 template <int G, int BN>
 struct Wide {
-    static constexpr int CTAS = BN <= 64 ? 2 : 1;         // an SM
-    static constexpr int DW = BN == 256 ? 4 : 8, PW = BN <= 64 ? 4 : 8;
+    static constexpr int DW = BN == 256 ? 4 : 8, PW = BN == 32 ? 4 : 8;
     static constexpr int WARPS = 4 + DW + PW, THREADS = 32 * WARPS;
-    static constexpr int REGS = BN == 256 ? 128 : BN == 128 ? 96 : 64;
-    static constexpr int R_CONTROL = 40;
-    static constexpr int R_WIDEN = BN == 256 ? 104 : BN == 128 ? 88 : BN == 64 ? 56 : 72;
-    static constexpr int R_PROMOTE = BN == 256 ? 184 : BN == 128 ? 128 : BN == 64 ? 104 : 72;
+    static constexpr int REGS = BN == 128 || BN == 64 ? 96 : 128;
+    static constexpr int R_CONTROL = BN >= 128 ? 40 : REGS;
+    static constexpr int R_WIDEN = BN == 256 ? 104 : BN == 128 ? 88 : REGS;
+    static constexpr int R_PROMOTE = BN == 256 ? 184 : BN == 128 ? 128 : REGS;
     static constexpr int TILES = 8 / DW;                  // row tiles of a widening warp
     static constexpr int COLS = BN / (PW / 4);            // columns of a promoting thread
     // rings: A with B, codes (with zero points), scales
-    static constexpr int SR = BN >= 128 ? 3 : 2, SC = BN == 256 ? 3 : BN == 128 ? 6 : BN == 64 ? 3 : 4, SS = BN <= 64 && G == 32 ? 4 : 8;
+    static constexpr int SR = BN >= 128 ? 3 : 4, SC = BN == 256 ? 3 : 6, SS = 8;
+    // a buffer of D holds the sums of H groups of a block, BN columns
+    // each; there are ND
+    static constexpr int PER = 128 / G, H = PER < 256 / BN ? PER : 256 / BN;
+    static constexpr int ND = 512 / (H * BN) < 8 ? 512 / (H * BN) : 8;
     static constexpr int B_HALF = BN / 2 * 64 * 2, B_BYTES = 2 * B_HALF;
     static constexpr int Z_BYTES = 128 / G * 64, C_BYTES = 8192 + Z_BYTES, S_BYTES = 128 / G * 256;
     static constexpr int OFF_B = SR * A_BYTES, OFF_C = OFF_B + SR * B_BYTES, OFF_S = OFF_C + SC * C_BYTES;
     static constexpr int OFF_BAR = OFF_S + SS * S_BYTES;
-    static constexpr int NBAR = 3 * SR + 2 * (SC + SS) + 4 + 2;
+    static constexpr int NBAR = 3 * SR + 2 * (SC + SS + ND) + 2;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
-    static constexpr uint32_t TMEM = 2 * BN;
-    static_assert(SMEM <= (CTAS == 2 ? 113 : 227) * 1024, "shared memory");
+    static constexpr uint32_t TMEM = ND * H * BN;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(OFF_S >= BN * BM * 4, "the sums, over the rings");
-    static_assert(CTAS == 2 || SMEM > 114 * 1024, "one CTA may take all of the tensor memory");
+    static_assert(SMEM > 114 * 1024, "one CTA an SM: it may take all of the tensor memory");
 };
 
 struct WideArgs {
@@ -211,12 +214,12 @@ __device__ __forceinline__ void arrive_at(uint32_t addr)
 }
 
 template <class T, int G, int BN, bool GATED>
-__global__ void __launch_bounds__(Wide<G, BN>::THREADS, Wide<G, BN>::CTAS)
+__global__ void __launch_bounds__(Wide<G, BN>::THREADS, 1)
 q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ WideArgs a)
 {
     using C = Wide<G, BN>;
     static_assert(4 * C::R_CONTROL + C::DW * C::R_WIDEN + C::PW * C::R_PROMOTE <= C::WARPS * C::REGS, "shares of the launch's registers");
-    constexpr int SR = C::SR, SC = C::SC, SS = C::SS;
+    constexpr int SR = C::SR, SC = C::SC, SS = C::SS, ND = C::ND, PER = C::PER, H = C::H;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (bspx::smem_u32(smem_raw) & 1023u)) & 1023u);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -244,8 +247,8 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     uint64_t* s_full = c_empty + SC;
     uint64_t* s_empty = s_full + SS;
     uint64_t* d_full = s_empty + SS;
-    uint64_t* d_empty = d_full + 2;                                   // in the first CTA
-    uint64_t* drain = d_empty + 2;
+    uint64_t* d_empty = d_full + ND;                                  // in the first CTA
+    uint64_t* drain = d_empty + ND;
     uint64_t* read = drain + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(read + 1);
 
@@ -271,7 +274,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             bspx::mbar_init(s_full + i, 1);
             bspx::mbar_init(s_empty + i, C::PW);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < ND; ++i) {
             bspx::mbar_init(d_full + i, 1);
             bspx::mbar_init(d_empty + i, 2 * C::PW);
         }
@@ -336,9 +339,9 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                 const uint32_t tm = __shfl_sync(FULL, tmem, 0), both = __shfl_sync(FULL, 3u << lead, 0);
                 const uint64_t a_desc = smem_desc(bspx::smem_u32(smem)), b_desc = smem_desc(bspx::smem_u32(smem + C::OFF_B));
                 constexpr uint32_t ID = idesc<T>(BN);
-                constexpr int PER = 128 / G, KS = G / 16;         // groups of a block, products of a group
+                constexpr int KS = G / 16;                        // products of a group
                 int s = 0;
-                // the next group's buffer is buf; its last sums have been read when
+                // the next groups' buffer is buf; its last sums have been read when
                 // phase pd of its barrier is over (a fresh barrier's phase 1 is)
                 uint32_t ph = 0, buf = 0, pd = 1;
                 for (int i = 0; i < n && !failed; ++i) {
@@ -349,21 +352,24 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                     const uint64_t ad = a_desc + (uint64_t)(s * (A_BYTES >> 4)), bd = b_desc + (uint64_t)(s * (C::B_BYTES >> 4));
 #pragma unroll
                     for (int x = 0; x < PER; ++x) {
-                        if (!wait(d_empty + buf, pd, cap)) {
-                            failed = true;
-                            break;
+                        if (x % H == 0) {
+                            if (!wait(d_empty + buf, pd, cap)) {
+                                failed = true;
+                                break;
+                            }
+                            tc_after();
                         }
-                        tc_after();
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             const int at = x * KS + k;            // of the block's eight
-                            product(tm + buf * BN, ad + (uint64_t)((at >> 2) * (A_HALF >> 4) + (at & 3) * 2),
+                            product(tm + (buf * H + x % H) * BN, ad + (uint64_t)((at >> 2) * (A_HALF >> 4) + (at & 3) * 2),
                                     bd + (uint64_t)((at >> 2) * (C::B_HALF >> 4) + (at & 3) * 2), ID, k ? 1u : 0u);
                         }
                         if (x == PER - 1) commit(empty + s, both);
-                        commit(d_full + buf, both);
-                        buf ^= 1u;
-                        if (!buf) pd ^= 1u;
+                        if (x % H == H - 1) {
+                            commit(d_full + buf, both);
+                            if (++buf == ND) { buf = 0; pd ^= 1u; }
+                        }
                     }
                     if (++s == SR) { s = 0; ph ^= 1u; }
                 }
@@ -489,7 +495,6 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         const uint32_t scales = bspx::smem_u32(smem + C::OFF_S) + (row / 16 * 8 + row % 8) * 4 + (row >> 3 & 1) * 2;
         const uint32_t told = bspx::mapa_shared(bspx::smem_u32(d_empty), lead);
         const float upper = row & 8 ? 1.f / Codes<T>::UPPER : 1.f;
-        constexpr int PER = 128 / G;  // groups of a block
         float sum[C::COLS];
 #pragma unroll
         for (int i = 0; i < C::COLS; ++i) sum[i] = 0.f;
@@ -506,24 +511,27 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             for (int y = 0; y < PER; ++y) f[y] = half_of<T>(lds2(scales + ss * C::S_BYTES + y * 256), 0) * upper;
 #pragma unroll
             for (int y = 0; y < PER; ++y) {
-                if (!wait(d_full + buf, pd, cap)) {
-                    failed = true;
-                    break;
+                if (y % H == 0) {
+                    if (!wait(d_full + buf, pd, cap)) {
+                        failed = true;
+                        break;
+                    }
+                    tc_after();
                 }
-                tc_after();
 #pragma unroll
                 for (int c = 0; c < C::COLS; c += 32) {
                     uint32_t r[32];
-                    tmem_ld32(at + buf * BN + c, r);
+                    tmem_ld32(at + (buf * H + y % H) * BN + c, r);
                     tmem_wait(r);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) sum[c + i] = fmaf(f[y], __uint_as_float(r[i]), sum[c + i]);
                 }
-                tc_before();
-                __syncwarp();
-                if (lane == 0) arrive_at(told + buf * 8);
-                buf ^= 1u;
-                if (!buf) pd ^= 1u;
+                if (y % H == H - 1) {
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(told + buf * 8);
+                    if (++buf == ND) { buf = 0; pd ^= 1u; }
+                }
             }
             if (lane == 0) bspx::mbar_arrive(s_empty + ss);  // (every lane has used its scales: see the codes)
             if (++ss == SS) { ss = 0; ps ^= 1u; }
@@ -673,7 +681,7 @@ bsp_status_t wide_by_shape(const Problem& p, cudaStream_t s)
     const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2;
     auto go = [&](auto bn) {
         constexpr int BN = decltype(bn)::value;
-        const int64_t tiles = pairs * ((p.N + BN - 1) / BN), places = (int64_t)p.num_sms / 2 * Wide<G, BN>::CTAS;
+        const int64_t tiles = pairs * ((p.N + BN - 1) / BN), places = p.num_sms / 2;
         // pairs that share a tile's columns: while the tiles leave half of the
         // GPU's places idle and each keeps four blocks
         int shares = 1;
