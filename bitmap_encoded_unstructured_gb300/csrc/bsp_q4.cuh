@@ -1,4 +1,4 @@
-// Internal declarations of the 4-bit weights (q4_weights.cu, q4_narrow.cu,
+// Internal declarations of the 4-bit weights (q4_weights.cu, q4_narrow.cuh,
 // q4_wide.cuh): the handle, its layout and the products' arguments.
 #pragma once
 
@@ -150,8 +150,11 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 
 }  // namespace bspq4
 
-// Few rows of X (q4_narrow.cu), and more (q4_wide.cuh, by type).
-constexpr int64_t BSP_Q4_NARROW_N = 16;
-bsp_status_t bsp_run_q4_narrow(const bspq4::Problem& p, cudaStream_t s);
+// Few rows of X (q4_narrow.cuh), and more (q4_wide.cuh), by type.  With 32
+// rows the narrow kernel takes 57 us for 28672 x 8192 and 36 for 20480 x 5120
+// where the wide one takes 79 and 46; with 33 it would read the codes twice.
+constexpr int64_t BSP_Q4_NARROW_N = 32;
+bsp_status_t bsp_run_q4_narrow_f16(const bspq4::Problem& p, cudaStream_t s);
+bsp_status_t bsp_run_q4_narrow_bf16(const bspq4::Problem& p, cudaStream_t s);
 bsp_status_t bsp_run_q4_wide_f16(const bspq4::Problem& p, cudaStream_t s);
 bsp_status_t bsp_run_q4_wide_bf16(const bspq4::Problem& p, cudaStream_t s);

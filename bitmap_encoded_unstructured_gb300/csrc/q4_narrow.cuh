@@ -1,4 +1,4 @@
-// Products of 4-bit weights with few activation rows (decoding), and the
+// Products of 4-bit weights with up to 32 activation rows (decoding), and the
 // gated form over two weights, on mma.sync.
 //
 // A warp takes RT row tiles (16 rows of W each) and a share of the columns;
@@ -17,6 +17,8 @@
 // The warps of a CTA split the columns, and C CTAs of a cluster split them
 // further where the row tiles alone do not fill the GPU; all parts are added in
 // a fixed order.
+#pragma once
+
 #include "bsp_q4.cuh"
 
 #include <algorithm>
@@ -47,7 +49,7 @@ struct Ring {
     static constexpr int S = RT * 1024, Z = S + PER * RT * 32;
     static constexpr int BYTES = (Z + PER * RT * 8 + 15) / 16 * 16;
     static constexpr int DEPTH = RT == 2 ? 6 : 4, ALL = WARPS * DEPTH * BYTES;
-    static constexpr int CTAS = RT == 2 ? 4 : 3;  // an SM
+    static constexpr int CTAS = RT == 2 && NT == 1 ? 4 : 3;  // an SM
     static_assert(ALL >= WARPS * RT * 8 * NT * 17 * 4 + RT * 8 * NT * 16 * 4, "parts of the warps and their sum");
     static_assert(CTAS * (ALL + 1024) <= 227 * 1024, "shared memory");
 };
@@ -346,11 +348,11 @@ bsp_status_t launch_as(const Problem& p, cudaStream_t s)
     a.y_stride = p.y_stride;
     constexpr int TILES = GATED ? RT / 2 : RT;
     const int64_t tiles = (p.M + 16 * TILES - 1) / (16 * TILES), blocks = (p.N + 8 * NT - 1) / (8 * NT);
-    // a cluster splits the columns while its CTAs fit the GPU at once and a
-    // warp keeps four blocks of columns (4864 x 4096, one row: 8.3 us in
+    // a cluster splits the columns as far as its CTAs fit the GPU at once and
+    // a warp keeps four blocks of columns (4864 x 4096, one row: 8.3 us in
     // clusters of four with two blocks a warp, 5.9 in pairs with four)
-    int c = 1;
-    while (c < 8 && tiles * blocks * c * 2 <= (int64_t)Ring<G, RT, NT>::CTAS * p.num_sms && p.k_tiles / 2 >= 4 * WARPS * c * 2) c *= 2;
+    const int64_t fit = (int64_t)Ring<G, RT, NT>::CTAS * p.num_sms / (tiles * blocks), keep = p.k_tiles / 2 / (4 * WARPS);
+    const int c = (int)std::max<int64_t>(1, std::min<int64_t>({8, fit, keep}));
     if (tiles * c > INT32_MAX || blocks > 65535) return BSP_ERR_SHAPE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * c), (unsigned)blocks);
@@ -380,9 +382,15 @@ template <class T, int G>
 bsp_status_t by_shape(const Problem& p, cudaStream_t s)
 {
     // activations are read once for every RT row tiles: two for up to 8
-    // columns, four for up to 16
-    if (p.gated) return p.N <= 8 ? launch<T, G, 1, 2, true>(p, s) : launch<T, G, 2, 4, true>(p, s);
-    return p.N <= 8 ? launch<T, G, 1, 2, false>(p, s) : launch<T, G, 2, 4, false>(p, s);
+    // columns, four for up to 16 (and two again for up to 32, whose sums and
+    // activations fill the registers)
+    auto go = [&](auto gated) {
+        constexpr bool GATED = decltype(gated)::value;
+        if (p.N <= 8) return launch<T, G, 1, 2, GATED>(p, s);
+        if (p.N <= 16) return launch<T, G, 2, 4, GATED>(p, s);
+        return launch<T, G, 4, 2, GATED>(p, s);
+    };
+    return p.gated ? go(std::true_type()) : go(std::false_type());
 }
 
 template <class T>
@@ -396,8 +404,3 @@ bsp_status_t by_group(const Problem& p, cudaStream_t s)
 }
 
 }  // namespace
-
-bsp_status_t bsp_run_q4_narrow(const Problem& p, cudaStream_t s)
-{
-    return p.dtype == BSP_FP16 ? by_group<__half>(p, s) : by_group<__nv_bfloat16>(p, s);
-}

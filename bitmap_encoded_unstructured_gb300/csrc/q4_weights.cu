@@ -340,8 +340,9 @@ bsp_status_t run(const bsp_q4* h, const bsp_q4* up, const void* X, int64_t x_str
     p.device = h->device;
     p.num_sms = h->num_sms;
     p.err = h->err;
-    if (N <= BSP_Q4_NARROW_N) return bsp_run_q4_narrow(p, s);
-    return p.dtype == BSP_FP16 ? bsp_run_q4_wide_f16(p, s) : bsp_run_q4_wide_bf16(p, s);
+    const bool f16 = p.dtype == BSP_FP16;
+    if (N <= BSP_Q4_NARROW_N) return f16 ? bsp_run_q4_narrow_f16(p, s) : bsp_run_q4_narrow_bf16(p, s);
+    return f16 ? bsp_run_q4_wide_f16(p, s) : bsp_run_q4_wide_bf16(p, s);
 }
 
 }  // namespace

@@ -675,24 +675,82 @@ bsp_status_t launch_wide(const Problem& p, int shares, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, q4_wide_kernel<T, G, BN, GATED>, map, a) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
+// Clusters of 2, 4, 6 and 8 CTAs, one CTA an SM, that fit the GPU at once.
+template <class T, int G>
+const int* clusters_at_once(int device, int num_sms)
+{
+    static std::mutex mu;
+    static int most[64][4];
+    if (device < 0 || device >= 64) return nullptr;
+    std::lock_guard<std::mutex> g(mu);
+    int* m = most[device];
+    if (!m[0]) {
+        auto* k = q4_wide_kernel<T, G, 256, false>;
+        using C = Wide<G, 256>;
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return nullptr;
+        for (int i = 3; i >= 0; --i) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(2 * (i + 1));
+            cfg.blockDim = dim3(C::THREADS);
+            cfg.dynamicSmemBytes = C::SMEM;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = 2 * (i + 1);
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess) return nullptr;
+            m[i] = std::max(1, std::min(n, num_sms / (2 * (i + 1))));
+        }
+    }
+    return m;
+}
+
+// The columns of Y a tile takes and the pairs that share its columns of W:
+// the least of waves x (blocks of a pair x a block's time + what a tile takes
+// at its ends), in tens of ns, measured one wave at a time on 19456 rows.
+struct Plan {
+    int bn, shares;
+};
+template <int G>
+Plan plan_of(const Problem& p, const int* clusters)
+{
+    constexpr int BN[4] = {32, 64, 128, 256};
+    constexpr int BLOCK[4] = {55, 57, G == 32 ? 86 : 61, G == 128 ? 70 : G == 64 ? 107 : 190}, ENDS[4] = {500, 600, 700, 960};
+    const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2, blocks = p.k_tiles / 2;
+    Plan best = {256, 1};
+    int64_t least = INT64_MAX;
+    for (int i = 0; i < 4; ++i)
+        for (int s = 1; s <= 4 && s <= blocks; ++s) {
+            const int64_t tiles = pairs * ((p.N + BN[i] - 1) / BN[i]), waves = (tiles + clusters[s - 1] - 1) / clusters[s - 1];
+            const int64_t cost = waves * ((blocks + s - 1) / s * BLOCK[i] + ENDS[i] + (s > 1 ? 100 : 0));
+            if (cost < least) {
+                least = cost;
+                best = {BN[i], s};
+            }
+        }
+    return best;
+}
+
 template <class T, int G>
 bsp_status_t wide_by_shape(const Problem& p, cudaStream_t s)
 {
-    const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2;
+    const int* clusters = clusters_at_once<T, G>(p.device, p.num_sms);
+    if (!clusters) return BSP_ERR_CUDA;
+    const Plan plan = plan_of<G>(p, clusters);
     auto go = [&](auto bn) {
         constexpr int BN = decltype(bn)::value;
-        const int64_t tiles = pairs * ((p.N + BN - 1) / BN), places = p.num_sms / 2;
-        // pairs that share a tile's columns: while the tiles leave half of the
-        // GPU's places idle and each keeps four blocks
-        int shares = 1;
-        while (shares < 4 && tiles * shares * 2 <= places && p.k_tiles / 2 >= 4 * 2 * shares) shares *= 2;
-        return p.gated ? launch_wide<T, G, BN, true>(p, shares, s) : launch_wide<T, G, BN, false>(p, shares, s);
+        return p.gated ? launch_wide<T, G, BN, true>(p, plan.shares, s) : launch_wide<T, G, BN, false>(p, plan.shares, s);
     };
     using std::integral_constant;
-    if (p.N <= 32) return go(integral_constant<int, 32>());
-    if (p.N <= 64) return go(integral_constant<int, 64>());
-    if (p.N <= 128) return go(integral_constant<int, 128>());
-    return go(integral_constant<int, 256>());
+    switch (plan.bn) {
+    case 32: return go(integral_constant<int, 32>());
+    case 64: return go(integral_constant<int, 64>());
+    case 128: return go(integral_constant<int, 128>());
+    default: return go(integral_constant<int, 256>());
+    }
 }
 
 template <class T>
