@@ -24,6 +24,7 @@ from __future__ import annotations
 import contextlib
 import ctypes as C
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -1075,6 +1076,9 @@ class Int4Matrix:
         return Y
 
 
+_ROPE_ROWS = struct.Struct("@PPi4xqqqq").pack  # bsp_rope_rows_t
+
+
 class Rotary:
     """Rotary positions for heads of ``dim`` values, of which the first
     ``rot`` (all by default) turn, in pairs (i, i + rot / 2) or, if
@@ -1152,22 +1156,23 @@ class Rotary:
             pass
 
     def _of(self, name, x, out, rows, dtype):
-        """(the C description of x and its output, the output)"""
+        """(the C description of x and its output, as bytes: a Structure costs as much as a launch; the output)"""
         shape = x.shape
         if len(shape) != 3 or shape[0] != rows or shape[2] != self.dim or x.dtype is not dtype \
                 or x.get_device() != self._index:
             raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, q and k of one type")
         xr, xh, xd = x.stride()
+        heads = shape[1]
         if out is None:
             out = self._empty(shape, dtype=dtype, device=self.device)
-            orow, oh, od = shape[1] * self.dim, self.dim, 1
+            orow, oh, od = heads * self.dim, self.dim, 1
         else:
             if out.shape != shape or out.dtype is not dtype or out.get_device() != self._index:
                 raise ValueError(f"the output of {name} must have its shape and type, beside it")
             orow, oh, od = out.stride()
         if xd != 1 or od != 1:
             raise ValueError(f"{name} and its output must have contiguous values")
-        return bsp_rope_rows_t(x.data_ptr(), out.data_ptr(), shape[1], xr, xh, orow, oh), out
+        return _ROPE_ROWS(x.data_ptr(), out.data_ptr(), heads, xr, xh, orow, oh), out
 
     def apply(self, q, k, positions, out=None, inverse: bool = False, stream=None):
         """Turn rows ``q`` [rows][heads][dim] and ``k`` [rows][kv heads][dim]
@@ -1194,7 +1199,7 @@ class Rotary:
         cq, out_q = self._of("q", q, out_q, rows, dtype)
         if k is not None:
             ck, out_k = self._of("k", k, out_k, rows, dtype)
-        st = self._apply(self.h, C.addressof(cq), C.addressof(ck) if k is not None else None, dt, rows,
+        st = self._apply(self.h, cq, ck if k is not None else None, dt, rows,
                          positions.data_ptr(), apart, int(inverse), self._on(stream))
         if st:
             raise BspError("bsp_rope_apply", st)

@@ -160,13 +160,12 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
     const int whole = (int)(a.K / 128) - first;       // blocks from here on that lie inside K
     const int left = (int)(a.K % 128) - 8 * t;        // of the block behind them: columns from this lane's first on
     uint4 b[NT][4];
-    auto load_x = [&](int nt, int q, int i) {  // of block i
-        if (i < whole) b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q));
-        else {  // K, a multiple of 8, ends here
-            b[nt][q] = make_uint4(0u, 0u, 0u, 0u);
-            if (i == whole && left > 32 * q) b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q));
-        }
+    auto load_x = [&](int nt, int q) { b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q)); };
+    auto load_last_x = [&](int nt, int q) {  // of a block in which K, a multiple of 8, ends
+        b[nt][q] = make_uint4(0u, 0u, 0u, 0u);
+        if (left > 32 * q) load_x(nt, q);
     };
+    const int full = min(count, whole);  // blocks inside K
 
     auto copy_weights = [&](uint32_t slot) {
         const uint32_t to = slot + lane * 16;
@@ -196,11 +195,11 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
     }
     launch_dependents();
     wait_prior_grids();
-    if (count > 0)
+    if (full > 0)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) load_x(nt, q, 0);
+            for (int q = 0; q < 4; ++q) load_x(nt, q);
 
     float out[RT][NT][4];
 #pragma unroll
@@ -211,18 +210,17 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
             for (int e = 0; e < 4; ++e) out[r][nt][e] = 0.f;
 
     uint32_t slot = ring, to_slot = ring + (D - 1) * R::BYTES;  // to read; to fill: the one read last
-    for (int i = 0; i < count; ++i) {
+    auto block = [&](int i, auto last) {
+        constexpr bool LAST = decltype(last)::value;
         cp_wait<D - 2>();
         __syncwarp();  // every lane's copies of this block are there, and the slot of the last one is free
         if (i + D - 1 < count) copy_weights(to_slot);
         cp_commit();
+        to_slot = slot;
         // the next block's activations take the place of this one's as they are
-        // used (behind the last block: its own again)
-        const int next = min(i + 1, count - 1);
+        // used (behind the last whole block: its own again)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) x[nt] += i + 1 < count ? step[nt] : 0;
-        to_slot += R::BYTES;
-        if (to_slot == ring_end) to_slot = ring;
+        for (int nt = 0; nt < NT; ++nt) x[nt] += i + 1 < full ? step[nt] : 0;
         float acc[RT][NT][4];
         float s0[RT], s1[RT];
         uint32_t z0[RT], z1[RT];
@@ -268,7 +266,8 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
                         }
                     }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) load_x(nt, 2 * e + h, next);
+                for (int nt = 0; nt < NT; ++nt)
+                    if (!LAST) load_x(nt, 2 * e + h);
                 if (G == 32) flush();
             }
             if (G == 64) flush();
@@ -276,6 +275,16 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
         if (G == 128) flush();
         slot += R::BYTES;
         if (slot == ring_end) slot = ring;
+    };
+    for (int i = 0; i < full; ++i) block(i, std::false_type());
+    if (full < count) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (full > 0) x[nt] += step[nt];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) load_last_x(nt, q);
+        }
+        block(full, std::true_type());
     }
 
     // ---- the warps' parts, then the cluster's, added in order

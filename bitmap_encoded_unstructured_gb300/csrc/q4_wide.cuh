@@ -52,8 +52,8 @@ struct Wide {
     static constexpr int WARPS = 4 + DW + PW, THREADS = 32 * WARPS;
     static constexpr int REGS = BN == 128 || BN == 64 ? 96 : 128;
     static constexpr int R_CONTROL = BN >= 128 ? 40 : REGS;
-    static constexpr int R_WIDEN = BN == 256 ? 104 : BN == 128 ? 88 : REGS;
-    static constexpr int R_PROMOTE = BN == 256 ? 184 : BN == 128 ? 128 : REGS;
+    static constexpr int R_WIDEN = BN == 256 ? 136 : BN == 128 ? 104 : REGS;
+    static constexpr int R_PROMOTE = BN == 256 ? 168 : BN == 128 ? 112 : REGS;
     static constexpr int TILES = 8 / DW;                  // row tiles of a widening warp
     static constexpr int COLS = BN / (PW / 4);            // columns of a promoting thread
     // rings: A with B, codes (with zero points), scales
@@ -718,7 +718,7 @@ template <int G>
 Plan plan_of(const Problem& p, const int* clusters)
 {
     constexpr int BN[4] = {32, 64, 128, 256};
-    constexpr int BLOCK[4] = {55, 57, G == 32 ? 86 : 61, G == 128 ? 70 : G == 64 ? 107 : 190}, ENDS[4] = {500, 600, 700, 960};
+    constexpr int BLOCK[4] = {55, 57, G == 32 ? 86 : 61, G == 128 ? 70 : G == 64 ? 87 : 172}, ENDS[4] = {500, 600, 700, 960};
     const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2, blocks = p.k_tiles / 2;
     Plan best = {256, 1};
     int64_t least = INT64_MAX;
