@@ -964,6 +964,8 @@ class Int4Matrix:
         if device is None:
             device = codes.device if codes.is_cuda else torch.device("cuda", torch.cuda.current_device())
         device = torch.device(device)
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         if any(t is not None and t.is_cuda and t.device != device for t in (codes, scales, zeros)):
             raise ValueError(f"codes, scales and zeros must be on {device} or the CPU")
         kept = [None if t is None else t.contiguous() for t in (codes, scales, zeros)]

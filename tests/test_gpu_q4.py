@@ -236,6 +236,81 @@ def test_same_bits_on_any_stream_and_in_graphs(dtype):
     up.close()
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_repeats_give_the_same_bits(group):
+    """Rings that hand a slot on too early show here: one block in some thousands."""
+    import torch
+    M, K = 2048, 2560
+    m = matrix(weight(M, K, group, True, "float16", 1), group, "float16")
+    for N in (1, 16, 30, 50, 100, 300, 600):
+        x = dev(rows(N, K, "float16", N), "float16")
+        want = m.mm(x)
+        bad = torch.zeros((), dtype=torch.int64, device="cuda")
+        for _ in range(150):
+            bad += (m.mm(x) != want).any()
+        assert int(bad) == 0, N
+    m.check()
+    m.close()
+
+
+FRESH = """
+import sys, threading
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import bitmap_encoded_unstructured_gb300 as bsp
+from test_gpu_q4 import dev, matrix, rows, weight
+m, u = (matrix(weight(300, 520, 64, z, "bfloat16", 3), 64, "bfloat16") for z in (True, False))
+xs = [dev(rows(n, 520, "bfloat16", n), "bfloat16") for n in (1, 12, 30, 70, 200)]
+torch.cuda.synchronize()
+{body}
+for x, (y, z) in zip(xs, got):
+    assert torch.equal(m.mm(x), y) and torch.equal(m.gated(u, x), z)
+m.check()
+print("fine")
+"""
+CAPTURED = """
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = [(m.mm(x), m.gated(u, x)) for x in xs]
+g.replay()
+torch.cuda.synchronize()
+"""
+THREADS = """
+res = [None] * 4
+def work(i):
+    with torch.cuda.stream(torch.cuda.Stream()):
+        res[i] = [(m.mm(x), m.gated(u, x)) for x in xs]
+        torch.cuda.current_stream().synchronize()
+ts = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+[t.start() for t in ts]
+[t.join() for t in ts]
+got = res[0]
+assert all(torch.equal(a, c) and torch.equal(b, d) for r in res for (a, b), (c, d) in zip(r, got))
+"""
+
+
+@pytest.mark.parametrize("body", [CAPTURED, THREADS], ids=["captured", "threads"])
+def test_first_calls_of_a_process(body):
+    """The first calls: captured in a graph, or from four threads at once."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FRESH.format(root=os.path.dirname(tests), tests=tests, body=body)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("fine"), r.stderr[-2000:]
+
+
+def test_device_by_name():
+    import torch
+    w = weight(16, 64, 32, False, "float16", 1)
+    m = bsp.Int4Matrix.from_arrays(dev(q4.pack(w[0])), dev(w[1], "float16"), group=32, device="cuda")
+    assert m.device == torch.device("cuda", torch.cuda.current_device())
+    x = rows(3, 64, "float16", 2)
+    close(m.mm(dev(x, "float16")), q4.product(x, *w, 32), q4.error_bound(x, *w, 32), "float16")
+    m.close()
+
+
 def test_binding_errors():
     import torch
     m = matrix(weight(16, 64, 32, False, "float16", 1), 32, "float16")
