@@ -52,15 +52,16 @@ constexpr int BM = 128, BK = 128;      // rows of a strip, columns of a block
 constexpr int A_HALF = BM * 64 * 2, A_BYTES = 2 * A_HALF;  // 64 columns of a strip; a block
 
 // BN columns of Y, G columns of a group.  Registers of a thread by role, from
-// REGS of each at launch (their sum over warpgroups is the launch's).
-template <int G, int BN>
+// REGS of each at launch (their sum over warpgroups is within the launch's),
+// as the compiler needs them to spill nothing, or least.
+template <int G, int BN, bool GATED>
 struct Wide {
     static constexpr int DW = BN == 256 ? 4 : 8, PW = BN == 32 ? 4 : 8;
     static constexpr int WARPS = 4 + DW + PW, THREADS = 32 * WARPS;
     static constexpr int REGS = BN == 128 || BN == 64 ? 96 : 128;
     static constexpr int R_CONTROL = BN >= 128 ? 40 : REGS;
-    static constexpr int R_WIDEN = BN == 256 ? 136 : BN == 128 ? 104 : REGS;
-    static constexpr int R_PROMOTE = BN == 256 ? 168 : BN == 128 ? 112 : REGS;
+    static constexpr int R_WIDEN = BN == 256 ? (GATED ? 120 : 136) : BN == 128 ? 104 : REGS;
+    static constexpr int R_PROMOTE = BN == 256 ? (GATED ? 176 : 168) : BN == 128 ? 112 : REGS;
     static constexpr int TILES = 8 / DW;                  // row tiles of a widening warp
     static constexpr int COLS = BN / (PW / 4);            // columns of a promoting thread
     // rings: A with B, codes (with zero points), scales
@@ -221,10 +222,10 @@ __device__ __forceinline__ void arrive_at(uint32_t addr)
 }
 
 template <class T, int G, int BN, bool GATED>
-__global__ void __launch_bounds__(Wide<G, BN>::THREADS, 1)
+__global__ void __launch_bounds__(Wide<G, BN, GATED>::THREADS, 1)
 q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ WideArgs a)
 {
-    using C = Wide<G, BN>;
+    using C = Wide<G, BN, GATED>;
     static_assert(4 * C::R_CONTROL + C::DW * C::R_WIDEN + C::PW * C::R_PROMOTE <= C::WARPS * C::REGS, "shares of the launch's registers");
     constexpr int SR = C::SR, SC = C::SC, SS = C::SS, ND = C::ND, PER = C::PER, H = C::H;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -291,14 +292,23 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
     }
     tc_before();
     __syncthreads();
-    bspx::cluster_sync();
-    tc_after();
-    const uint32_t tmem = *tmem_slot;
-    // one product addresses both CTAs' tensor memory: they were given the same
-    uint32_t other;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(bspx::mapa_shared(bspx::smem_u32(tmem_slot), rank ^ 1u)) : "memory");
-    bool failed = other != tmem;
-    if (failed) blocks = 0;
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    bool failed = false;
+    uint32_t tmem = 0;
+    // The pair meets before a warp reaches into the other CTA; the warps that
+    // load, which do not, start at once.
+    auto meet = [&]() {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        tc_after();
+        tmem = *tmem_slot;
+        // one product addresses both CTAs' tensor memory: they were given the same
+        uint32_t other;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(bspx::mapa_shared(bspx::smem_u32(tmem_slot), rank ^ 1u)) : "memory");
+        failed = other != tmem;
+        if (failed) blocks = 0;
+    };
     // Every role waits for the kernels before this one ahead of its first
     // bounded wait that depends on X: a bounded wait counts only this kernel's
     // time.
@@ -329,8 +339,12 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             }
             // no copy may land after the CTA is gone (the full cap, whatever `cap` is)
             for (int k = std::max(a.stall ? 1 : 0, i - SR); k < i; ++k) bspx::mbar_wait_bounded(x_full + k % SR, (k / SR) & 1);
+            const bool late = failed;
+            meet();
+            failed = failed || late;
         } else if (warp == 2) {
             // ---------------- tells the first CTA that this half of X is here
+            meet();
             wait_prior_grids();
             int s = 0;
             uint32_t ph = 0;
@@ -344,6 +358,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                 if (++s == SR) { s = 0; ph ^= 1u; }
             }
         } else if (warp == 1) {
+            meet();
             if (!half) {
                 // ---------------- products
                 wait_prior_grids();
@@ -424,6 +439,9 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             }
             for (int k = std::max(0, u - SC); k < u; ++k) bspx::mbar_wait_bounded(c_full + k % SC, (k / SC) & 1);
             for (int k = std::max(0, u - SS); k < u; ++k) bspx::mbar_wait_bounded(s_full + k % SS, (k / SS) & 1);
+            const bool late = failed;
+            meet();
+            failed = failed || late;
         }
         if (failed && lane == 0) atomicExch(a.err, (int)BSP_ERR_TIMEOUT);
         bspx::cluster_sync();
@@ -433,6 +451,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
 
     if (warp < 4 + C::DW) {
         take_registers<C::REGS, C::R_WIDEN>();
+        meet();
         // ---------------- codes -> A.  Warp w takes row tiles w, w + DW of the
         // strip.  Lanes of odd rows store the upper half of their columns
         // first, so that the eight lanes of a store's phase reach distinct
@@ -504,6 +523,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
 
     take_registers<C::REGS, C::R_PROMOTE>();
     {
+        meet();
         // ---------------- sums of groups, scaled, into registers
         const int p = warp - 4 - C::DW, quad = warp & 3, row = 32 * quad + lane, c0 = (p >> 2) * C::COLS;
         const uint32_t scales = bspx::smem_u32(smem + C::OFF_S) + (row / 16 * 8 + row % 8) * 4 + (row >> 3 & 1) * 2;
@@ -554,69 +574,100 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         tc_before();
         __syncwarp();
         if (lane == 0) bspx::mbar_arrive(read);
-        // ---------------- the sums to shared memory, [column][row], over the
-        // rings: every product is done, and every promoting warp has its last
-        // scales
-        asm volatile("bar.sync 1, %0;" ::"n"(C::PW * 32) : "memory");
-        float* part = reinterpret_cast<float*>(smem);
+        const int64_t m = strip * BM + row;
+        T* y = reinterpret_cast<T*>(a.y) + m;
+        float* part = reinterpret_cast<float*>(smem);  // over the rings: every product is done
+        if (shares == 1 && !GATED) {
+            // ---------------- out as they are: a warp 32 rows of a column
+            bspx::cluster_sync();
+            if (!failed && m < a.M)
 #pragma unroll
-        for (int i = 0; i < C::COLS; ++i) part[(c0 + i) * BM + row] = sum[i];
-        bspx::cluster_sync();
-        // a warp four columns at a time (another CTA's sums take some 1000 cycles
-        // to come), four rows a lane.  Rows of one strip: its CTAs share its
-        // columns.  Gated: all CTAs do.
-        const int of = GATED ? ranks : shares, mine = GATED ? rank : share;
-        const int from_col = BN * mine / of, to_col = (int)min((int64_t)(BN * (mine + 1) / of), a.N - n0);
-        const int64_t m0 = strip * BM + 4 * lane;
-        const bool whole = m0 + 4 <= a.M && a.y_stride % 4 == 0;
-        auto total = [&](uint32_t side, int c0, float4 (&v)[4]) {  // of columns c0, c0 + PW, ...
+                for (int i = 0; i < C::COLS; ++i)
+                    if (n0 + c0 + i < a.N) y[(n0 + c0 + i) * a.y_stride] = from_float<T>(sum[i]);
+            bspx::cluster_sync();
+        } else if (shares == 1) {
+            // ---------------- gate and up meet: of every thread's columns the
+            // first CTA finishes the first half, the second the other; what the
+            // other CTA finishes goes to its shared memory
+            constexpr int HALF = C::COLS / 2;
+            float* own = part + (p >> 2) * (HALF * BM) + row;
+            const uint32_t here = bspx::smem_u32(own), there = bspx::mapa_shared(here + BN / 2 * BM * 4, rank ^ 1u);
+            const uint32_t to[2] = {half ? there : here, half ? here : there};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (uint32_t k = 0; k < shares; ++k) {
-                const uint32_t from = bspx::mapa_shared(bspx::smem_u32(part + c0 * BM + 4 * lane), 2 * k + side);
-                float4 x[4];
+            for (int i = 0; i < C::COLS; ++i)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to[i / HALF] + i % HALF * BM * 4), "f"(sum[i]) : "memory");
+            bspx::cluster_sync();
+            const int64_t n1 = n0 + c0 + half * HALF;
+            const int last = (int)min((int64_t)HALF, a.N - n1);
+            const float* gate = own + (half ? BN / 2 * BM : 0);
+            const float* up = own + (half ? 0 : BN / 2 * BM);
+            if (!failed && m < a.M)
+#pragma unroll 4
+                for (int i = 0; i < last; ++i) y[(n1 + i) * a.y_stride] = from_float<T>(activate(gate[i * BM], a.act) * up[i * BM]);
+            bspx::cluster_sync();
+        } else {
+            // ---------------- parts to shared memory, [column][row], and their sums
+            // from all CTAs that share the tile's columns
+            asm volatile("bar.sync 1, %0;" ::"n"(C::PW * 32) : "memory");
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                                 : "=f"(x[j].x), "=f"(x[j].y), "=f"(x[j].z), "=f"(x[j].w)
-                                 : "r"(from + (c0 + j * C::PW < to_col ? j * C::PW * BM * 4 : 0))
-                                 : "memory");
+            for (int i = 0; i < C::COLS; ++i) part[(c0 + i) * BM + row] = sum[i];
+            bspx::cluster_sync();
+            // a warp four columns at a time (another CTA's sums take some 1000 cycles
+            // to come), four rows a lane.  Rows of one strip: its CTAs share its
+            // columns.  Gated: all CTAs do.
+            const int of = GATED ? ranks : shares, mine = GATED ? rank : share;
+            const int from_col = BN * mine / of, to_col = (int)min((int64_t)(BN * (mine + 1) / of), a.N - n0);
+            const int64_t m0 = strip * BM + 4 * lane;
+            const bool whole = m0 + 4 <= a.M && a.y_stride % 4 == 0;
+            auto total = [&](uint32_t side, int c0, float4 (&v)[4]) {  // of columns c0, c0 + PW, ...
 #pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (uint32_t k = 0; k < shares; ++k) {
+                    const uint32_t from = bspx::mapa_shared(bspx::smem_u32(part + c0 * BM + 4 * lane), 2 * k + side);
+                    float4 x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(x[j].x), "=f"(x[j].y), "=f"(x[j].z), "=f"(x[j].w)
+                                     : "r"(from + (c0 + j * C::PW < to_col ? j * C::PW * BM * 4 : 0))
+                                     : "memory");
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[j].x += x[j].x;
+                        v[j].y += x[j].y;
+                        v[j].z += x[j].z;
+                        v[j].w += x[j].w;
+                    }
+                }
+            };
+#pragma unroll 1
+            for (int c = from_col + p; c < to_col && !failed; c += 4 * C::PW) {
+                float4 v[4], u[4];
+                total(GATED ? 0 : half, c, v);
+                if (GATED) total(1, c, u);
+#pragma unroll 1
                 for (int j = 0; j < 4; ++j) {
-                    v[j].x += x[j].x;
-                    v[j].y += x[j].y;
-                    v[j].z += x[j].z;
-                    v[j].w += x[j].w;
+                    const int n = c + j * C::PW;
+                    if (n >= to_col) break;
+                    float4 z = v[0];
+                    if (GATED) z = make_float4(activate(z.x, a.act) * u[0].x, activate(z.y, a.act) * u[0].y, activate(z.z, a.act) * u[0].z,
+                                               activate(z.w, a.act) * u[0].w);
+                    T* y = reinterpret_cast<T*>(a.y) + (n0 + n) * a.y_stride + m0;
+                    alignas(8) const T o[4] = {from_float<T>(z.x), from_float<T>(z.y), from_float<T>(z.z), from_float<T>(z.w)};
+                    if (whole) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
+                    else
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (m0 + e < a.M) y[e] = o[e];
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {  // the next one
+                        v[i] = v[i + 1];
+                        if (GATED) u[i] = u[i + 1];
+                    }
                 }
             }
-        };
-#pragma unroll 1
-        for (int c = from_col + p; c < to_col && !failed; c += 4 * C::PW) {
-            float4 v[4], u[4];
-            total(GATED ? 0 : half, c, v);
-            if (GATED) total(1, c, u);
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                const int n = c + j * C::PW;
-                if (n >= to_col) break;
-                float4 z = v[0];
-                if (GATED) z = make_float4(activate(z.x, a.act) * u[0].x, activate(z.y, a.act) * u[0].y, activate(z.z, a.act) * u[0].z,
-                                           activate(z.w, a.act) * u[0].w);
-                T* y = reinterpret_cast<T*>(a.y) + (n0 + n) * a.y_stride + m0;
-                alignas(8) const T o[4] = {from_float<T>(z.x), from_float<T>(z.y), from_float<T>(z.z), from_float<T>(z.w)};
-                if (whole) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
-                else
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (m0 + e < a.M) y[e] = o[e];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) {  // the next one
-                    v[i] = v[i + 1];
-                    if (GATED) u[i] = u[i + 1];
-                }
-            }
+            bspx::cluster_sync();  // others may still read this CTA's sums
         }
-        bspx::cluster_sync();  // others may still read this CTA's sums
     }
     if (failed && lane == 0) atomicExch(a.err, (int)BSP_ERR_TIMEOUT);
 }
@@ -638,7 +689,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 template <class T, int G, int BN, bool GATED>
 bsp_status_t launch_wide(const Problem& p, int shares, cudaStream_t s)
 {
-    using C = Wide<G, BN>;
+    using C = Wide<G, BN, GATED>;
     static bsp_attr_once attr_once;
     if (!attr_once.run(p.device, [] {
             return cudaFuncSetAttribute(q4_wide_kernel<T, G, BN, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -700,7 +751,7 @@ const int* clusters_at_once(int device, int num_sms)
     int* m = most[device];
     if (!m[0]) {
         auto* k = q4_wide_kernel<T, G, 256, false>;
-        using C = Wide<G, 256>;
+        using C = Wide<G, 256, false>;
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return nullptr;
         for (int i = 3; i >= 0; --i) {
             cudaLaunchConfig_t cfg = {};
@@ -732,7 +783,7 @@ template <int G>
 Plan plan_of(const Problem& p, const int* clusters)
 {
     constexpr int BN[4] = {32, 64, 128, 256};
-    constexpr int BLOCK[4] = {55, 57, G == 32 ? 86 : 61, G == 128 ? 70 : G == 64 ? 87 : 172}, ENDS[4] = {500, 600, 700, 960};
+    constexpr int BLOCK[4] = {56, G == 32 ? 69 : 57, G == 32 ? 96 : 61, G == 128 ? 70 : G == 64 ? 87 : 145}, ENDS[4] = {500, 600, 700, 960};
     const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2, blocks = p.k_tiles / 2;
     Plan best = {256, 1};
     int64_t least = INT64_MAX;
