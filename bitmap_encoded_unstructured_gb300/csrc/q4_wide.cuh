@@ -26,9 +26,9 @@
 //
 // With groups of 128 a block of 256 columns of Y takes 690 ns where its products
 // alone take 540 (tensor pipe 66% busy); groups of 64 and 32 are bound by the
-// promoting warps, 870 and 1720 ns (two and four passes over the sums a
-// block), tiles of 128 columns and fewer by their chain of waits, 560 to 620.
-// 1501 rows of 8192 x 28672: 505 us (1395 TFLOP/s, 0.74 of the library's bf16
+// promoting warps, 870 and 1400 ns (two and four passes over the sums a
+// block), tiles of 128 columns and fewer by their chain of waits, 480 to 620.
+// 1501 rows of 8192 x 28672: 484 us (1457 TFLOP/s, 0.77 of the library's bf16
 // product); gated 2048 rows of 28672 x 8192: 1460 us (1318 TFLOP/s).
 #pragma once
 
