@@ -182,22 +182,24 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// (Volatile: a plain load may be moved behind the arrival that gives its slot
+// back, and even behind the next wait.)
 __device__ __forceinline__ uint4 lds16(uint32_t at)
 {
     uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds2(uint32_t at)
 {
     uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
+    asm volatile("ld.volatile.shared.u16 %0, [%1];" : "=h"(v) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds1(uint32_t at)
 {
     uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    asm volatile("ld.volatile.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
     return v;
 }
 __device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
@@ -505,9 +507,9 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                 }
             bspx::fence_proxy_async_smem();
             __syncwarp();
-            // the codes' slot is given back here, not where they were loaded: an
-            // arrival there went ahead of other lanes' loads (one block in some
-            // thousands held codes of a later one)
+            // the codes' slot is given back here, behind the stores that need them:
+            // an arrival right behind their loads went ahead of some lanes' (one
+            // block in some thousands held codes of a later one)
             if (lane == 0) {
                 arrive_at(told + s * 8);
                 bspx::mbar_arrive(c_empty + sc);
