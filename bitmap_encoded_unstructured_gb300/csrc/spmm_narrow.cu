@@ -702,7 +702,12 @@ spmm_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const NarrowArgs a)
                 const uint32_t seg = !I8 ? t - (uint32_t)t0
                                          : (t == (uint32_t)t0 ? pos / RUN : R0 + (t - (uint32_t)t0 - 1) * RT + k / RUN);
                 const uint32_t buf = seg & 1u;
-                if (!__all_sync(FULL, wait_bar(acc_full + buf, (seg >> 1) & 1u, cap, BSP_NARROW_SLEEP_DEC))) {
+                // First the MMAs of this step: a decoder runs up to NG steps
+                // ahead of them, segments can be a step long, and a parity
+                // wait for this use of the buffer would pass while its last
+                // use but one (two segments back) is still to come.
+                if (!__all_sync(FULL, wait_bar(a_empty + G, it & 1u, cap, BSP_NARROW_SLEEP_DEC) &&
+                                          wait_bar(acc_full + buf, (seg >> 1) & 1u, cap, BSP_NARROW_SLEEP_DEC))) {
                     failed = true;
                     break;
                 }
