@@ -56,9 +56,9 @@ constexpr int A_HALF = BM * 64 * 2, A_BYTES = 2 * A_HALF;  // 64 columns of a st
 // as the compiler needs them to spill nothing, or least.
 template <int G, int BN, bool GATED>
 struct Wide {
-    static constexpr int DW = BN == 256 ? 4 : 8, PW = BN == 32 ? 4 : 8;
+    static constexpr int DW = BN == 256 ? 4 : 8, PW = 8;
     static constexpr int WARPS = 4 + DW + PW, THREADS = 32 * WARPS;
-    static constexpr int REGS = BN == 128 || BN == 64 ? 96 : 128;
+    static constexpr int REGS = BN == 256 ? 128 : 96;
     static constexpr int R_CONTROL = BN >= 128 ? 40 : REGS;
     static constexpr int R_WIDEN = BN == 256 ? (GATED ? 120 : 136) : BN == 128 ? 104 : REGS;
     static constexpr int R_PROMOTE = BN == 256 ? (GATED ? 176 : 168) : BN == 128 ? 112 : REGS;
@@ -784,12 +784,12 @@ struct Plan {
 template <int G>
 Plan plan_of(const Problem& p, const int* clusters)
 {
-    constexpr int BN[4] = {32, 64, 128, 256};
-    constexpr int BLOCK[4] = {56, G == 32 ? 69 : 57, G == 32 ? 96 : 61, G == 128 ? 70 : G == 64 ? 87 : 145}, ENDS[4] = {500, 600, 700, 960};
+    constexpr int BN[3] = {64, 128, 256};
+    constexpr int BLOCK[3] = {G == 32 ? 60 : 48, G == 32 ? 92 : 55, G == 128 ? 67 : G == 64 ? 86 : 137}, ENDS[3] = {600, 790, 1060};
     const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2, blocks = p.k_tiles / 2;
     Plan best = {256, 1};
     int64_t least = INT64_MAX;
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 3; ++i)
         for (int s = 1; s <= 4 && s <= blocks; ++s) {
             const int64_t tiles = pairs * ((p.N + BN[i] - 1) / BN[i]), waves = (tiles + clusters[s - 1] - 1) / clusters[s - 1];
             const int64_t cost = waves * ((blocks + s - 1) / s * BLOCK[i] + ENDS[i] + (s > 1 ? 100 : 0));
@@ -813,7 +813,6 @@ bsp_status_t wide_by_shape(const Problem& p, cudaStream_t s)
     };
     using std::integral_constant;
     switch (plan.bn) {
-    case 32: return go(integral_constant<int, 32>());
     case 64: return go(integral_constant<int, 64>());
     case 128: return go(integral_constant<int, 128>());
     default: return go(integral_constant<int, 256>());
