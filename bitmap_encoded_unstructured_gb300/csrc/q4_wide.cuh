@@ -311,12 +311,12 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         failed = other != tmem;
         if (failed) blocks = 0;
     };
+    // The next kernel may start now that the tensor memory is this CTA's (one that
+    // starts earlier may take some, and then waits for this kernel).
+    if (threadIdx.x == 0) launch_dependents();
     // Every role waits for the kernels before this one ahead of its first
     // bounded wait that depends on X: a bounded wait counts only this kernel's
     // time.
-    // (not before the tensor memory is this CTA's: a kernel that starts early
-    // may take some, and then waits for this one)
-    if (threadIdx.x == 0) launch_dependents();
 
     if (warp < 4) {
         take_registers<C::REGS, C::R_CONTROL>();
@@ -361,9 +361,9 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             }
         } else if (warp == 1) {
             meet();
+            wait_prior_grids();  // both CTAs: the second one's waits for the end of the products below count too
             if (!half) {
                 // ---------------- products
-                wait_prior_grids();
                 const int n = __shfl_sync(FULL, blocks, 0);
                 const uint32_t tm = __shfl_sync(FULL, tmem, 0), both = __shfl_sync(FULL, 3u << lead, 0);
                 const uint64_t a_desc = smem_desc(bspx::smem_u32(smem)), b_desc = smem_desc(bspx::smem_u32(smem + C::OFF_B));
