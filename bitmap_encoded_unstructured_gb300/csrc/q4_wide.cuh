@@ -468,6 +468,9 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         int s = 0, sc = 0;
         uint32_t ph = 0, pc = 0;
         for (int u = 0; u < blocks; ++u) {
+            // from block SC on codes come, and from block SR on slots fall free, only
+            // once the kernels before this one are done (see the loads, and the products)
+            if (u == (SC < SR ? SC : SR)) wait_prior_grids();
             if (!wait(c_full + sc, pc, cap)) {
                 failed = true;
                 break;
@@ -482,7 +485,6 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                 for (int y = 0; y < ZN; ++y)
                     z[x][y] = has_zeros ? lds1(zero + sc * C::C_BYTES + x * (C::DW * 8) + y * 64) : 0x88u;
             }
-            if (u == SR) wait_prior_grids();
             if (u >= SR && !wait(empty + s, ph ^ 1u, cap)) {
                 failed = true;
                 break;

@@ -82,3 +82,42 @@ def product(before, M, K, N, group, dtype):
 def test_wide_product(before, M, K, N, group, dtype):
     """Tiles of 64 columns: both CTAs of a pair start, and free their tensor memory, behind the long call."""
     product(before, M, K, N, group, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("M,K,N,group", [(1000, 1024, 1300, 64), (2600, 1032, 900, 128), (2600, 2056, 400, 64), (3300, 520, 2000, 32)])
+def test_large_tiles(before, M, K, N, group, dtype):
+    """Tiles of 128 and 256 columns: a ring of codes no longer than that of the tiles they become."""
+    product(before, M, K, N, group, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("N", [5, 50, 700])
+def test_gated(before, N, dtype):
+    import torch
+    M, K, group = 2600, 1032, 64
+    x = dev(rows(N, K, dtype, 3), dtype)
+
+    class Pair:
+        def __init__(self):
+            self.a, self.b = (matrix(weight(M, K, group, z, dtype, 4), group, dtype) for z in (True, False))
+
+        def check(self):
+            self.a.check()
+
+        def close(self):
+            self.a.close()
+            self.b.close()
+
+    p = Pair()
+    right = p.a.gated(p.b, x)
+    p.close()
+    if N > 32:
+        behind(before, Pair, lambda p: p.a.gated(p.b, x), right)
+        return
+    T, long, first = before  # the narrow kernel has no bounded wait
+    p = Pair()
+    for _ in range(3):
+        long()
+        assert torch.equal(p.a.gated(p.b, x), right)
+    p.close()
