@@ -702,6 +702,9 @@ spmm_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const NarrowArgs a)
                 const uint32_t seg = !I8 ? t - (uint32_t)t0
                                          : (t == (uint32_t)t0 ? pos / RUN : R0 + (t - (uint32_t)t0 - 1) * RT + k / RUN);
                 const uint32_t buf = seg & 1u;
+                // Y and the workspace: the previous kernel is done with them
+                // (and its time does not count below: this step's MMAs wait for it)
+                wait_prior_grids();
                 // First the MMAs of this step: a decoder runs up to NG steps
                 // ahead of them, segments can be a step long, and a parity
                 // wait for this use of the buffer would pass while its last
@@ -712,7 +715,6 @@ spmm_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const NarrowArgs a)
                     break;
                 }
                 tc_fence_after();
-                wait_prior_grids();  // Y and the workspace: the previous kernel is done with them
                 uint32_t r[16];
                 tmem_ld16(tmem_base + buf * D_COLS + tq, r);
                 const int64_t m = (int64_t)t * BM + 32 * q + lane;
