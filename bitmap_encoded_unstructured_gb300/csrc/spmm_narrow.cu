@@ -645,9 +645,12 @@ spmm_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const NarrowArgs a)
         uint32_t sc = G, pc = 0;
         uint32_t it = 0;
         for (uint32_t i = G; i < S; i += NG, ++it) {
+            // the MMAs wait for the previous kernel, and so do C stages from
+            // the SC-th step on (see the producer): wait for it ahead of the
+            // bounded waits that depend on either
+            if (it == 1) wait_prior_grids();
             bool ok = wait_bar(c_full + sc, pc, cap, BSP_NARROW_SLEEP_DEC);
             // the MMAs of this group's previous step read A stage G: done
-            if (it == 1) wait_prior_grids();  // the MMAs wait for the previous kernel (see the producer)
             if (it > 0) ok = ok && wait_bar(a_empty + G, (it - 1) & 1u, cap, BSP_NARROW_SLEEP_DEC);
             if (!__all_sync(FULL, ok)) { failed = true; break; }
             tc_fence_after();

@@ -9,7 +9,8 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("N", [4, 16])
-@pytest.mark.parametrize("M,K", [(2000, 64), (11008, 64), (9000, 192), (128, 256)])  # a tile ends in a decoder group's first step
+@pytest.mark.parametrize("M,K", [(2000, 64), (11008, 64), (9000, 192), (128, 256),    # a tile ends in a decoder group's first step
+                                 (20000, 2048), (11008, 4096)])                       # dense: as few stages as there may be
 def test_products(before, M, K, N):  # noqa: F811
     import torch
     T, long, first = before
