@@ -92,6 +92,16 @@ __device__ __forceinline__ uint32_t lds1(uint32_t at)
     return v;
 }
 
+// 16 bytes of activations.  Not through the read-only path: the kernel is
+// resident while the kernel before it may still write them, and only loads
+// behind griddepcontrol.wait see what it wrote (volatile asm keeps its place).
+__device__ __forceinline__ uint4 ldg16(const char* at)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+}
+
 // c += a b, or a b (FIRST).
 template <class T, bool FIRST>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -166,7 +176,7 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
     const int whole = (int)(a.K / 128) - first;       // blocks from here on that lie inside K
     const int left = (int)(a.K % 128) - 8 * t;        // of the block behind them: columns from this lane's first on
     uint4 b[NT][4];
-    auto load_x = [&](int nt, int q) { b[nt][q] = __ldg(reinterpret_cast<const uint4*>(x[nt] + 64 * q)); };
+    auto load_x = [&](int nt, int q) { b[nt][q] = ldg16(x[nt] + 64 * q); };
     auto load_last_x = [&](int nt, int q) {  // of a block in which K, a multiple of 8, ends
         b[nt][q] = make_uint4(0u, 0u, 0u, 0u);
         if (left > 32 * q) load_x(nt, q);
