@@ -789,11 +789,11 @@ spmm_narrow_kernel(const __grid_constant__ CUtensorMap tmX, const NarrowArgs a)
 // Finishing kernel: Y of the tiles whose steps are split between CTAs (and,
 // int8, of the tiles of several runs), from the workspace (which it clears)
 // or, deterministically, from the segments' slots added in segment order.
-// One thread per (row, column < N).
+// One thread per (row, column < N).  (No __restrict__: it is resident while the
+// product kernel writes the slots, which read-only loads do not allow for.)
 template <bool I8>
 __global__ void __launch_bounds__(256)
-spmm_narrow_finish_kernel(void* __restrict__ Y, float* __restrict__ ws, const float* __restrict__ ws_det,
-                          int64_t M, int64_t N, int64_t KT, int64_t T, int64_t P)
+spmm_narrow_finish_kernel(void* Y, float* ws, const float* ws_det, int64_t M, int64_t N, int64_t KT, int64_t T, int64_t P)
 {
     // the next product kernel may start its prologue now (it waits for this
     // grid before it touches Y or the workspace)
