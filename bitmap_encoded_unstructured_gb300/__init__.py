@@ -409,6 +409,24 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on_stream(stream, device):
+    """torch's work goes to a call's explicit ``stream`` (a Stream or a
+    handle) inside the block."""
+    import torch
+    if isinstance(stream, int):  # 0 and 1 are the default stream's handles
+        stream = torch.cuda.ExternalStream(stream, device) if stream > 1 else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _contiguous(t, stream):
+    """``t`` with contiguous rows; a copy is made on the call's stream, which
+    the caller has ordered behind what wrote ``t``."""
+    if stream is None or not t.is_cuda or t.is_contiguous():
+        return t.contiguous()
+    with _on_stream(stream, t.device):
+        return t.contiguous()
+
+
 class BitmapMatrix:
     """An encoded weight W (M x K) living on one GPU.
 
@@ -430,7 +448,7 @@ class BitmapMatrix:
             self.dtype = BSP_INT8
         else:
             raise TypeError("W must be float16 or int8")
-        W = W.contiguous()
+        W = _contiguous(W, stream)
         self.M, self.K = W.shape
         self.device = W.device
         self.torch_dtype = W.dtype
@@ -448,7 +466,7 @@ class BitmapMatrix:
         def ptr(a):
             if isinstance(a, np.ndarray):
                 return np.ascontiguousarray(a).ctypes.data, a
-            a = a.contiguous()
+            a = _contiguous(a, stream)
             return a.data_ptr(), a
 
         vals = values
@@ -602,7 +620,7 @@ class UnionMatrix:
         import torch
         if W.dtype != torch.int8 or not W.is_cuda or W.dim() != 2:
             raise TypeError("W must be a 2-D int8 CUDA tensor")
-        W = W.contiguous()
+        W = _contiguous(W, stream)
         self.M, self.K = int(W.shape[0]), int(W.shape[1])
         self.bits = int(bits)
         self.device = W.device
@@ -940,7 +958,7 @@ class Int4Matrix:
         if not W.is_cuda or W.dim() != 2:
             raise ValueError("W must be a 2-D CUDA tensor")
         dt = _row_dtype(W.dtype)
-        W = W.contiguous()
+        W = _contiguous(W, stream)
         h = C.c_void_p()
         with torch.cuda.device(W.device):
             _check("bsp_q4_encode", lib().bsp_q4_encode(W.data_ptr(), dt, W.shape[0], W.shape[1], int(group),
@@ -968,7 +986,7 @@ class Int4Matrix:
             device = torch.device("cuda", torch.cuda.current_device())
         if any(t is not None and t.is_cuda and t.device != device for t in (codes, scales, zeros)):
             raise ValueError(f"codes, scales and zeros must be on {device} or the CPU")
-        kept = [None if t is None else t.contiguous() for t in (codes, scales, zeros)]
+        kept = [None if t is None else _contiguous(t, stream) for t in (codes, scales, zeros)]
         at = [None if t is None else t.data_ptr() for t in kept]
         h = C.c_void_p()
         with torch.cuda.device(device):
