@@ -12,6 +12,11 @@ Two layers:
   (the paged 8-bit KV cache and its attention) and ``Rotary`` (rotary
   positions), handle owners with tensor-level methods.
 
+A method's ``stream`` (a ``torch.cuda.Stream`` or a handle; None: the current
+one) takes the place of the current stream in all that the call does: a call with
+``stream=s`` is one inside ``with torch.cuda.stream(s)``.  The caller orders
+``s`` behind what wrote the tensors that it hands over.
+
 The library is loaded on first use; if it is missing or fails to load, the
 call raises ``RuntimeError`` (there is no fallback of any kind).
 
@@ -427,6 +432,17 @@ def _contiguous(t, stream):
         return t.contiguous()
 
 
+def _new(stream, shape, dtype, device):
+    """Memory for a call's output.  With an explicit stream it belongs to that
+    stream, as if the call were made inside ``torch.cuda.stream(stream)``: memory of the
+    current stream may still be in use there."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on_stream(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class BitmapMatrix:
     """An encoded weight W (M x K) living on one GPU.
 
@@ -514,9 +530,9 @@ class BitmapMatrix:
         import torch
         o = bsp_info(self.h)
         dev = self.device
-        bm = torch.empty(o.NBT, dtype=torch.int64, device=dev)
-        off = torch.empty(o.NGT + 1, dtype=torch.int32, device=dev)
-        vals = torch.empty(o.NNZ, dtype=self.torch_dtype, device=dev)
+        bm = _new(stream, o.NBT, torch.int64, dev)
+        off = _new(stream, o.NGT + 1, torch.int32, dev)
+        vals = _new(stream, o.NNZ, self.torch_dtype, dev)
         bsp_export(self.h, bm.data_ptr(), off.data_ptr(), vals.data_ptr() if o.NNZ else None,
                    _stream(stream))
         return bm, off, vals
@@ -542,11 +558,11 @@ class BitmapMatrix:
         tc = -(-self.K // 64)
         ngt = tr * tc
         dev = self.device
-        off = torch.empty(ngt + 1, dtype=torch.int32, device=dev)
-        ci = torch.empty(ngt * 64, dtype=torch.int32, device=dev)
-        bm = torch.empty(ngt * 64 * 4, dtype=torch.int64, device=dev)
+        off = _new(stream, ngt + 1, torch.int32, dev)
+        ci = _new(stream, ngt * 64, torch.int32, dev)
+        bm = _new(stream, ngt * 64 * 4, torch.int64, dev)
         nnz = self.nnz
-        vals = torch.empty(nnz, dtype=self.torch_dtype, device=dev)
+        vals = _new(stream, nnz, self.torch_dtype, dev)
         _check("bsp_column_index_export", lib().bsp_column_index_export(
             self.h, off.data_ptr(), ci.data_ptr(), bm.data_ptr(), vals.data_ptr() if nnz else None,
             _stream(stream)))
@@ -558,38 +574,35 @@ class BitmapMatrix:
         bsp_set_deterministic(self.h, on)
 
     # -- compute
-    def _out(self, N, out, dtype):
-        import torch
-        if out is None:
-            out = torch.empty((N, self.M), dtype=dtype, device=self.device)
-        return out
+    def _out(self, N, out, dtype, stream):
+        return _new(stream, (N, self.M), dtype, self.device) if out is None else out
 
     def spmm(self, X, out=None, stream=None):
         import torch
         N = X.shape[0]
         ydt = torch.float16 if self.dtype == BSP_FP16 else torch.int32
-        Y = self._out(N, out, ydt)
+        Y = self._out(N, out, ydt, stream)
         bsp_spmm(self.h, X.data_ptr(), N, Y.data_ptr(), _stream(stream))
         return Y
 
     def spmm_scaled(self, X, row_scale, out=None, stream=None):
         import torch
         N = X.shape[0]
-        Y = self._out(N, out, torch.float32)
+        Y = self._out(N, out, torch.float32, stream)
         bsp_spmm_scaled(self.h, X.data_ptr(), N, row_scale.data_ptr(), Y.data_ptr(), _stream(stream))
         return Y
 
     def spmspv(self, x, out=None, stream=None):
         import torch
         ydt = torch.float16 if self.dtype == BSP_FP16 else torch.int32
-        y = out if out is not None else torch.empty(self.M, dtype=ydt, device=self.device)
+        y = out if out is not None else _new(stream, self.M, ydt, self.device)
         bsp_spmspv(self.h, x.data_ptr(), y.data_ptr(), _stream(stream))
         return y
 
     def spmspv_threshold(self, x, threshold, out=None, stream=None):
         import torch
         ydt = torch.float16 if self.dtype == BSP_FP16 else torch.int32
-        y = out if out is not None else torch.empty(self.M, dtype=ydt, device=self.device)
+        y = out if out is not None else _new(stream, self.M, ydt, self.device)
         bsp_spmspv_threshold(self.h, x.data_ptr(), float(threshold), y.data_ptr(), _stream(stream))
         return y
 
@@ -603,9 +616,7 @@ class BitmapMatrix:
         return Y_host
 
     def decode(self, out=None, stream=None):
-        import torch
-        W = out if out is not None else torch.empty((self.M, self.K), dtype=self.torch_dtype,
-                                                    device=self.device)
+        W = out if out is not None else _new(stream, (self.M, self.K), self.torch_dtype, self.device)
         bsp_decode(self.h, W.data_ptr(), _stream(stream))
         return W
 
@@ -649,16 +660,16 @@ class UnionMatrix:
         """Copies of (masks int64 [NLT * 16], offsets int32 [NLT + 1], values uint8 [value_bytes])."""
         import torch
         o = bsp_union_info(self.h)
-        masks = torch.empty(o.NLT * 16, dtype=torch.int64, device=self.device)
-        offsets = torch.empty(o.NLT + 1, dtype=torch.int32, device=self.device)
-        values = torch.empty(o.value_bytes, dtype=torch.uint8, device=self.device)
+        masks = _new(stream, o.NLT * 16, torch.int64, self.device)
+        offsets = _new(stream, o.NLT + 1, torch.int32, self.device)
+        values = _new(stream, o.value_bytes, torch.uint8, self.device)
         bsp_union_export(self.h, masks.data_ptr(), offsets.data_ptr(), values.data_ptr() if o.value_bytes else None,
                          _stream(stream))
         return masks, offsets, values
 
     def decode(self, stream=None):
         import torch
-        W = torch.empty((self.M, self.K), dtype=torch.int8, device=self.device)
+        W = _new(stream, (self.M, self.K), torch.int8, self.device)
         bsp_union_decode(self.h, W.data_ptr(), _stream(stream))
         return W
 
@@ -666,7 +677,7 @@ class UnionMatrix:
         """Copy of the per-LT row permutations (uint8 [NLT, 64]) of a reordered encoding."""
         import torch
         o = bsp_union_info(self.h)
-        p = torch.empty((o.NLT, 64), dtype=torch.uint8, device=self.device)
+        p = _new(stream, (o.NLT, 64), torch.uint8, self.device)
         bsp_union_export_perms(self.h, p.data_ptr(), _stream(stream))
         return p
 
@@ -676,7 +687,7 @@ class UnionMatrix:
     def spmm(self, X, out=None, stream=None):
         import torch
         N = int(X.shape[0])
-        Y = out if out is not None else torch.empty((N, self.M), dtype=torch.int32, device=self.device)
+        Y = out if out is not None else _new(stream, (N, self.M), torch.int32, self.device)
         bsp_union_spmm(self.h, X.data_ptr(), N, Y.data_ptr(), _stream(stream))
         return Y
 
@@ -829,7 +840,11 @@ class KvCache:
         a request's new rows: with it (1 for single tokens) attention does not
         launch the prompt kernel in vain.  The step also carries ``granted``,
         ``slots``, ``positions`` and the new ``free_count``."""
-        step = KvStep.empty(block_table.shape[0], tokens, block_table.device) if out is None else out
+        if out is None:
+            with contextlib.nullcontext() if stream is None else _on_stream(stream, block_table.device):
+                step = KvStep.empty(block_table.shape[0], tokens, block_table.device)
+        else:
+            step = out
         if step.block_table is not block_table:
             step._bind(block_table, max_new)
         c, index = step._c, self._index
@@ -890,8 +905,11 @@ class KvCache:
         dt = _row_dtype(dtype)
         if out is None:
             shape = (n, self.heads, self.dim)  # two allocations cost less than two views of one
-            k = self._empty(shape, dtype=dtype, device=self.device)
-            v = self._empty(shape, dtype=dtype, device=self.device)
+            if stream is None:
+                k = self._empty(shape, dtype=dtype, device=self.device)
+                v = self._empty(shape, dtype=dtype, device=self.device)
+            else:
+                k, v = (_new(stream, shape, dtype, self.device) for _ in range(2))
         else:
             k, v = out
             for t in (k, v):
@@ -919,14 +937,15 @@ class KvCache:
         if step._index != self._index:
             self._refuse_step()
         if out is None:
-            out = self._empty(shape, dtype=q.dtype, device=self.device)
+            out = self._empty(shape, dtype=q.dtype, device=self.device) if stream is None \
+                else _new(stream, shape, q.dtype, self.device)
             orow, oh = heads * dim, dim
         else:
             orow, oh, od = out.stride()
             if out.dtype is not q.dtype or out.shape != shape or od != 1 or out.get_device() != self._index:
                 raise ValueError("out must have q's shape and type, dim contiguous, beside the cache")
         if with_lse:
-            lse = self._empty((rows, heads), dtype=self._float32, device=self.device)
+            lse = _new(stream, (rows, heads), self._float32, self.device)
             pl = lse.data_ptr()
         else:
             lse = pl = None
@@ -1031,16 +1050,16 @@ class Int4Matrix:
         None without zero points."""
         import torch
         groups = -(-self.K // self.group)
-        codes = torch.empty((self.M, self.K // 2), dtype=torch.uint8, device=self.device)
-        scales = torch.empty((self.M, groups), dtype=self.torch_dtype, device=self.device)
-        zeros = torch.empty((self.M, groups), dtype=torch.uint8, device=self.device) if self.has_zeros else None
+        codes = _new(stream, (self.M, self.K // 2), torch.uint8, self.device)
+        scales = _new(stream, (self.M, groups), self.torch_dtype, self.device)
+        zeros = _new(stream, (self.M, groups), torch.uint8, self.device) if self.has_zeros else None
         _check("bsp_q4_export", lib().bsp_q4_export(self.h, codes.data_ptr(), scales.data_ptr(),
                                                     zeros.data_ptr() if self.has_zeros else None, self._on(stream)))
         return codes, scales, zeros
 
     def decode(self, out=None, stream=None):
         """W as a dense tensor [M][K]: scale * (code - zero), rounded once."""
-        W = self._empty((self.M, self.K), dtype=self.torch_dtype, device=self.device) if out is None else out
+        W = _new(stream, (self.M, self.K), self.torch_dtype, self.device) if out is None else out
         if W.dtype is not self.torch_dtype or W.shape != (self.M, self.K) or not W.is_contiguous() \
                 or W.get_device() != self._index:
             raise ValueError("out must be a contiguous tensor [M][K] of the scales' type beside the matrix")
@@ -1056,7 +1075,7 @@ class Int4Matrix:
             return self._current(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def _rows(self, X, out):
+    def _rows(self, X, out, stream):
         """N, the rows' strides and the output of a product with X."""
         shape = X.shape
         if len(shape) != 2 or shape[1] != self.K or X.dtype is not self.torch_dtype or X.get_device() != self._index:
@@ -1066,7 +1085,10 @@ class Int4Matrix:
         if one != 1:
             raise ValueError("X must have contiguous rows")
         if out is None:
-            return N, xs, self._empty((N, self.M), dtype=self.torch_dtype, device=self.device), self.M
+            shape = (N, self.M)
+            out = self._empty(shape, dtype=self.torch_dtype, device=self.device) if stream is None \
+                else _new(stream, shape, self.torch_dtype, self.device)
+            return N, xs, out, self.M
         ys, one = out.stride()
         if (out.dtype is not self.torch_dtype or out.shape != (N, self.M) or (one != 1 and self.M > 1)
                 or out.get_device() != self._index):
@@ -1075,7 +1097,7 @@ class Int4Matrix:
 
     def mm(self, X, out=None, stream=None):
         """Y = W X: X [N][K], Y [N][M]."""
-        N, xs, Y, ys = self._rows(X, out)
+        N, xs, Y, ys = self._rows(X, out, stream)
         st = self._mm(self.h, X.data_ptr(), xs, N, Y.data_ptr(), ys, self._on(stream))
         if st:
             raise BspError("bsp_q4_mm", st)
@@ -1085,7 +1107,7 @@ class Int4Matrix:
         """Y = act(W X) * (W_up X), the first half of a gated feed-forward
         block whose gate is this matrix; ``activation`` a key of
         ``ACTIVATIONS``."""
-        N, xs, Y, ys = self._rows(X, out)
+        N, xs, Y, ys = self._rows(X, out, stream)
         try:
             act = ACTIVATIONS[activation]
         except KeyError:
@@ -1175,7 +1197,7 @@ class Rotary:
         except Exception:
             pass
 
-    def _of(self, name, x, out, rows, dtype):
+    def _of(self, name, x, out, rows, dtype, stream):
         """(the C description of x and its output, as bytes: a Structure costs as much as a launch; the output)"""
         shape = x.shape
         if len(shape) != 3 or shape[0] != rows or shape[2] != self.dim or x.dtype is not dtype \
@@ -1184,7 +1206,8 @@ class Rotary:
         xr, xh, xd = x.stride()
         heads = shape[1]
         if out is None:
-            out = self._empty(shape, dtype=dtype, device=self.device)
+            out = self._empty(shape, dtype=dtype, device=self.device) if stream is None \
+                else _new(stream, shape, dtype, self.device)
             orow, oh, od = heads * self.dim, self.dim, 1
         else:
             if out.shape != shape or out.dtype is not dtype or out.get_device() != self._index:
@@ -1216,9 +1239,9 @@ class Rotary:
         if not ok or stride != 1:
             raise ValueError(f"positions must be [axes][rows] = [{self.axes}][{rows}], rows contiguous")
         out_q, out_k = (None, None) if out is None else out
-        cq, out_q = self._of("q", q, out_q, rows, dtype)
+        cq, out_q = self._of("q", q, out_q, rows, dtype, stream)
         if k is not None:
-            ck, out_k = self._of("k", k, out_k, rows, dtype)
+            ck, out_k = self._of("k", k, out_k, rows, dtype, stream)
         st = self._apply(self.h, cq, ck if k is not None else None, dt, rows,
                          positions.data_ptr(), apart, int(inverse), self._on(stream))
         if st:
