@@ -159,7 +159,7 @@ class bsp_rope_desc_t(C.Structure):
                 ("freq", C.c_void_p), ("axis", C.c_void_p), ("scale", C.c_float)]
 
 
-class bsp_rope_rows_t(C.Structure):
+class bsp_rope_rows_t(C.Structure):  # with clear = 0, the four bytes behind heads
     _fields_ = [("in_", C.c_void_p), ("out", C.c_void_p), ("heads", C.c_int32), ("in_row", C.c_int64),
                 ("in_head", C.c_int64), ("out_row", C.c_int64), ("out_head", C.c_int64)]
 
@@ -1118,7 +1118,7 @@ class Int4Matrix:
         return Y
 
 
-_ROPE_ROWS = struct.Struct("@PPi4xqqqq").pack  # bsp_rope_rows_t
+_ROPE_ROWS = struct.Struct("@PPiiqqqq").pack  # bsp_rope_rows_t, clear behind heads
 
 
 class Rotary:
@@ -1205,7 +1205,8 @@ class Rotary:
             raise ValueError(f"{name} must be [rows][heads][{self.dim}] on {self.device}, q and k of one type")
         xr, xh, xd = x.stride()
         heads = shape[1]
-        if out is None:
+        made = out is None
+        if made:
             out = self._empty(shape, dtype=dtype, device=self.device) if stream is None \
                 else _new(stream, shape, dtype, self.device)
             orow, oh, od = heads * self.dim, self.dim, 1
@@ -1215,7 +1216,7 @@ class Rotary:
             orow, oh, od = out.stride()
         if xd != 1 or od != 1:
             raise ValueError(f"{name} and its output must have contiguous values")
-        return _ROPE_ROWS(x.data_ptr(), out.data_ptr(), heads, xr, xh, orow, oh), out
+        return _ROPE_ROWS(x.data_ptr(), out.data_ptr(), heads, made, xr, xh, orow, oh), out
 
     def apply(self, q, k, positions, out=None, inverse: bool = False, stream=None):
         """Turn rows ``q`` [rows][heads][dim] and ``k`` [rows][kv heads][dim]
@@ -1223,8 +1224,9 @@ class Rotary:
         ``positions``: [rows] with one axis, else [axes][rows].  ``out``: (q
         out, k out); ``out=(q, k)`` works in place, None allocates.  A row with a
         negative position on any axis (``KvStep.positions`` behind the last
-        row) is not written.  ``inverse`` turns back.  Returns (q out, k out),
-        or q out alone without k."""
+        row) is not written in an output given, and zeros in one allocated
+        here.  ``inverse`` turns back.  Returns (q out, k out), or q out alone
+        without k."""
         dtype, rows = q.dtype, q.shape[0]
         dt = _row_dtype(dtype)
         if positions.dtype is not self._int32 or positions.get_device() != self._index:

@@ -46,6 +46,7 @@ struct Rows {
     int64_t in_row, in_head, out_row, out_head;  // bytes
     int32_t heads;
     bool moves;  // the output is not the input
+    bool clear;  // rows that are not there become zeros
 };
 
 struct RopeArgs {
@@ -82,6 +83,13 @@ __device__ __forceinline__ void store(char* p, const Pack<T, N>& x)
 {
     using W = typename Word<N * sizeof(T)>::type;
     *reinterpret_cast<W*>(p) = *reinterpret_cast<const W*>(&x);
+}
+
+template <class T, int N>
+__device__ __forceinline__ void clear(char* p)
+{
+    using W = typename Word<N * sizeof(T)>::type;
+    *reinterpret_cast<W*>(p) = W{};
 }
 
 // threadIdx.x: the piece of a head (VEC pairs, or behind them the tail's
@@ -122,19 +130,25 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a)
             ++r;
         }
         if (r >= rows) return;
-        if (!there[r]) continue;
         const bool key = h0 + h >= a.x[0].heads;
         const Rows& x = a.x[key];
+        if (!there[r] && !x.clear) continue;
         const int hd = h0 + h - (key ? a.x[0].heads : 0);
         const char* in = x.in + (row0 + r) * x.in_row + hd * x.in_head;
         char* out = x.out + (row0 + r) * x.out_row + hd * x.out_head;
         if (piece >= pieces) {  // the values that do not turn
             const int64_t at = (2 * a.half + (piece - pieces) * 8) * (int64_t)sizeof(T);
-            if (x.moves) store<T, 8>(out + at, load<T, 8>(in + at));
+            if (!there[r]) clear<T, 8>(out + at);
+            else if (x.moves) store<T, 8>(out + at, load<T, 8>(in + at));
             continue;
         }
         const int64_t at0 = (INTERLEAVED ? 2 : 1) * piece * VEC * (int64_t)sizeof(T);
         const int64_t at1 = at0 + (INTERLEAVED ? VEC : a.half) * (int64_t)sizeof(T);
+        if (!there[r]) {
+            clear<T, VEC>(out + at0);
+            clear<T, VEC>(out + at1);
+            continue;
+        }
         Pack<T, VEC> u = load<T, VEC>(in + at0), v = load<T, VEC>(in + at1);
 #pragma unroll
         for (int i = 0; i < VEC / 2; ++i) {
@@ -352,7 +366,7 @@ bsp_status_t bsp_rope_apply(bsp_rope_t h, const bsp_rope_rows_t* q, const bsp_ro
     RopeArgs a = {};
     for (int i = 0; i < 2; ++i)
         a.x[i] = {(const char*)x[i].in, (char*)x[i].out,         2 * x[i].in_row, 2 * x[i].in_head, 2 * x[i].out_row,
-                  2 * x[i].out_head,    x[i].heads,              !same(x[i], rows)};
+                  2 * x[i].out_head,    x[i].heads,              !same(x[i], rows),  x[i].clear == 1};
     a.positions = positions;
     a.axis_stride = h->axes > 1 ? axis_stride : 0;
     a.rows = rows;

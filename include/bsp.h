@@ -838,6 +838,8 @@ typedef struct {
     const void *in;       /* device [rows][heads][dim], dim contiguous, 16-B aligned */
     void *out;            /* the same shape, aligned; may be `in` with in's strides  */
     int32_t heads;        /* 0: there is none (in and out are not looked at)         */
+    int32_t clear;        /* 1: rows of out that are not there become zeros; else they
+                             are left as they were                                   */
     int64_t in_row, in_head, out_row, out_head; /* strides in elements, multiples of 8
                              (any with one row, or one head); an output's rows and heads
                              do not overlap                                          */
@@ -847,8 +849,8 @@ typedef struct {
  * Turn the rows of q and k (either may have no heads, or be NULL) in one launch.
  *   positions device int32 [axes][rows], axis_stride entries apart (any with
  *          one axis).  A row with a negative position on any axis is not there:
- *          its output is left as it was (bsp_kv_plan's positions are -1 behind
- *          the step's last row).
+ *          its output is left as it was, or becomes zeros (`clear`; bsp_kv_plan's
+ *          positions are -1 behind the step's last row).
  *   inverse  1: by -p instead (the rotation undone, but for s twice; also its
  *          gradient).
  * fp32 arithmetic, rounded once; the angle is reduced exactly, whatever the
