@@ -3,10 +3,11 @@
 //
 // A pair's angle is positions[axis] * freq.  Far positions lose an angle held
 // in fp32 (at 10^6 its last bit is 0.06 radians), so the handle keeps each
-// frequency in turns as a 64-bit fraction, F = freq / (2 pi) 2^64 mod 2^64:
-// position * F in 64-bit integers drops whole turns exactly, and its upper
-// half, read as signed, is the angle in 2^-32 turns.  Error: position 2^-65
-// turns, and the one rounding to fp32.
+// frequency in turns as a 64-bit fraction, F = freq / (2 pi) 2^64 mod 2^64 to
+// the nearest: position * F in 64-bit integers drops whole turns exactly, and
+// read as signed it is the angle in 2^-64 turns, rounded once to fp32 (so
+// that a small angle keeps its relative accuracy).  Error: position 2^-65
+// turns, and the one rounding.
 //
 // A block makes the cosines and sines of its rows once, in shared memory,
 // and then passes over the heads: a thread takes VEC pairs (two 16-byte
@@ -112,9 +113,9 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a)
     for (int i = tid; i < rows * a.half; i += threads) {
         const int r = i / a.half, p = i - r * a.half;
         const uint32_t pos = (uint32_t)a.positions[(a.axes > 1 ? a.axis[p] : 0) * a.axis_stride + row0 + r];
-        const uint32_t up = (uint32_t)(((uint64_t)pos * a.turns[p]) >> 32);
+        const int64_t turn = (int64_t)((uint64_t)pos * a.turns[p]);
         float s, c;
-        sincospif((float)(int32_t)up * 0x1p-31f, &s, &c);
+        sincospif((float)turn * 0x1p-63f, &s, &c);
         reinterpret_cast<float2*>(table)[((r * (VEC / 2) + p % VEC / 2) * pieces + p / VEC) * 2 + (p & 1)] =
             make_float2(c * a.scale, s * a.scale * a.sign);
     }
@@ -200,15 +201,15 @@ void free_rope(bsp_rope* h)
     delete h;
 }
 
-// freq / (2 pi) 2^64 mod 2^64: the quotient as an unevaluated sum of two
-// doubles (1 / (2 pi) has two terms), whose whole turns drop out.
+// freq / (2 pi) 2^64 mod 2^64, to the nearest: the quotient as an unevaluated
+// sum of two doubles (1 / (2 pi) has two terms), whose whole turns drop out.
 uint64_t turns_of(double freq)
 {
     if (freq < 0) return 0 - turns_of(-freq);
     const double inv = 0x1.45f306dc9c883p-3, inv_rest = -0x1.6b01ec5417056p-57;
     const double t = freq * inv, rest = std::fma(freq, inv, -t) + freq * inv_rest;
-    const double part = t - std::floor(t);  // exact
-    return (uint64_t)std::ldexp(part, 64) + (uint64_t)std::llrint(std::ldexp(rest, 64));
+    const double part = std::ldexp(t - std::floor(t), 64), whole = std::floor(part);  // exact
+    return (uint64_t)whole + (uint64_t)std::llrint(part - whole + std::ldexp(rest, 64));
 }
 
 // A row tensor's memory as strided pieces: by rows where heads lie inside

@@ -853,8 +853,8 @@ typedef struct {
  *          positions are -1 behind the step's last row).
  *   inverse  1: by -p instead (the rotation undone, but for s twice; also its
  *          gradient).
- * fp32 arithmetic, rounded once; the angle is reduced exactly, whatever the
- * position.  An output is its own input, element for element, or shares no
+ * fp32 arithmetic, rounded once; the angle, less its whole turns, is within position
+ * 2^-65 turns and one rounding to fp32 of positions * freq.  An output is its own input, element for element, or shares no
  * memory with either input or the other output (BSP_ERR_INVALID_ARG; slices
  * of the same rows do not).
  * Asynchronous, allocates nothing; calls on one handle may run at the same time.

@@ -26,8 +26,8 @@ def rotate(x, positions, freqs, axis, interleaved: bool, scale: float = 1.0, inv
 
 def bound(x, want, rot: int, dtype: str, scale: float = 1.0, interleaved: bool = False, turn: float = 2.0 ** -25):
     """Bound of the kernel's error: the angle is off by at most one fp32
-    rounding of half a turn (pi 2^-24) and by `turn` turns of the fixed point
-    (2^-32, rounded down, and position 2^-65), sine and cosine by 2^-22, the
+    rounding of half a turn (pi 2^-24) and by the fixed point (position 2^-65
+    turns, at most 2^-34; 2^-31 is allowed, `turn` 2^-6), sine and cosine by 2^-22, the
     three products and sum by 2^-22 of |a| + |b| together; then one rounding
     to the type (half a step, eps / 2; its subnormals)."""
     half = rot // 2
