@@ -87,13 +87,16 @@ __device__ __forceinline__ float half_of(uint32_t pair, int high)
     return to_float(*reinterpret_cast<const T*>(&bits));
 }
 
-// Pairs of the dtype from a word of codes: c - z of rows g (a[0], a[2]), and UPPER
-// times that of rows g + 8; z0 and z1 are the pairs that bias() makes.
+// Pairs of the dtype from a word of codes: UNIT (c - z) of rows g (a[0],
+// a[2]), and UPPER times as much of rows g + 8; z0 and z1 are the pairs that
+// bias() makes.  Outputs are divided by UNIT, a power of two: bf16 codes are
+// that small so that a group's sum before its scale, at most 128 x 15 x 2^-11
+// of the largest activation, is finite wherever the activations are.
 template <class T>
 struct Codes;
 template <>
 struct Codes<__half> {
-    static constexpr float UPPER = 16.f;
+    static constexpr float UNIT = 1.f, UPPER = 16.f;
     static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b)
     {
         const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -115,7 +118,7 @@ struct Codes<__half> {
 };
 template <>
 struct Codes<__nv_bfloat16> {
-    static constexpr float UPPER = 1.f;
+    static constexpr float UNIT = 0x1p-11f, UPPER = 1.f;
     static __device__ __forceinline__ uint32_t less(uint32_t a, uint32_t b)
     {
         const __nv_bfloat162 d =
@@ -124,13 +127,13 @@ struct Codes<__nv_bfloat16> {
     }
     static __device__ __forceinline__ void bias(uint32_t zeros, uint32_t& z0, uint32_t& z1)
     {
-        z0 = (zeros & 15u) * 0x10001u | 0x43004300u;
-        z1 = (zeros >> 4) * 0x10001u | 0x43004300u;
+        z0 = (zeros & 15u) * 0x10001u | 0x3D803D80u;
+        z1 = (zeros >> 4) * 0x10001u | 0x3D803D80u;
     }
     static __device__ __forceinline__ void widen(uint32_t w, uint32_t z0, uint32_t z1, uint32_t (&a)[4])
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = less(((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, i & 1 ? z1 : z0);
+        for (int i = 0; i < 4; ++i) a[i] = less(((w >> (4 * i)) & 0x000F000Fu) | 0x3D803D80u, i & 1 ? z1 : z0);
     }
 };
 

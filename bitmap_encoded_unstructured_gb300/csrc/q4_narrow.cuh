@@ -10,7 +10,8 @@
 //   fp16: a masked nibble under the exponent of 1024 is 1024 + c, or 1024 +
 //   16 c in the second nibble, which belongs to the tile's upper rows and so
 //   to sums of their own; one subtraction of two values takes the rest away,
-//   and the 16 goes into the scale.  bf16: 128 + c.
+//   and the 16 comes off at the end.  bf16: the same with 2^-4 + 2^-11 c, for the
+//   range of its sums (bsp_q4.cuh).
 //   (A masked nibble alone, a subnormal, needs no subtraction, but tensor
 //   cores align subnormals as if they had the smallest normal exponent: the sums
 //   lose ten bits.)
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 parts[((warp * RT + r) * COLS + 8 * nt + 2 * t + (e & 1)) * 17 + g + 8 * (e >> 1)] =
-                    e < 2 ? out[r][nt][e] : out[r][nt][e] * (1.f / Codes<T>::UPPER);
+                    out[r][nt][e] * ((e < 2 ? 1.f : 1.f / Codes<T>::UPPER) / Codes<T>::UNIT);
     __syncthreads();
     for (int i = threadIdx.x; i < RT * COLS * 16; i += THREADS) {
         float v = 0.f;

@@ -578,6 +578,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         tc_before();
         __syncwarp();
         if (lane == 0) bspx::mbar_arrive(read);
+        constexpr float OUT = 1.f / Codes<T>::UNIT;
         const int64_t m = strip * BM + row;
         T* y = reinterpret_cast<T*>(a.y) + m;
         float* part = reinterpret_cast<float*>(smem);  // over the rings: every product is done
@@ -587,7 +588,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             if (!failed && m < a.M)
 #pragma unroll
                 for (int i = 0; i < C::COLS; ++i)
-                    if (n0 + c0 + i < a.N) y[(n0 + c0 + i) * a.y_stride] = from_float<T>(sum[i]);
+                    if (n0 + c0 + i < a.N) y[(n0 + c0 + i) * a.y_stride] = from_float<T>(sum[i] * OUT);
             bspx::cluster_sync();
         } else if (shares == 1) {
             // ---------------- gate and up meet: of every thread's columns the
@@ -607,7 +608,7 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             const float* up = own + (half ? 0 : BN / 2 * BM);
             if (!failed && m < a.M)
 #pragma unroll 4
-                for (int i = 0; i < last; ++i) y[(n1 + i) * a.y_stride] = from_float<T>(activate(gate[i * BM], a.act) * up[i * BM]);
+                for (int i = 0; i < last; ++i) y[(n1 + i) * a.y_stride] = from_float<T>(activate(gate[i * BM] * OUT, a.act) * (up[i * BM] * OUT));
             bspx::cluster_sync();
         } else {
             // ---------------- parts to shared memory, [column][row], and their sums
@@ -643,6 +644,8 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                         v[j].w += x[j].w;
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = make_float4(v[j].x * OUT, v[j].y * OUT, v[j].z * OUT, v[j].w * OUT);
             };
 #pragma unroll 1
             for (int c = from_col + p; c < to_col && !failed; c += 4 * C::PW) {

@@ -789,7 +789,8 @@ bsp_status_t bsp_q4_destroy(bsp_q4_t h);
  * aligned.  N = 0 does nothing.  X and Y share no memory
  * (BSP_ERR_INVALID_ARG; two slices of one tensor's rows do not).  Sums are
  * fp32 and the scales are applied to the sums of whole groups: weights are
- * not rounded, and Y is rounded once.  The same call gives the same bits.
+ * not rounded, and Y is rounded once.  A group's sum before its scale is
+ * finite for all finite X.  The same call gives the same bits.
  * Asynchronous, allocates nothing.
  */
 bsp_status_t bsp_q4_mm(bsp_q4_t h, const void *X, int64_t x_stride, int64_t N, void *Y, int64_t y_stride,
