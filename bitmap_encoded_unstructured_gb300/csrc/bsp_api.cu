@@ -54,7 +54,7 @@ bsp_status_t grow(void** p, size_t* have, size_t need)
     cudaFree(*p);
     *p = nullptr;
     *have = 0;
-    if (cudaMalloc(p, need) != cudaSuccess) { *p = nullptr; return BSP_ERR_OOM; }
+    if (bsp_malloc(p, need) != cudaSuccess) { *p = nullptr; return BSP_ERR_OOM; }
     *have = need;
     return BSP_OK;
 }
@@ -64,8 +64,8 @@ bsp_status_t alloc_scratch(bsp_handle* h, cudaStream_t s)
 {
     const size_t ws_bytes = (size_t)BSP_DECODE_MAX_N * (size_t)h->M * 4;
     const size_t cnt_bytes = (size_t)(h->Mp / 64) * 4;
-    if (cudaMalloc(&h->ws, ws_bytes) != cudaSuccess || cudaMalloc(&h->counters, cnt_bytes) != cudaSuccess ||
-        cudaMalloc(&h->err, sizeof(int)) != cudaSuccess)
+    if (bsp_malloc(&h->ws, ws_bytes) != cudaSuccess || bsp_malloc(&h->counters, cnt_bytes) != cudaSuccess ||
+        bsp_malloc(&h->err, sizeof(int)) != cudaSuccess)
         return BSP_ERR_OOM;
     if (cudaMemsetAsync(h->ws, 0, ws_bytes, s) != cudaSuccess ||
         cudaMemsetAsync(h->counters, 0, cnt_bytes, s) != cudaSuccess ||
@@ -336,7 +336,7 @@ bsp_status_t bsp_set_deterministic(bsp_handle_t h, int on)
         if (!g.ok) return BSP_ERR_CUDA;
         const int slots = bsp_decode_split_cap(bsp_problem_of(h));
         const size_t bytes = (size_t)slots * BSP_DECODE_MAX_N * (size_t)h->M * 4;
-        if (cudaMalloc(&h->ws_det, bytes) != cudaSuccess) {
+        if (bsp_malloc(&h->ws_det, bytes) != cudaSuccess) {
             h->ws_det = nullptr;
             return BSP_ERR_OOM;
         }
@@ -382,9 +382,9 @@ bsp_status_t bsp_import(const uint64_t* bitmaps, const uint32_t* offsets, const 
     const int eb = bsp_elem_bytes(dtype);
     h->NNZ = nnz;
     h->values_alloc = ((size_t)nnz * eb + 16 + 15) & ~(size_t)15;
-    if (cudaMalloc(&h->bitmaps, (size_t)h->NBT * 8) != cudaSuccess ||
-        cudaMalloc(&h->offsets, (size_t)(h->NGT + 1) * 4) != cudaSuccess ||
-        cudaMalloc(&h->values, h->values_alloc) != cudaSuccess) {
+    if (bsp_malloc(&h->bitmaps, (size_t)h->NBT * 8) != cudaSuccess ||
+        bsp_malloc(&h->offsets, (size_t)(h->NGT + 1) * 4) != cudaSuccess ||
+        bsp_malloc(&h->values, h->values_alloc) != cudaSuccess) {
         free_handle(h);
         return BSP_ERR_OOM;
     }

@@ -53,6 +53,20 @@ struct bsp_handle {
     size_t stage_y_bytes;
 };
 
+// cudaMalloc whose failure is this call's own: the runtime's last error is
+// cleared, so that the checks of later launches (the library's, or the
+// caller's) do not find it.
+template <class T>
+static inline cudaError_t bsp_malloc(T** p, size_t bytes)
+{
+    const cudaError_t e = cudaMalloc(p, bytes);
+    if (e != cudaSuccess) {
+        *p = nullptr;
+        cudaGetLastError();
+    }
+    return e;
+}
+
 static inline int bsp_elem_bytes(bsp_dtype_t d) { return d == BSP_INT8 ? 1 : 2; }
 
 // Output modes of the decode-path kernel.

@@ -328,11 +328,11 @@ bsp_status_t bsp_run_encode(bsp_handle* h, const void* W, cudaStream_t s)
     uint32_t total = 0;
     int ovf = 0, maxc = 0;
 
-    if (cudaMalloc(&h->bitmaps, (size_t)h->NBT * 8) != cudaSuccess ||
-        cudaMalloc(&h->offsets, (size_t)(h->NGT + 1) * 4) != cudaSuccess ||
-        cudaMalloc(&bt_prefix, (size_t)h->NBT * 4) != cudaSuccess ||
-        cudaMalloc(&gt_nnz, (size_t)h->NGT * 4) != cudaSuccess ||
-        cudaMalloc(&overflow, 2 * sizeof(int)) != cudaSuccess) {  // overflow flag, largest GT count
+    if (bsp_malloc(&h->bitmaps, (size_t)h->NBT * 8) != cudaSuccess ||
+        bsp_malloc(&h->offsets, (size_t)(h->NGT + 1) * 4) != cudaSuccess ||
+        bsp_malloc(&bt_prefix, (size_t)h->NBT * 4) != cudaSuccess ||
+        bsp_malloc(&gt_nnz, (size_t)h->NGT * 4) != cudaSuccess ||
+        bsp_malloc(&overflow, 2 * sizeof(int)) != cudaSuccess) {  // overflow flag, largest GT count
         st = BSP_ERR_OOM;
         goto done;
     }
@@ -359,7 +359,7 @@ bsp_status_t bsp_run_encode(bsp_handle* h, const void* W, cudaStream_t s)
     // values + at least 16 zeroed bytes of tail slack, so that 16-byte
     // vector loads of the last span never leave the allocation
     h->values_alloc = ((size_t)total * eb + 16 + 15) & ~(size_t)15;
-    if (cudaMalloc(&h->values, h->values_alloc) != cudaSuccess) { st = BSP_ERR_OOM; goto done; }
+    if (bsp_malloc(&h->values, h->values_alloc) != cudaSuccess) { st = BSP_ERR_OOM; goto done; }
     if (cudaMemsetAsync(h->values, 0, h->values_alloc, s) != cudaSuccess) { st = BSP_ERR_CUDA; goto done; }
     if (eb == 2)
         enc_pack_kernel<2><<<grid_for(n_rowbytes, 256), 256, 0, s>>>(W, n_rowbytes, sh, h->bitmaps, h->offsets,
@@ -403,7 +403,7 @@ bsp_status_t bsp_run_validate(bsp_handle* h, cudaStream_t s)
     int hbad = 0, maxc = 0;
     uint32_t last = 0;
     bsp_status_t st = BSP_OK;
-    if (cudaMalloc(&bad, 2 * sizeof(int)) != cudaSuccess) return BSP_ERR_OOM;
+    if (bsp_malloc(&bad, 2 * sizeof(int)) != cudaSuccess) return BSP_ERR_OOM;
     if (cudaMemsetAsync(bad, 0, 2 * sizeof(int), s) != cudaSuccess) { st = BSP_ERR_CUDA; goto done; }
     validate_kernel<<<grid_for(h->NGT * 32, 256), 256, 0, s>>>(h->bitmaps, h->offsets, h->NGT, h->M, h->K,
                                                                h->Kp / 64, bad);

@@ -1054,8 +1054,8 @@ bsp_status_t attention_setup(bsp_kv* h, cudaStream_t s)
                         : c.dim <= 128 ? std::max(floats(DecCfg<128, 1>{}), floats(DecCfg<128, 3>{}))
                                        : floats(DecCfg<256, 2>{});
     h->part_floats = (size_t)h->num_sms * DEC_WARPS * 2 * part;
-    if (cudaMalloc(&h->parts, h->part_floats * sizeof(float)) != cudaSuccess ||
-        cudaMalloc(&h->cuts, workers * sizeof(KvCut)) != cudaSuccess)
+    if (bsp_malloc(&h->parts, h->part_floats * sizeof(float)) != cudaSuccess ||
+        bsp_malloc(&h->cuts, workers * sizeof(KvCut)) != cudaSuccess)
         return BSP_ERR_OOM;
     if (cudaMemsetAsync(h->cuts, 0, workers * sizeof(KvCut), s) != cudaSuccess) return BSP_ERR_CUDA;
     return BSP_OK;

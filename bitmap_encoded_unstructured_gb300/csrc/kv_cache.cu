@@ -512,7 +512,7 @@ bsp_status_t bsp_kv_create(const bsp_kv_desc_t* d, bsp_stream_t stream, bsp_kv_t
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess)
         st = BSP_ERR_CUDA;
-    else if (cudaMalloc(&h->ticket, 2 * sizeof(int)) != cudaSuccess || cudaMalloc(&h->err, sizeof(int)) != cudaSuccess)
+    else if (bsp_malloc(&h->ticket, 2 * sizeof(int)) != cudaSuccess || bsp_malloc(&h->err, sizeof(int)) != cudaSuccess)
         st = BSP_ERR_OOM;
     else if (cudaMemsetAsync(h->ticket, 0, 2 * sizeof(int), s) != cudaSuccess ||
              cudaMemsetAsync(h->err, 0, sizeof(int), s) != cudaSuccess)

@@ -256,7 +256,7 @@ bsp_status_t check_shape(bsp_dtype_t dtype, int64_t M, int64_t K, int32_t group)
 struct Temp {
     void* p = nullptr;
     ~Temp() { cudaFree(p); }
-    bool get(size_t n) { return cudaMalloc(&p, n ? n : 1) == cudaSuccess; }
+    bool get(size_t n) { return bsp_malloc(&p, n ? n : 1) == cudaSuccess; }
 };
 
 // A handle from plain device arrays; synchronises s.
@@ -278,8 +278,8 @@ bsp_status_t build(bsp_dtype_t dtype, int64_t M, int64_t K, int32_t group, const
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess)
         st = BSP_ERR_CUDA;
-    else if (cudaMalloc(&h->codes, lanes * 16) != cudaSuccess || cudaMalloc(&h->scales, pairs * 4) != cudaSuccess ||
-             (zeros && cudaMalloc(&h->zeros, pairs) != cudaSuccess) || cudaMalloc(&h->err, sizeof(int)) != cudaSuccess)
+    else if (bsp_malloc(&h->codes, lanes * 16) != cudaSuccess || bsp_malloc(&h->scales, pairs * 4) != cudaSuccess ||
+             (zeros && bsp_malloc(&h->zeros, pairs) != cudaSuccess) || bsp_malloc(&h->err, sizeof(int)) != cudaSuccess)
         st = BSP_ERR_OOM;
     else {
         q4_pack_kernel<<<blocks_for(lanes), BLOCK, 0, s>>>(codes, M, K, h->k_tiles, lanes, h->codes);

@@ -309,7 +309,7 @@ bsp_status_t bsp_rope_create(const bsp_rope_desc_t* d, bsp_stream_t stream, bsp_
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess)
         st = BSP_ERR_CUDA;
-    else if (cudaMalloc(&h->turns, half * sizeof(uint64_t)) != cudaSuccess || cudaMalloc(&h->axis, half) != cudaSuccess)
+    else if (bsp_malloc(&h->turns, half * sizeof(uint64_t)) != cudaSuccess || bsp_malloc(&h->axis, half) != cudaSuccess)
         st = BSP_ERR_OOM;
     else if (cudaMemcpyAsync(h->turns, turns, half * sizeof(uint64_t), cudaMemcpyHostToDevice, s) != cudaSuccess ||
              cudaMemcpyAsync(h->axis, axis, half, cudaMemcpyHostToDevice, s) != cudaSuccess ||

@@ -432,10 +432,10 @@ bsp_status_t bsp_run_build_cbc(bsp_handle* h, cudaStream_t s)
         cudaFree(values);
         return e;
     };
-    if (cudaMalloc(&W, (size_t)h->M * h->K * eb) != cudaSuccess || cudaMalloc(&colnnz, ncols * 4) != cudaSuccess ||
-        cudaMalloc(&tile_nnz, ngt * 4) != cudaSuccess || cudaMalloc(&overflow, sizeof(int)) != cudaSuccess ||
-        cudaMalloc(&offsets, (ngt + 1) * 4) != cudaSuccess || cudaMalloc(&colinfo, ncols * 4) != cudaSuccess ||
-        cudaMalloc(&bitmaps, ncols * WORDS * 8) != cudaSuccess)
+    if (bsp_malloc(&W, (size_t)h->M * h->K * eb) != cudaSuccess || bsp_malloc(&colnnz, ncols * 4) != cudaSuccess ||
+        bsp_malloc(&tile_nnz, ngt * 4) != cudaSuccess || bsp_malloc(&overflow, sizeof(int)) != cudaSuccess ||
+        bsp_malloc(&offsets, (ngt + 1) * 4) != cudaSuccess || bsp_malloc(&colinfo, ncols * 4) != cudaSuccess ||
+        bsp_malloc(&bitmaps, ncols * WORDS * 8) != cudaSuccess)
         st = BSP_ERR_OOM;
     if (st == BSP_OK) st = bsp_run_decode(h, W, s);
     if (st == BSP_OK) {
@@ -455,7 +455,7 @@ bsp_status_t bsp_run_build_cbc(bsp_handle* h, cudaStream_t s)
         st = BSP_ERR_CUDA;
     if (st == BSP_OK && (ovf || total != h->NNZ)) st = BSP_ERR_INTERNAL;  // the same nonzeros as the handle
     const size_t vbytes = ((size_t)total * eb + 16 + 15) & ~(size_t)15;
-    if (st == BSP_OK && cudaMalloc(&values, vbytes) != cudaSuccess) st = BSP_ERR_OOM;
+    if (st == BSP_OK && bsp_malloc(&values, vbytes) != cudaSuccess) st = BSP_ERR_OOM;
     if (st == BSP_OK) {
         if (cudaMemsetAsync(values, 0, vbytes, s) != cudaSuccess) st = BSP_ERR_CUDA;
         if (eb == 2)

@@ -546,7 +546,7 @@ namespace {
 bsp_status_t solve_perms(bsp_union* h, const int8_t* W, int64_t KT, cudaStream_t s)
 {
     uint64_t* act = nullptr;
-    if (cudaMalloc(&act, (size_t)h->NLT * LT * 8) != cudaSuccess) return BSP_ERR_OOM;
+    if (bsp_malloc(&act, (size_t)h->NLT * LT * 8) != cudaSuccess) return BSP_ERR_OOM;
     ub_rowact_kernel<<<blocks_for(h->NLT * 32, 256), 256, 0, s>>>(W, h->M, h->K, KT, h->NLT, act);
     std::vector<uint64_t> hact((size_t)h->NLT * LT);
     const bool ok = cudaGetLastError() == cudaSuccess &&
@@ -569,7 +569,7 @@ bsp_status_t solve_perms(bsp_union* h, const int8_t* W, int64_t KT, cudaStream_t
             }
         });
     for (auto& th : pool) th.join();
-    if (cudaMalloc(&h->perms, hperm.size()) != cudaSuccess) return BSP_ERR_OOM;
+    if (bsp_malloc(&h->perms, hperm.size()) != cudaSuccess) return BSP_ERR_OOM;
     if (cudaMemcpyAsync(h->perms, hperm.data(), hperm.size(), cudaMemcpyHostToDevice, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return BSP_ERR_CUDA;
@@ -611,11 +611,11 @@ bsp_status_t union_encode(const int8_t* W, int bits, int64_t M, int64_t K, bool 
         st = BSP_ERR_CUDA;
         goto done;
     }
-    if (cudaMalloc(&h->masks, (size_t)h->NLT * 128) != cudaSuccess ||
-        cudaMalloc(&h->offsets, (size_t)(h->NLT + 1) * 4) != cudaSuccess ||
-        cudaMalloc(&counts, (size_t)h->NLT * 4) != cudaSuccess || cudaMalloc(&flags, 2 * sizeof(int)) != cudaSuccess ||
-        cudaMalloc(&nnz, sizeof(unsigned long long)) != cudaSuccess || cudaMalloc(&h->ws, ws_bytes) != cudaSuccess ||
-        cudaMalloc(&h->counters, cnt_bytes) != cudaSuccess || cudaMalloc(&h->err, sizeof(int)) != cudaSuccess) {
+    if (bsp_malloc(&h->masks, (size_t)h->NLT * 128) != cudaSuccess ||
+        bsp_malloc(&h->offsets, (size_t)(h->NLT + 1) * 4) != cudaSuccess ||
+        bsp_malloc(&counts, (size_t)h->NLT * 4) != cudaSuccess || bsp_malloc(&flags, 2 * sizeof(int)) != cudaSuccess ||
+        bsp_malloc(&nnz, sizeof(unsigned long long)) != cudaSuccess || bsp_malloc(&h->ws, ws_bytes) != cudaSuccess ||
+        bsp_malloc(&h->counters, cnt_bytes) != cudaSuccess || bsp_malloc(&h->err, sizeof(int)) != cudaSuccess) {
         st = BSP_ERR_OOM;
         goto done;
     }
@@ -647,7 +647,7 @@ bsp_status_t union_encode(const int8_t* W, int bits, int64_t M, int64_t K, bool 
     h->value_bytes = ((uint64_t)total * (uint64_t)bits + 7) / 8;
     // 32 zeroed bytes of slack: the product's copies and four-value fetches
     // read up to 16 B past the last span
-    if (cudaMalloc(&h->values, h->value_bytes + 32) != cudaSuccess) { st = BSP_ERR_OOM; goto done; }
+    if (bsp_malloc(&h->values, h->value_bytes + 32) != cudaSuccess) { st = BSP_ERR_OOM; goto done; }
     if (cudaMemsetAsync(h->values, 0, h->value_bytes + 32, s) != cudaSuccess) { st = BSP_ERR_CUDA; goto done; }
     ub_pack_kernel<<<blocks_for(h->NLT * 32, 256), 256, 0, s>>>(W, M, K, KT, h->NLT, bits, h->perms,
                                                                 reinterpret_cast<const uint32_t*>(h->masks),
