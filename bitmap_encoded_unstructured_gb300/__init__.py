@@ -481,7 +481,8 @@ class BitmapMatrix:
 
         def ptr(a):
             if isinstance(a, np.ndarray):
-                return np.ascontiguousarray(a).ctypes.data, a
+                a = np.ascontiguousarray(a)  # kept: the pointer is the copy's
+                return a.ctypes.data, a
             a = _contiguous(a, stream)
             return a.data_ptr(), a
 

@@ -1,0 +1,23 @@
+"""What the binding hands to the library, without a device: the library's entry is replaced by one that looks at it."""
+import ctypes as C
+import types
+
+import numpy as np
+import pytest
+import torch
+
+import bitmap_encoded_unstructured_gb300 as bsp
+
+
+def test_bitmap_from_strided_numpy_arrays(monkeypatch):
+    """The copies that the pointers point to live until the call returns."""
+    g = np.random.default_rng(1)
+    arrays = [g.integers(0, 1 << 30, (n, 2)).astype(t)[:, 0] for n, t in ((900, np.uint64), (900, np.uint64), (3600, np.uint16))]
+
+    def look(bitmaps, offsets, values, *rest):
+        for a, p in zip(arrays, (bitmaps, offsets, values)):
+            assert C.string_at(p, a.nbytes) == a.tobytes()
+        return 0
+
+    monkeypatch.setattr(bsp, "bsp_import", look)
+    bsp.BitmapMatrix.from_arrays(*arrays, 64, 64, device="cuda:0", stream=0)
