@@ -1002,6 +1002,8 @@ class Int4Matrix:
         if device is None:
             device = codes.device if codes.is_cuda else torch.device("cuda", torch.cuda.current_device())
         device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("device must be a GPU: the matrix lives there, wherever its arrays are")
         if device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
         if any(t is not None and t.is_cuda and t.device != device for t in (codes, scales, zeros)):

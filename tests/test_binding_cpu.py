@@ -21,3 +21,10 @@ def test_bitmap_from_strided_numpy_arrays(monkeypatch):
 
     monkeypatch.setattr(bsp, "bsp_import", look)
     bsp.BitmapMatrix.from_arrays(*arrays, 64, 64, device="cuda:0", stream=0)
+
+
+def test_int4_from_arrays_refuses_another_kind_of_device():
+    """(It went to the current GPU.)"""
+    with pytest.raises(ValueError, match="GPU"):
+        bsp.Int4Matrix.from_arrays(torch.zeros((4, 32), dtype=torch.uint8), torch.zeros((4, 2), dtype=torch.float16), group=32,
+                                   device="cpu")
