@@ -1144,7 +1144,10 @@ class Rotary:
         if axis is not None and sections is not None:
             raise ValueError("axis or sections, not both")
         if sections is not None:
-            axis = self._axes_of(list(sections), cyclic)
+            sections = [int(n) for n in sections]
+            if any(n < 0 for n in sections):
+                raise ValueError("sections are numbers of pairs")
+            axis = self._axes_of(sections, cyclic)
         axis = [0] * half if axis is None else [int(a) for a in axis]
         if len(axis) != half or any(not 0 <= a < 8 for a in axis):
             raise ValueError(f"every one of the {half} pairs needs an axis, 0 to 7")
@@ -1163,7 +1166,7 @@ class Rotary:
             raise ValueError(f"{half} pairs need as many frequencies")
         self.dim, self.rot, self.axes, self.interleaved = int(dim), int(rot), max(axis, default=0) + 1, bool(interleaved)
         if sections is not None:
-            self.axes = len(list(sections))
+            self.axes = len(sections)
         self.freqs, self.axis, self.scale = freqs, axis, float(scale)
         f, a = (C.c_double * max(1, half))(*freqs), (C.c_uint8 * max(1, half))(*axis)
         d = bsp_rope_desc_t(self.dim, self.rot, self.axes, int(self.interleaved), C.addressof(f), C.addressof(a),
