@@ -53,6 +53,22 @@ struct bsp_handle {
     size_t stage_y_bytes;
 };
 
+// Run on the handle's device, restoring the caller's current device after.
+struct DeviceGuard {
+    int prev = -1;
+    bool ok = true;
+    explicit DeviceGuard(int dev)
+    {
+        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
+        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+    }
+    ~DeviceGuard()
+    {
+        int cur = -1;
+        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+    }
+};
+
 // cudaMalloc whose failure is this call's own: the runtime's last error is
 // cleared, so that the checks of later launches (the library's, or the
 // caller's) do not find it.

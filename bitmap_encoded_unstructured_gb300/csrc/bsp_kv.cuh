@@ -57,22 +57,6 @@ namespace bspkv {
 inline bool valid(const bsp_kv* h) { return h != nullptr && h->magic == BSP_KV_MAGIC; }
 inline bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
-// Run on the handle's device, restoring the caller's current device after.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
 // Rows of a call and rows a block table row can name: positions, and their
 // differences to a window, stay in 32 bits.
 constexpr int64_t MOST_ROWS = (int64_t)1 << 30;

@@ -85,7 +85,7 @@ struct Wide {
 struct WideArgs {
     Q4View w[2];
     int act;
-    int64_t M, N, groups, strips;
+    int64_t M, N, strips;
     int32_t k_tiles, ntiles;
     void* y;
     int64_t y_stride;
@@ -719,7 +719,6 @@ bsp_status_t launch_wide(const Problem& p, int shares, cudaStream_t s)
     a.act = p.act;
     a.M = p.M;
     a.N = p.N;
-    a.groups = p.k_tiles * 64 / G;
     a.strips = p.strips;
     a.k_tiles = (int32_t)p.k_tiles;
     a.ntiles = (int32_t)((p.N + BN - 1) / BN);

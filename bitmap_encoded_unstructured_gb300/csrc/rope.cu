@@ -177,21 +177,6 @@ __global__ void __launch_bounds__(THREADS) rope_kernel(const RopeArgs a)
 bool valid(const bsp_rope* h) { return h != nullptr && h->magic == BSP_ROPE_MAGIC; }
 bool aligned(const void* p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) == 0; }
 
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
 void free_rope(bsp_rope* h)
 {
     if (!h) return;

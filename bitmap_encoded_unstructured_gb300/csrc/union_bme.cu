@@ -63,21 +63,6 @@ constexpr uint32_t FULL = 0xFFFFFFFFu;
 bool valid(const bsp_union* h) { return h != nullptr && h->magic == BSP_UNION_MAGIC; }
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
 inline unsigned blocks_for(int64_t n, int block) { return (unsigned)((n + block - 1) / block); }
 
 __device__ __forceinline__ int w_at(const int8_t* W, int64_t M, int64_t K, int64_t r, int64_t c)
