@@ -137,23 +137,16 @@ struct Codes<__nv_bfloat16> {
     }
 };
 
-// g / (1 + exp(-y)) for y of g's sign, from exp(-|y|): exp(-y) itself would be
-// infinite from y = -88.7 on, where the quotient is still far from 0 in bf16.
-__device__ __forceinline__ float times_sigmoid(float g, float y)
-{
-    const float e = __expf(-fabsf(y));
-    return (y < 0.f ? g * e : g) / (1.f + e);
-}
-
 __device__ __forceinline__ float activate(float g, int act)
 {
-    switch (act) {
-    case BSP_ACT_SILU: return times_sigmoid(g, g);
-    case BSP_ACT_GELU: return 0.5f * g * erfcf(-0.70710678118654752f * g);
-    // 0.5 (1 + tanh(y)) = 1 / (1 + exp(-2 y))
-    case BSP_ACT_GELU_TANH: return times_sigmoid(g, 1.59576912160573071f * (g + 0.044715f * g * g * g));
-    default: return g != g ? g : fmaxf(g, 0.f);  // relu; a NaN stays one
-    }
+    if (act == BSP_ACT_RELU) return g != g ? g : fmaxf(g, 0.f);  // a NaN stays one
+    if (act == BSP_ACT_GELU) return 0.5f * g * erfcf(-0.70710678118654752f * g);
+    // silu: g / (1 + exp(-y)) with y = g; gelu_tanh: the same with its own y,
+    // 0.5 (1 + tanh(y / 2)) being 1 / (1 + exp(-y)).  From exp(-|y|): exp(-y) itself
+    // would be infinite from y = -88.7 on, where the quotient is still far from 0 in bf16.
+    const float y = act == BSP_ACT_SILU ? g : 1.59576912160573071f * (g + 0.044715f * g * g * g);
+    const float e = __expf(-fabsf(y));
+    return (y < 0.f ? g * e : g) / (1.f + e);
 }
 
 __device__ __forceinline__ void wait_prior_grids() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
