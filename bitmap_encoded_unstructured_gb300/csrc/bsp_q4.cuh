@@ -154,9 +154,11 @@ __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontr
 
 }  // namespace bspq4
 
-// Few rows of X (q4_narrow.cuh), and more (q4_wide.cuh), by type.  With 32
-// rows the narrow kernel takes 57 us for 28672 x 8192 and 36 for 20480 x 5120
-// where the wide one takes 79 and 46; with 33 it would read the codes twice.
+// Few rows of X (q4_narrow.cuh), and more (q4_wide.cuh), by type.  The narrow
+// kernel takes 53.6 us for 32 rows of 28672 x 8192, 33.2 of 20480 x 5120, 16.3 of
+// 11008 x 4096, 11.2 of 4096 x 4096 and 7.0 of 1024 x 4096, the wide one for 33
+// rows 68.0, 40.0, 18.6, 9.8 and 6.5: it is ahead but for small weights.  With 33 the narrow
+// one would read the codes twice.
 constexpr int64_t BSP_Q4_NARROW_N = 32;
 bsp_status_t bsp_run_q4_narrow_f16(const bspq4::Problem& p, cudaStream_t s);
 bsp_status_t bsp_run_q4_narrow_bf16(const bspq4::Problem& p, cudaStream_t s);

@@ -19,11 +19,16 @@
 // further where the row tiles alone do not fill the GPU; all parts are added in
 // a fixed order.
 //
-// Bound by the logic pipe and the latency of four warps a scheduler (55% of
-// issue slots, 56% of the logic pipe): one row of 28672 x 8192 takes 28.2 us
-// (4.3 TB/s, 0.63 of a copy), 16 rows 32.4, 32 rows 54; the same loads without
-// the arithmetic run at 0.9 of a copy.  Short calls are latency: one row
-// of 5120 x 5120 takes 7.6 us, of which the codes' bytes are 2.0.
+// Nothing is saturated (DRAM 44%, issue slots 55%, logic pipe 56% with one row of 28672 x
+// 8192; the same loads without the arithmetic run at 0.9 of a copy): a warp
+// waits for its own chain of copy, widening and product, three or four
+// CTAs of four warps an SM, and CTAs come in whole waves of 608 (32 rows of W
+// a CTA; gated 16) or 456 (9 to 16 rows of X: 64 rows of W).  8192 columns, one row: 19456 rows of W (one wave)
+// 18.5 us (0.66 of a copy), 28672 (1.47 waves) 27.0 (0.66), 38912 (two) 34.4
+// (0.70).  Gated, 4096 columns: 9728 rows (one wave) 11.5 us, 11008 (1.13) 15.2.
+// 16 rows, 5120 columns: 20480 rows of W (320 CTAs) 21.2 us, 29184 (456) 22.4.
+// 17 to 32 rows: 8192 columns and 29184 rows of W 53.9 us with 32.  Short calls are latency:
+// one row of 5120 x 5120 takes 7.2 us, of which the codes' bytes are 2.0.
 #pragma once
 
 #include "bsp_q4.cuh"
@@ -171,7 +176,8 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         step[i] = 8 * i + g < n_here ? 256 : 0;
-        x[i] = step[i] ? reinterpret_cast<const char*>(a.x) + ((int64_t)(n0 + 8 * i + g) * a.x_stride + (int64_t)first * 128 + 8 * t) * 2
+        const int64_t at = (int64_t)(n0 + 8 * i + g) * a.x_stride + (int64_t)first * 128 + 8 * t;
+        x[i] = step[i] ? reinterpret_cast<const char*>(a.x) + at * 2
                        : reinterpret_cast<const char*>(kNothing) + t * 16;
     }
     const int whole = (int)(a.K / 128) - first;       // blocks from here on that lie inside K
@@ -247,7 +253,8 @@ __global__ void __launch_bounds__(THREADS, Ring<G, RT, NT>::CTAS) q4_narrow_kern
                 const uint32_t pair = lds4(slot + R::S + (p * RT + r) * 32 + g * 4);
                 s0[r] = half_of<T>(pair, 0);
                 s1[r] = half_of<T>(pair, 1);
-                Codes<T>::bias(ZEROS && has_zeros[GATED && r >= TILES] ? lds1(slot + R::Z + (p * RT + r) * 8 + g) : 0x88u, z0[r], z1[r]);
+                const bool own = ZEROS && has_zeros[GATED && r >= TILES];
+                Codes<T>::bias(own ? lds1(slot + R::Z + (p * RT + r) * 8 + g) : 0x88u, z0[r], z1[r]);
             }
         };
         auto flush = [&]() {  // the group's sums, scaled, into out

@@ -12,24 +12,30 @@
 //   D  sums of one group of columns, in tensor memory, two to eight buffers; one
 //      product (cta_group::2) works on both CTAs' rows
 // Scales are applied to D: the promoting warps read a group's sums while
-// the next group's products run, and add s D to fp32 sums in registers.  So no weight is rounded, whatever its scale; weights
-// multiplied out and rounded to the type would leave an error of 1.3 times
-// the output's own rounding (the gated form 1.55 times).
+// the next group's products run, and add s D to fp32 sums in registers.  So no
+// weight is rounded, whatever its scale; weights multiplied out and rounded to
+// the type would leave an error of 1.3 times the output's own rounding (the
+// gated form 1.55 times).
 //
 // Warps of a CTA: 0 loads X and 2 says when it is there, 1 issues the products
-// (in the pair's first CTA), 3 loads codes and scales, DW widen, PW promote (a warp reaches the tensor-memory lanes 32 (w % 4) .. + 31, so
-// a thread has one row).  The issuing warp sets the pace, not the tensor
-// pipe: a wait costs it about 150 cycles though it is over, a product 75.  So
-// a block has one barrier for all that its products read, from both CTAs.
+// (in the pair's first CTA), 3 loads codes and scales, DW widen, PW promote (a
+// warp reaches the tensor-memory lanes 32 (w % 4) .. + 31, so a thread has one
+// row).  The issuing warp sets the pace, not the tensor pipe: a wait costs it
+// about 150 cycles though it is over, a product 75.  So a block has one
+// barrier for all that its products read, from both CTAs.
 // Where few tiles leave SMs idle, the pairs of a larger cluster share a
 // tile's columns and add their parts in order through shared memory.
 //
-// With groups of 128 a block of 256 columns of Y takes 690 ns where its products
-// alone take 540 (tensor pipe 66% busy); groups of 64 and 32 are bound by the
-// promoting warps, 870 and 1400 ns (two and four passes over the sums a
-// block), tiles of 128 columns and fewer by their chain of waits, 480 to 620.
-// 1501 rows of 8192 x 28672: 484 us (1457 TFLOP/s, 0.77 of the library's bf16
-// product); gated 2048 rows of 28672 x 8192: 1460 us (1318 TFLOP/s).
+// What a block takes, and a tile at its ends (one wave, one pair a tile):
+//   columns of Y    groups of 128    64         32          ends
+//   64              480 ns           510        600         5 us
+//   128             550              650        910         7
+//   256             670              860        1370        9.5
+// Large tiles of groups of 128 are bound by their products (540 of 670 ns;
+// tensor pipe 66% busy), of 64 and 32 by the promoting warps (two and four
+// passes over the sums a block), small tiles by a block's chain of waits.
+// 1501 rows of 8192 x 28672: 490 us (1438 TFLOP/s, 0.76 of the library's bf16
+// product); gated 2048 rows of 28672 x 8192: 1450 us (1327 TFLOP/s).
 #pragma once
 
 #include "bsp_q4.cuh"
@@ -187,7 +193,10 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ uint4 lds16(uint32_t at)
 {
     uint4 v;
-    asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    asm volatile("ld.volatile.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t lds2(uint32_t at)
@@ -228,7 +237,8 @@ __global__ void __launch_bounds__(Wide<G, BN, GATED>::THREADS, 1)
 q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ WideArgs a)
 {
     using C = Wide<G, BN, GATED>;
-    static_assert(4 * C::R_CONTROL + C::DW * C::R_WIDEN + C::PW * C::R_PROMOTE <= C::WARPS * C::REGS, "shares of the launch's registers");
+    static_assert(4 * C::R_CONTROL + C::DW * C::R_WIDEN + C::PW * C::R_PROMOTE <= C::WARPS * C::REGS,
+                  "shares of the launch's registers");
     constexpr int SR = C::SR, SC = C::SC, SS = C::SS, ND = C::ND, PER = C::PER, H = C::H;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (bspx::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -307,7 +317,8 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
         tmem = *tmem_slot;
         // one product addresses both CTAs' tensor memory: they were given the same
         uint32_t other;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(bspx::mapa_shared(bspx::smem_u32(tmem_slot), rank ^ 1u)) : "memory");
+        const uint32_t at = bspx::mapa_shared(bspx::smem_u32(tmem_slot), rank ^ 1u);
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(at) : "memory");
         failed = other != tmem;
         if (failed) blocks = 0;
     };
@@ -433,7 +444,8 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                     bspx::bulk_g2s(to, w.codes + (block0 + u) * 512, 8192, c_full + sc);
                     if (w.zeros) bspx::bulk_g2s(to + 8192, w.zeros + (block0 + u) * C::Z_BYTES, C::Z_BYTES, c_full + sc);
                     bspx::mbar_arrive_expect_tx(s_full + ss, C::S_BYTES);
-                    bspx::bulk_g2s(smem + C::OFF_S + ss * C::S_BYTES, w.scales + (block0 + u) * (C::S_BYTES / 4), C::S_BYTES, s_full + ss);
+                    bspx::bulk_g2s(smem + C::OFF_S + ss * C::S_BYTES, w.scales + (block0 + u) * (C::S_BYTES / 4), C::S_BYTES,
+                                   s_full + ss);
                 }
                 __syncwarp();
                 if (++sc == SC) { sc = 0; pc ^= 1u; }
@@ -499,7 +511,8 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t z0, z1, p[4], q[4];
-                        Codes<T>::bias(ZN == 4 ? ((odd ? !h : h) ? z[x][(2 * e + 1) % ZN] : z[x][2 * e % ZN]) : z[x][e % ZN], z0, z1);
+                        Codes<T>::bias(ZN == 4 ? ((odd ? !h : h) ? z[x][(2 * e + 1) % ZN] : z[x][2 * e % ZN]) : z[x][e % ZN],
+                                       z0, z1);
                         Codes<T>::widen(c[h][0], z0, z1, p);
                         Codes<T>::widen(c[h][1], z0, z1, q);
                         const uint32_t o = at ^ (h << 6);  // the other half: chunk ^ 4
@@ -608,7 +621,8 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
             const float* up = own + (half ? 0 : BN / 2 * BM);
             if (!failed && m < a.M)
 #pragma unroll 4
-                for (int i = 0; i < last; ++i) y[(n1 + i) * a.y_stride] = from_float<T>(activate(gate[i * BM] * OUT, a.act) * (up[i * BM] * OUT));
+                for (int i = 0; i < last; ++i)
+                    y[(n1 + i) * a.y_stride] = from_float<T>(activate(gate[i * BM] * OUT, a.act) * (up[i * BM] * OUT));
             bspx::cluster_sync();
         } else {
             // ---------------- parts to shared memory, [column][row], and their sums
@@ -657,8 +671,9 @@ q4_wide_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant_
                     const int n = c + j * C::PW;
                     if (n >= to_col) break;
                     float4 z = v[0];
-                    if (GATED) z = make_float4(activate(z.x, a.act) * u[0].x, activate(z.y, a.act) * u[0].y, activate(z.z, a.act) * u[0].z,
-                                               activate(z.w, a.act) * u[0].w);
+                    if (GATED)
+                        z = make_float4(activate(z.x, a.act) * u[0].x, activate(z.y, a.act) * u[0].y,
+                                        activate(z.z, a.act) * u[0].z, activate(z.w, a.act) * u[0].w);
                     T* y = reinterpret_cast<T*>(a.y) + (n0 + n) * a.y_stride + m0;
                     alignas(8) const T o[4] = {from_float<T>(z.x), from_float<T>(z.y), from_float<T>(z.z), from_float<T>(z.w)};
                     if (whole) *reinterpret_cast<uint2*>(y) = *reinterpret_cast<const uint2*>(o);
@@ -789,7 +804,8 @@ template <int G>
 Plan plan_of(const Problem& p, const int* clusters)
 {
     constexpr int BN[3] = {64, 128, 256};
-    constexpr int BLOCK[3] = {G == 32 ? 60 : 48, G == 32 ? 92 : 55, G == 128 ? 67 : G == 64 ? 86 : 137}, ENDS[3] = {600, 790, 1060};
+    constexpr int BLOCK[3] = {G == 32 ? 60 : 48, G == 32 ? 92 : 55, G == 128 ? 67 : G == 64 ? 86 : 137};
+    constexpr int ENDS[3] = {600, 790, 1060};
     const int64_t pairs = p.gated ? p.strips : (p.strips + 1) / 2, blocks = p.k_tiles / 2;
     Plan best = {256, 1};
     int64_t least = INT64_MAX;

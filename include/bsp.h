@@ -72,7 +72,8 @@ typedef enum {
 typedef enum {
     BSP_FP16 = 0, /* IEEE binary16 values, fp32 accumulation, fp16 output */
     BSP_INT8 = 1, /* int8 values, int32 accumulation (exact)             */
-    BSP_BF16 = 2  /* bfloat16: rows and queries of the KV cache only     */
+    BSP_BF16 = 2  /* bfloat16: the KV cache's rows and queries, 4-bit
+                     weights' scales and activations, rotary rows        */
 } bsp_dtype_t;
 
 /* Largest N of the decode path (the skinny product, N <= 16): split-K
