@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
-@pytest.mark.parametrize("N", [1, 7, 16, 30, 90])
+@pytest.mark.parametrize("N", [1, 7, 16, 30, 90, 600])
 @pytest.mark.parametrize("size", [256, 2048, 5120])
 def test_through_one_pair_of_buffers(size, N, dtype):
     import torch
